@@ -313,6 +313,173 @@ kvring_status kvring_attention(kvring_t* ring, const void* q_bf16, const int32_t
 kvring_status kvring_attention_noalloc(kvring_t* ring, const void* q_bf16, const int32_t* qpos,
                                        int32_t n_q, void* out, int32_t out_dtype, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A paged cache for many requests (sessions of different lengths on one
+ * GPU), beside the ring: kvring_pages_t holds, for every layer of a model,
+ * a pool of pages, each page holding `page_size` tokens' keys and values
+ * of all key/value heads, and one set of block tables that all layers
+ * share.  A step is
+ *   kvring_pages_plan        where the step's new tokens go
+ *   for every layer:
+ *     kvring_pages_write     head norms, RoPE, keys and values into the pages
+ *     kvring_pages_attention the new tokens' queries over their requests
+ *   kvring_pages_commit      the new lengths and the taken pages become final
+ * and nothing in it needs the host: lengths, tables, the free list and the
+ * plan live in device memory, so a captured step replays with whatever
+ * lengths the device then holds.  The conventions at the top of this file
+ * hold (alignment, streams, checks, device); calls on one kvring_pages_t
+ * must be ordered (one stream, or the caller's events), captured graphs
+ * that use one included, since its plan and workspace are shared by them.
+ *
+ * Requests live in rows 0 .. max_requests - 1 of the block tables.  A row
+ * is free when its length is 0.  Pages are taken from a stack of free page
+ * ids, the last id first, in the order of the plan's requests and of their
+ * pages; kvring_pages_release puts a request's pages back, first page first.
+ * ------------------------------------------------------------------------ */
+typedef struct kvring_pages kvring_pages_t;
+
+#define KVRING_CACHE_E4M3 0
+#define KVRING_CACHE_BF16 1
+#define KVRING_ROPE_ADJACENT 0   /* pairs (x[2i], x[2i+1]), as the ring's */
+#define KVRING_ROPE_HALVES 1     /* pairs (x[i], x[i + d/2]) */
+
+typedef struct {
+  int32_t num_q_heads;   /* Hq, a multiple of num_kv_heads */
+  int32_t num_kv_heads;  /* Hkv; query head h reads key/value head h / (Hq / Hkv).  Hq / Hkv <= 64 */
+  int32_t head_dim;      /* d: 64 or 128 */
+  int32_t num_layers;    /* 1 .. 1024 */
+  int32_t page_size;     /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t num_pages;     /* pages per layer; num_pages * Hkv * page_size < 2^31 */
+  int32_t max_requests;  /* rows of the block tables, 1 .. 4096 */
+  int32_t max_pages_per_request;  /* W, entries per row; W * page_size <= 2^24 */
+  int32_t max_tokens;    /* most new tokens of one step, 1 .. 2^20 */
+  int32_t cache_dtype;   /* KVRING_CACHE_* */
+  int32_t rope_pairing;  /* KVRING_ROPE_* */
+  int32_t reserved;      /* 0 */
+  double rope_base;
+} kvring_pages_config;
+
+/* Where things lie in the buffer given to kvring_pages_create (byte
+ * offsets), for a caller's own kernels, snapshots and tests. */
+typedef struct {
+  size_t k_cache;      /* [L][num_pages][Hkv][page_size][d] cache_dtype */
+  size_t v_cache;      /* the same */
+  size_t scales;       /* float [L][4][Hkv]: scale_k, scale_v, 1/scale_k, 1/scale_v (1 at create) */
+  size_t lengths;      /* int32 [max_requests]: committed lengths */
+  size_t tables;       /* int32 [max_requests][W]: page ids, -1 where never set */
+  size_t free_pages;   /* int32 [num_pages]: the stack of free page ids */
+  size_t state;        /* int32 [KVRING_PAGES_STATE_WORDS] */
+  size_t step_rows;    /* int32 [max_requests]: the planned requests' rows */
+  size_t step_cu;      /* int32 [max_requests + 1]: first new token of each planned request */
+  size_t step_lengths; /* int32 [max_requests]: their lengths with the new tokens */
+  size_t positions;    /* int32 [max_tokens]: position of each new token in its request */
+  size_t slots;        /* int32 [max_tokens]: page * page_size + offset, -1 for padding */
+  size_t total;        /* bytes of the whole buffer */
+} kvring_pages_layout;
+
+#define KVRING_PAGES_STATE_FREE 0       /* free pages */
+#define KVRING_PAGES_STATE_ERROR 1      /* KVRING_PAGES_ERR_* bits, never cleared by the library */
+#define KVRING_PAGES_STATE_PLANNED 2    /* 1 while a plan awaits its commit */
+#define KVRING_PAGES_STATE_REQUESTS 3   /* requests of the last plan */
+#define KVRING_PAGES_STATE_TOKENS 4     /* its new tokens */
+#define KVRING_PAGES_STATE_TAKEN 5      /* pages it takes */
+#define KVRING_PAGES_STATE_WORDS 8
+
+#define KVRING_PAGES_ERR_ROW 1u      /* a row outside [0, max_requests), or twice in one call */
+#define KVRING_PAGES_ERR_TOKENS 2u   /* negative or more than max_new tokens, or more than num_tokens in all */
+#define KVRING_PAGES_ERR_LENGTH 4u   /* a request longer than W pages */
+#define KVRING_PAGES_ERR_PAGES 8u    /* not enough free pages */
+#define KVRING_PAGES_ERR_COMMIT 16u  /* a commit with no plan before it */
+#define KVRING_PAGES_ERR_TABLE 32u   /* a page id outside [0, num_pages) in a table or the free list */
+#define KVRING_PAGES_ERR_TIMEOUT 64u /* a wait in the attention kernel gave up */
+
+/* The layout for a config; INVALID_ARG if the config is invalid (*out is
+ * then zeroed).  layout.total is what kvring_pages_create needs. */
+kvring_status kvring_pages_get_layout(const kvring_pages_config* cfg, kvring_pages_layout* out);
+
+/* Create a paged cache inside `dev_buf` (device memory of at least
+ * layout.total bytes, 256-byte aligned, the caller's until after
+ * kvring_pages_destroy).  Every row is empty, every page free (the stack
+ * holds num_pages - 1 .. 0, so page 0 is taken first), scales are 1; cached
+ * keys and values are not cleared.  Waits for its own set-up on `stream`. */
+kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf, size_t bytes, void* stream,
+                                  kvring_pages_t** out);
+kvring_status kvring_pages_destroy(kvring_pages_t* pages);
+
+/* Take over a state: lengths int32 [max_requests], tables int32
+ * [max_requests][W], free_pages int32 [n_free] (the stack, bottom first).
+ * Device pointers.  Drops a plan that awaits its commit. */
+kvring_status kvring_pages_restore(kvring_pages_t* pages, const int32_t* lengths, const int32_t* tables,
+                                   const int32_t* free_pages, int32_t n_free, void* stream);
+
+/* Per-head scales of one layer of an E4M3 cache (device, float [Hkv] each):
+ * a cached value is code * scale.  Must be positive and finite. */
+kvring_status kvring_pages_set_scales(kvring_pages_t* pages, int32_t layer, const float* scale_k,
+                                      const float* scale_v, void* stream);
+
+/* Plan a step: request i (of num_requests) is row rows[i] of the tables
+ * (rows NULL: row i) and gets new_tokens[i] >= 0 new tokens, positions
+ * len .. len + new - 1.  Both are device int32 arrays.  On the device:
+ *   step_cu       exclusive sums of new_tokens (num_requests + 1 entries)
+ *   step_lengths  length + new
+ *   tables        entries of the pages the new tokens need beyond those the
+ *                 request has, taken from the free stack
+ *   positions, slots  for tokens 0 .. num_tokens - 1; those past the last
+ *                 request's get slot -1, position 0
+ * num_tokens (<= max_tokens) is the token count of the step's tensors, at
+ * least the sum of new_tokens; max_new bounds every new_tokens[i] and lets
+ * kvring_pages_attention pick its kernels (num_tokens if unknown).
+ * Lengths and the free list change only with kvring_pages_commit: a plan
+ * that is not committed is dropped by the next one and costs nothing.
+ * A plan that cannot be made (rows, tokens, length or pages: see the error
+ * bits) sets its error bit and plans no token for any request. */
+kvring_status kvring_pages_plan(kvring_pages_t* pages, const int32_t* rows, const int32_t* new_tokens,
+                                int32_t num_requests, int32_t num_tokens, int32_t max_new, void* stream);
+
+/* Make the last plan final: row lengths and the free list. */
+kvring_status kvring_pages_commit(kvring_pages_t* pages, void* stream);
+
+/* End num_requests requests: their pages go back to the free stack (in the
+ * order of `rows` (device int32), each request's first page first) and
+ * their lengths to 0.  Rows that are already empty are allowed; a row out
+ * of range or given twice sets KVRING_PAGES_ERR_ROW and nothing is
+ * released.  Drops a plan that awaits its commit, and empties the step. */
+kvring_status kvring_pages_release(kvring_pages_t* pages, const int32_t* rows, int32_t num_requests, void* stream);
+
+/* Keys, values and queries of the planned tokens, for one layer:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   per head row (q_weight,
+ *       k_weight: bf16 [d]; NULL leaves q or k as it is)
+ *   q_out[t] = rope(y_q, positions[t]), bf16 [num_tokens][Hq][d] contiguous
+ *   K page   = rope(y_k, positions[t]), V page = v
+ * at slots[t].  An E4M3 cache stores e4m3(value * (1/scale)).  Everything
+ * between reading bf16 and the one rounding of the result is fp32.
+ * q, k, v: bf16, row (t, h) at base + t * token_stride + h * d (elements;
+ * strides a multiple of 8, at least that of heads * d), so slices of one
+ * packed projection output can be passed.  q_out must not overlap them.
+ * Tokens past the plan's are not read, and their rows of q_out stay as
+ * they were.  num_tokens is that of the tensors (<= max_tokens). */
+kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const void* q, const void* k, const void* v,
+                                 int64_t q_stride, int64_t k_stride, int64_t v_stride, const void* q_weight,
+                                 const void* k_weight, float eps, void* q_out, int32_t num_tokens, void* stream);
+
+/* Attention of the planned tokens' queries over their requests' cached
+ * tokens, the new ones included:
+ *   out[t,h] = sum_j softmax_j(scale * q[t,h] . K[j,h/G]) V[j,h/G]
+ * causal != 0: j <= position of t, and with window > 0 also
+ * j > position - window; causal == 0: every cached and new token of the
+ * request (window must be 0).  scale 0 means 1/sqrt(d).  q (rotated) and
+ * out: bf16 [num_tokens][Hq][d], q with a token stride (elements, a multiple
+ * of 8), out contiguous and not overlapping q; rows past the plan's tokens stay as
+ * they were.  Scores, softmax statistics and sums are fp32; probabilities
+ * are rounded once, to bf16 (f16 over an E4M3 cache).  Cached tokens that
+ * a query's mask hides do not affect it, whatever they hold. */
+kvring_status kvring_pages_attention(kvring_pages_t* pages, int32_t layer, const void* q, int64_t q_stride, void* out,
+                                     int32_t num_tokens, int32_t causal, int32_t window, float scale, void* stream);
+
+/* Test support for the chunk kernel's bounded waits: as
+ * kvring_debug_set_attention_wait (limit_ns in [1000, 6e10], stall 0 or 1). */
+kvring_status kvring_pages_debug_set_wait(kvring_pages_t* pages, int64_t limit_ns, int32_t stall);
+
 /* Copy the ring out for inspection (tests, snapshots).  Any pointer may be
  * NULL to skip that part.  k_out, v_out: uint8 [H][capacity][d] codes;
  * scales: float [4H] = scale_k, scale_v, inv_scale_k, inv_scale_v;

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from collections import namedtuple
 
 import torch
 
@@ -26,6 +27,9 @@ __all__ = [
     "kvring_legacy_upkeep", "LegacyWindows", "kvring_project_write",
     "kvring_export",
     "kvring_status_string", "encode_e4m3", "STATE",
+    "KvPages", "KvStep", "PAGES_STATE", "kvring_pages_get_layout", "kvring_pages_create", "kvring_pages_destroy",
+    "kvring_pages_restore", "kvring_pages_set_scales", "kvring_pages_plan", "kvring_pages_commit",
+    "kvring_pages_release", "kvring_pages_write", "kvring_pages_attention",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -55,6 +59,27 @@ class KvringConfig(ctypes.Structure):
         ("rope_pairs_y", ctypes.c_int32),
         ("rope_base", ctypes.c_double),
     ]
+
+
+CACHE_E4M3, CACHE_BF16 = 0, 1
+ROPE_ADJACENT, ROPE_HALVES = 0, 1
+PAGES_STATE = dict(free=0, error=1, planned=2, requests=3, tokens=4, taken=5)
+PAGES_STATE_WORDS = 8
+PAGES_ERR_ROW, PAGES_ERR_TOKENS, PAGES_ERR_LENGTH, PAGES_ERR_PAGES = 1, 2, 4, 8
+PAGES_ERR_COMMIT, PAGES_ERR_TABLE, PAGES_ERR_TIMEOUT = 16, 32, 64
+
+
+class KvringPagesConfig(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in (
+        "num_q_heads", "num_kv_heads", "head_dim", "num_layers", "page_size", "num_pages", "max_requests",
+        "max_pages_per_request", "max_tokens", "cache_dtype", "rope_pairing", "reserved")] + [
+        ("rope_base", ctypes.c_double)]
+
+
+class KvringPagesLayout(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_size_t) for f in (
+        "k_cache", "v_cache", "scales", "lengths", "tables", "free_pages", "state", "step_rows", "step_cu",
+        "step_lengths", "positions", "slots", "total")]
 
 
 class KvRingError(RuntimeError):
@@ -95,6 +120,17 @@ def lib():
         "kvring_attention_noalloc": (i32, [vp, vp, vp, i32, vp, i32, vp]),
         "kvring_project_write": (i32, [vp, vp, vp, i32, vp, i32, vp, vp, i32, vp]),
         "kvring_export": (i32, [vp, vp, vp, vp, vp, vp, vp]),
+        "kvring_pages_get_layout": (i32, [ctypes.POINTER(KvringPagesConfig), ctypes.POINTER(KvringPagesLayout)]),
+        "kvring_pages_create": (i32, [ctypes.POINTER(KvringPagesConfig), vp, sz, vp, ctypes.POINTER(vp)]),
+        "kvring_pages_destroy": (i32, [vp]),
+        "kvring_pages_restore": (i32, [vp, vp, vp, vp, i32, vp]),
+        "kvring_pages_set_scales": (i32, [vp, i32, vp, vp, vp]),
+        "kvring_pages_plan": (i32, [vp, vp, vp, i32, i32, i32, vp]),
+        "kvring_pages_commit": (i32, [vp, vp]),
+        "kvring_pages_release": (i32, [vp, vp, i32, vp]),
+        "kvring_pages_write": (i32, [vp, i32, vp, vp, vp, i64, i64, i64, vp, vp, ctypes.c_float, vp, i32, vp]),
+        "kvring_pages_attention": (i32, [vp, i32, vp, i64, vp, i32, i32, i32, ctypes.c_float, vp]),
+        "kvring_pages_debug_set_wait": (i32, [vp, i64, i32]),
         "kvring_debug_encode_e4m3": (i32, [vp, vp, i64, vp]),
         "kvring_debug_attention_levels": (i32, [vp, vp, vp]),
         "kvring_debug_set_attention_wait": (i32, [vp, i64, i32]),
@@ -464,6 +500,279 @@ class KvRing:
     def close(self) -> None:
         if getattr(self, "handle", None):
             kvring_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------------------
+# The paged cache
+# ---------------------------------------------------------------------------
+def make_pages_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_requests, max_pages_per_request,
+                      max_tokens, layers=1, cache_dtype=CACHE_E4M3, rope_pairing=ROPE_ADJACENT,
+                      rope_base=10000.0) -> KvringPagesConfig:
+    return KvringPagesConfig(int(q_heads), int(kv_heads), int(head_dim), int(layers), int(page_size), int(num_pages),
+                             int(max_requests), int(max_pages_per_request), int(max_tokens), int(cache_dtype),
+                             int(rope_pairing), 0, float(rope_base))
+
+
+def kvring_pages_get_layout(cfg: KvringPagesConfig) -> KvringPagesLayout:
+    lay = KvringPagesLayout()
+    _check(lib().kvring_pages_get_layout(ctypes.byref(cfg), ctypes.byref(lay)), "kvring_pages_get_layout")
+    return lay
+
+
+def kvring_pages_create(cfg: KvringPagesConfig, buf: torch.Tensor, stream=None) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().kvring_pages_create(ctypes.byref(cfg), buf.data_ptr(), buf.numel() * buf.element_size(),
+                                     _stream_ptr(stream, buf.device), ctypes.byref(h)), "kvring_pages_create")
+    return h.value
+
+
+def kvring_pages_destroy(handle: int) -> None:
+    _check(lib().kvring_pages_destroy(handle), "kvring_pages_destroy")
+
+
+def kvring_pages_restore(handle, lengths, tables, free_pages, n_free, stream_ptr) -> None:
+    _check(lib().kvring_pages_restore(handle, _ptr(lengths), _ptr(tables), _ptr(free_pages), int(n_free), stream_ptr),
+           "kvring_pages_restore")
+
+
+def kvring_pages_set_scales(handle, layer, scale_k, scale_v, stream_ptr) -> None:
+    _check(lib().kvring_pages_set_scales(handle, int(layer), _ptr(scale_k), _ptr(scale_v), stream_ptr),
+           "kvring_pages_set_scales")
+
+
+def kvring_pages_plan(handle, rows, new_tokens, num_requests, num_tokens, max_new, stream_ptr) -> None:
+    _check(lib().kvring_pages_plan(handle, _ptr(rows), _ptr(new_tokens), int(num_requests), int(num_tokens),
+                                   int(max_new), stream_ptr), "kvring_pages_plan")
+
+
+def kvring_pages_commit(handle, stream_ptr) -> None:
+    _check(lib().kvring_pages_commit(handle, stream_ptr), "kvring_pages_commit")
+
+
+def kvring_pages_release(handle, rows, num_requests, stream_ptr) -> None:
+    _check(lib().kvring_pages_release(handle, _ptr(rows), int(num_requests), stream_ptr), "kvring_pages_release")
+
+
+def kvring_pages_write(handle, layer, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, q_out,
+                       num_tokens, stream_ptr) -> None:
+    _check(lib().kvring_pages_write(handle, int(layer), _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride,
+                                    _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(q_out), int(num_tokens),
+                                    stream_ptr), "kvring_pages_write")
+
+
+def kvring_pages_attention(handle, layer, q, q_stride, out, num_tokens, causal, window, scale, stream_ptr) -> None:
+    _check(lib().kvring_pages_attention(handle, int(layer), _ptr(q), q_stride, _ptr(out), int(num_tokens),
+                                        int(bool(causal)), int(window), float(scale), stream_ptr),
+           "kvring_pages_attention")
+
+
+# What a plan made, as views of the cache's own buffer (valid until the next
+# plan): cu [requests + 1], lengths [requests] with the new tokens, positions
+# and slots [num_tokens] (slot -1: padding).
+KvStep = namedtuple("KvStep", "cu lengths positions slots")
+
+
+class KvPages:
+    """A paged cache of every layer of a model for many requests, on one CUDA
+    device (the current one unless ``device`` names another).
+
+    A step: ``plan`` the new tokens of its requests, then for every layer
+    ``write`` and ``attention``, then ``commit``; ``release`` ends requests.
+    All of it runs on the device and can be captured in a CUDA graph.  Calls
+    on one object must be ordered (one stream, or events); graphs that use
+    one share its plan and workspace.  Every call runs with the object's
+    device current and takes tensors on it.  Its buffer is freed with the
+    object: keep it alive until the work enqueued on it has completed.
+    """
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, num_pages: int, max_requests: int,
+                 max_request_tokens: int, max_tokens: int, layers: int = 1, cache_dtype=torch.float8_e4m3fn,
+                 rope_pairing: str = "adjacent", rope_base: float = 10000.0, device=None, stream=None):
+        if not torch.cuda.is_available():
+            raise RuntimeError("KvPages needs a CUDA device")
+        d = torch.device(device) if device is not None else torch.device("cuda")
+        if d.type != "cuda":
+            raise ValueError("KvPages needs a CUDA device")
+        if cache_dtype not in (torch.float8_e4m3fn, torch.bfloat16):
+            raise ValueError("cache_dtype must be float8_e4m3fn or bfloat16")
+        if rope_pairing not in ("adjacent", "halves"):
+            raise ValueError("rope_pairing must be 'adjacent' or 'halves'")
+        self.device = d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
+        self.Hq, self.Hkv, self.d, self.P = int(q_heads), int(kv_heads), int(head_dim), int(page_size)
+        self.L, self.num_pages, self.R = int(layers), int(num_pages), int(max_requests)
+        self.W = -(-int(max_request_tokens) // max(1, self.P))
+        self.max_tokens, self.cache_dtype = int(max_tokens), cache_dtype
+        self.cfg = make_pages_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_requests, self.W,
+                                     max_tokens, layers, CACHE_E4M3 if cache_dtype == torch.float8_e4m3fn
+                                     else CACHE_BF16, ROPE_HALVES if rope_pairing == "halves" else ROPE_ADJACENT,
+                                     rope_base)
+        try:
+            self.layout = kvring_pages_get_layout(self.cfg)
+        except KvRingError:
+            raise ValueError("invalid paged-cache config") from None
+        self.nbytes = int(self.layout.total)
+        with torch.cuda.device(self.device):
+            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+            self.handle = kvring_pages_create(self.cfg, self.buf, stream)
+        lay = self.layout
+        self.lengths = self._ints(lay.lengths, self.R)
+        self.tables = self._ints(lay.tables, self.R * self.W).view(self.R, self.W)
+        self.free_pages = self._ints(lay.free_pages, self.num_pages)
+        self.state = self._ints(lay.state, PAGES_STATE_WORDS)
+        self._cu, self._klen = self._ints(lay.step_cu, self.R + 1), self._ints(lay.step_lengths, self.R)
+        self._pos, self._slots = self._ints(lay.positions, self.max_tokens), self._ints(lay.slots, self.max_tokens)
+        self._steps = {}
+
+    def _ints(self, off: int, n: int) -> torch.Tensor:
+        return self.buf[off:off + 4 * n].view(torch.int32)
+
+    def _s(self, stream) -> int:
+        return _stream_ptr(stream, self.device)
+
+    def _cache(self, off: int, layer: int) -> torch.Tensor:
+        if not 0 <= layer < self.L:
+            raise ValueError(f"layer must be in [0, {self.L})")
+        shape = (self.num_pages, self.Hkv, self.P, self.d)
+        n = self.num_pages * self.Hkv * self.P * self.d * self.cache_dtype.itemsize
+        return self.buf[off + layer * n:off + (layer + 1) * n].view(self.cache_dtype).view(shape)
+
+    def k_cache(self, layer: int = 0) -> torch.Tensor:
+        """The layer's keys [num_pages, Hkv, page_size, d], a view of the buffer."""
+        return self._cache(self.layout.k_cache, layer)
+
+    def v_cache(self, layer: int = 0) -> torch.Tensor:
+        """The layer's values [num_pages, Hkv, page_size, d], a view of the buffer."""
+        return self._cache(self.layout.v_cache, layer)
+
+    def _int_arg(self, x, name: str, shape=None):
+        if not isinstance(x, torch.Tensor) or x.device != self.device or x.dtype != torch.int32 \
+                or not x.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor on {self.device}")
+        if (shape is None and x.dim() != 1) or (shape is not None and tuple(x.shape) != shape):
+            raise ValueError(f"{name} must have shape {shape or '[n]'}, got {tuple(x.shape)}")
+        return x
+
+    def restore(self, lengths, tables, free_pages, stream=None) -> None:
+        """Take over a state: int32 lengths [max_requests], block tables
+        [max_requests, pages per request] and the stack of free pages [n]."""
+        self._int_arg(lengths, "lengths", (self.R,))
+        self._int_arg(tables, "tables", (self.R, self.W))
+        n = self._int_arg(free_pages, "free_pages").numel()
+        if n > self.num_pages:
+            raise ValueError(f"free_pages holds {n} pages, the cache {self.num_pages}")
+        with torch.cuda.device(self.device):
+            kvring_pages_restore(self.handle, lengths, tables, free_pages if n else None, n, self._s(stream))
+
+    def set_scales(self, layer: int, scale_k, scale_v, stream=None) -> None:
+        """Per-head scales (float32 [Hkv]) of one layer of an E4M3 cache."""
+        for t, name in ((scale_k, "scale_k"), (scale_v, "scale_v")):
+            if not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype != torch.float32 \
+                    or tuple(t.shape) != (self.Hkv,) or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 tensor [{self.Hkv}] on {self.device}")
+        with torch.cuda.device(self.device):
+            kvring_pages_set_scales(self.handle, layer, scale_k, scale_v, self._s(stream))
+
+    def plan(self, new_tokens, num_tokens: int, rows=None, max_new: int | None = None, stream=None) -> KvStep:
+        """Plan a step: request i (row ``rows[i]``, or row i) gets
+        ``new_tokens[i]`` tokens; ``num_tokens`` is the token count of the
+        step's tensors (at least the sum), ``max_new`` a bound on every
+        ``new_tokens[i]``.  Both index tensors are int32 on the device."""
+        n = self._int_arg(new_tokens, "new_tokens").numel()
+        if rows is not None:
+            self._int_arg(rows, "rows", (n,))
+        with torch.cuda.device(self.device):
+            kvring_pages_plan(self.handle, rows, new_tokens, n, num_tokens, num_tokens if max_new is None else max_new,
+                              self._s(stream))
+        step = self._steps.get((n, num_tokens))
+        if step is None:
+            if len(self._steps) >= 256:
+                self._steps.clear()
+            step = self._steps[(n, num_tokens)] = KvStep(self._cu[:n + 1], self._klen[:n], self._pos[:num_tokens],
+                                                         self._slots[:num_tokens])
+        return step
+
+    def commit(self, stream=None) -> None:
+        """Make the last plan final: the lengths and the free list."""
+        with torch.cuda.device(self.device):
+            kvring_pages_commit(self.handle, self._s(stream))
+
+    def release(self, rows, stream=None) -> None:
+        """End the requests in ``rows`` (int32): their pages become free."""
+        n = self._int_arg(rows, "rows").numel()
+        with torch.cuda.device(self.device):
+            kvring_pages_release(self.handle, rows, n, self._s(stream))
+
+    def _heads(self, x, heads: int, name: str) -> int:
+        """Check bf16 [n, heads, d] with whole rows of heads (a slice of a
+        packed projection output is one); returns n."""
+        if not isinstance(x, torch.Tensor) or x.device != self.device or x.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be a bfloat16 tensor on {self.device}")
+        if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != self.d:
+            raise ValueError(f"{name} must have shape [n, {heads}, {self.d}], got {tuple(x.shape)}")
+        if x.stride(2) != 1 or (heads > 1 and x.stride(1) != self.d) \
+                or (x.shape[0] > 1 and x.stride(0) < heads * self.d):
+            raise ValueError(f"{name}: the heads of a token must be contiguous, and tokens must not overlap")
+        return x.shape[0]
+
+    def _stride(self, x, heads: int) -> int:
+        return x.stride(0) if x.shape[0] > 1 else heads * self.d
+
+    def write(self, layer: int, q, k, v, q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None,
+              stream=None) -> torch.Tensor:
+        """Head norms (where weights bf16 [d] are given), RoPE and the write of
+        the planned tokens' keys and values; returns the rotated queries
+        (bf16 [n, Hq, d]).  Rows of ``q_out`` past the plan's tokens are left
+        as they were (undefined in a new tensor)."""
+        n = self._heads(q, self.Hq, "q")
+        if self._heads(k, self.Hkv, "k") != n or self._heads(v, self.Hkv, "v") != n:
+            raise ValueError("q, k and v must hold the same number of tokens")
+        for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if t is not None and (not isinstance(t, torch.Tensor) or t.device != self.device
+                                  or t.dtype != torch.bfloat16 or tuple(t.shape) != (self.d,)
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{self.d}] on {self.device}")
+        if q_out is None:
+            q_out = torch.empty((n, self.Hq, self.d), dtype=torch.bfloat16, device=self.device)
+        elif self._heads(q_out, self.Hq, "q_out") != n or not q_out.is_contiguous():
+            raise ValueError(f"q_out must be contiguous, [{n}, {self.Hq}, {self.d}]")
+        with torch.cuda.device(self.device):
+            kvring_pages_write(self.handle, layer, q, k, v, self._stride(q, self.Hq), self._stride(k, self.Hkv),
+                               self._stride(v, self.Hkv), q_norm, k_norm, eps, q_out, n, self._s(stream))
+        return q_out
+
+    def attention(self, layer: int, q, out=None, causal: bool = True, window: int = 0, scale: float = 0.0,
+                  stream=None) -> torch.Tensor:
+        """Attention of the planned tokens' queries (rotated, bf16 [n, Hq, d])
+        over their requests' cached tokens, the new ones included.  ``window``
+        limits a causal query to its last ``window`` tokens; ``scale`` 0 means
+        1/sqrt(d).  Rows of ``out`` past the plan's tokens are left as they
+        were (undefined in a new tensor)."""
+        n = self._heads(q, self.Hq, "q")
+        if out is None:
+            out = torch.empty((n, self.Hq, self.d), dtype=torch.bfloat16, device=self.device)
+        elif self._heads(out, self.Hq, "out") != n or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous, [{n}, {self.Hq}, {self.d}]")
+        with torch.cuda.device(self.device):
+            kvring_pages_attention(self.handle, layer, q, self._stride(q, self.Hq), out, n, causal, window, scale,
+                                   self._s(stream))
+        return out
+
+    def set_wait(self, limit_ns: int = 1_000_000_000, stall: bool = False) -> None:
+        """Test support: the attention kernels' wait limit, and a stall that
+        makes their first wait give up on purpose (see the C header)."""
+        _check(lib().kvring_pages_debug_set_wait(self.handle, int(limit_ns), int(bool(stall))),
+               "kvring_pages_debug_set_wait")
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            kvring_pages_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "kvring_internal.cuh"
+#include "kvring_pages.cuh"
 
 struct kvring {
   kvring_config cfg;
@@ -322,6 +323,15 @@ kvring_status passed_through(cudaStream_t s, F launch, kvring* const* rings, int
 }
 
 }  // namespace
+
+namespace kvr {
+kvring_status launch_recorded(cudaStream_t s, cudaError_t (*launch)(void*), void* ctx, const void* a, size_t a_bytes,
+                              const void* b, size_t b_bytes) {
+  std::lock_guard<std::mutex> lk(g_out_mu);
+  return tracked(s, [&] { return launch(ctx); }, Range{a, a_bytes}, Range{b, b_bytes});
+}
+EncodeTiledFn encode_tiled() { return get_encode_fn(); }
+}  // namespace kvr
 
 extern "C" {
 

@@ -1,0 +1,737 @@
+// Attention over the paged cache for requests with few query rows: single
+// tokens, drafts, short chunks (up to 64 rows a unit, a row being one query
+// head of one token).
+//
+//   out[r] = sum_j softmax_j(s_rj) V[j],  s_rj = scale q[r] . K[j]
+// by one pass over the keys with a running maximum m and sum l per row
+// (log2 units): m' = max(m, max_j s_rj), p = 2^(s - m'),
+// l' = l 2^(m - m') + sum p, O' = O 2^(m - m') + p V.
+//
+// Bound by HBM: every cached key and value of the request is read once per
+// key/value head (all its query heads share the tile), and with at most 64
+// rows the arithmetic is a small part of the tensor rate.  So the design is
+// about keeping copies in flight: one CTA per SM whose producer warp streams
+// page pieces by TMA into a ring of shared-memory slots (about 190 KB), and
+// about evenness: the (request, row tile, key/value head, 128-token tile)
+// space is flattened and cut into equal contiguous ranges, one per CTA, from
+// the lengths on the device, so ragged batches and a single long request
+// both load every SM alike.  A unit (request, row tile, head) that lies in
+// several ranges leaves partial (m, l, O) in the workspace; the last CTA to
+// arrive (one ticket per unit) merges the parts in range order, so results
+// do not depend on arrival.
+//
+// The matrix products use mma.sync (m16n8k16): with 16 rows a tile of
+// 128 tokens needs 32 instructions per warp, far from any limit, and a
+// register fragment lets the row tile be 16 high where tcgen05 has 64 or
+// 128 rows.  Eight warps: for the scores each takes 16 tokens, for the
+// values each takes 16 of the d columns (at d = 64 the warps' halves take
+// half the tokens each and are added at the end), with the probabilities
+// passed through shared memory.  Two barriers of the eight warps per tile.
+//
+// E4M3 tiles are read as 16-bit pairs by ldmatrix and widened in registers
+// to f16, exactly.  For the scores four consecutive bytes of a key become
+// the pair (k, k+1) and (k+8, k+9) of a k = 16 step, so the queries are
+// stored with that permutation of each 16 columns.  For the values the
+// transposed load gives two tokens x two columns; a byte permute makes the
+// token pairs, the even columns forming one n = 8 tile and the odd ones the
+// other.  Queries become f16 after scaling each row by a power of two into
+// [1, 2) at its largest value: bf16's 8 significant bits fit f16's 11, and
+// what the row's small values lose is below 2^-25 of its largest.
+#include "kvring_pages.cuh"
+
+namespace kvr {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kConsumers = kWarps * 32;
+constexpr int kFewThreads = kConsumers + 32;
+constexpr int kSmemMost = 232448;
+
+template <int D, bool E4M3, int MT>
+struct FewLayout {
+  static constexpr int UR = 16 * MT;                       // query rows of a unit
+  static constexpr int kSlot = kTile * D * (E4M3 ? 1 : 2); // one K or V tile
+  static constexpr int kQ = 0;                             // offsets behind the slots
+  static constexpr int kP = kQ + UR * D * 2;
+  static constexpr int kMax = kP + UR * kTile * 2;         // float [UR][8]
+  static constexpr int kSum = kMax + UR * 32;              // float [UR][8]
+  static constexpr int kRow = kSum + UR * 32;              // int lo, hi; float factor; pad: [UR][4]
+  static constexpr int kMisc = kRow + UR * 16;
+  static constexpr int kFixed = kMisc + 512;
+  static constexpr int kRoom = (kSmemMost - 1024 - kFixed) / kSlot;
+  static constexpr int kSlots = kRoom > 16 ? 16 : kRoom;
+  static constexpr int kBytes = 1024 + kSlots * kSlot + kFixed;
+  static_assert(kSlots >= 4, "two tiles in flight");
+};
+
+struct FewMisc {
+  uint64_t full[16];
+  uint64_t empty[16];
+  unsigned long long ws[9];
+  long long total;
+  long long base;    // tiles before the request the CTA starts in
+  int b0;
+  int parts;         // CTAs that have a range
+  int abort;
+  int last;
+};
+
+// Keeps the accumulator type of the two element types in one place.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// What a unit of a request needs to know.
+struct Req {
+  int q0, nq, klen;    // first token, tokens (that the tensors hold), length
+  int pos0;            // position of the first token
+  int nrows, nrt;      // query rows, row tiles
+  int lo, hi;          // tokens any row sees: [lo, hi)
+  int t0, nt;          // their tiles
+};
+
+template <int UR>
+__device__ __forceinline__ Req load_req(const PagesDev& p, const PagedAttn& a, int b, int G) {
+  Req r;
+  r.q0 = __ldcg(p.cu + b);
+  const int end = __ldcg(p.cu + b + 1);
+  r.klen = __ldcg(p.klen + b);
+  r.pos0 = r.klen - (end - r.q0);
+  r.nq = (end < a.T ? end : a.T) - r.q0;
+  if (r.nq < 0) r.nq = 0;
+  r.nrows = r.nq * G;
+  if (r.nrows <= a.min_rows || r.nrows > a.max_rows || r.klen <= 0) r.nrows = 0;
+  r.nrt = (r.nrows + UR - 1) / UR;
+  r.hi = r.klen;
+  r.lo = 0;
+  if (a.window > 0) {
+    const int lo = r.pos0 + 1 - a.window;
+    r.lo = lo > 0 ? lo : 0;
+  }
+  r.t0 = r.lo / kTile;
+  r.nt = r.nrows ? (r.hi + kTile - 1) / kTile - r.t0 : 0;
+  return r;
+}
+
+template <int D, bool E4M3, int MT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    k_paged_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagesDev p,
+                const PagedAttn a) {
+  using L = FewLayout<D, E4M3, MT>;
+  constexpr int UR = L::UR;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(sm);
+  uint8_t* fix = sm + L::kSlots * L::kSlot;
+  const uint32_t fbase = sbase + L::kSlots * L::kSlot;
+  FewMisc* misc = reinterpret_cast<FewMisc*>(fix + L::kMisc);
+  volatile int* abort = &misc->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
+  auto full = [&](int s) { return smem_u32(&misc->full[s]); };
+  auto empty = [&](int s) { return smem_u32(&misc->empty[s]); };
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), kWarps);
+    }
+    misc->abort = 0;
+    mbar_fence_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ------------------------------------------------- this CTA's range
+  const int B = __ldcg(p.state + PST_REQUESTS);
+  {
+    // tiles (of one head) of each thread's requests, then one block scan
+    const int per = (B + kFewThreads - 1) / kFewThreads;
+    const int i0 = threadIdx.x * per, i1 = i0 + per < B ? i0 + per : B;
+    unsigned long long mine = 0;
+    for (int i = i0; i < i1; ++i) {
+      const Req r = load_req<UR>(p, a, i, G);
+      mine += (unsigned long long)r.nrt * (unsigned)r.nt;
+    }
+    unsigned long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) misc->ws[warp] = x;
+    __syncthreads();
+    unsigned long long before = 0, total = 0;
+    for (int w = 0; w < kFewThreads / 32; ++w) {
+      if (w < warp) before += misc->ws[w];
+      total += misc->ws[w];
+    }
+    total *= (unsigned)p.Hkv;
+    before = (before + x - mine) * (unsigned)p.Hkv;
+    mine *= (unsigned)p.Hkv;
+    // as many ranges as there are CTAs, unless they would be shorter than
+    // min_tiles: below that a range's start-up and the merge cost more
+    unsigned long long parts = total / (unsigned)a.min_tiles;
+    parts = parts < 1 ? 1 : (parts > gridDim.x ? gridDim.x : parts);
+    const unsigned long long start = blockIdx.x < parts ? total * blockIdx.x / parts : total;
+    if (mine && start >= before && start < before + mine) {   // exactly one thread, unless total is 0
+      int i = i0;
+      for (; i < i1; ++i) {
+        const Req r = load_req<UR>(p, a, i, G);
+        const unsigned long long n = (unsigned long long)r.nrt * (unsigned)r.nt * (unsigned)p.Hkv;
+        if (start < before + n) break;
+        before += n;
+      }
+      misc->b0 = i;
+      misc->base = (long long)before;
+    }
+    if (threadIdx.x == 0) {
+      misc->total = (long long)total;
+      misc->parts = (int)parts;
+    }
+    __syncthreads();
+  }
+  const long long total = misc->total;
+  const long long parts = misc->parts;
+  const long long start = total * blockIdx.x / parts, stop = total * (blockIdx.x + 1) / parts;
+  if (blockIdx.x >= parts || start >= stop) return;
+
+  // The walk over units, the same in the producer and the consumers.
+  int b = misc->b0;
+  Req rq = load_req<UR>(p, a, b, G);
+  long long x = start;                       // next tile of the flattened space
+  long long ubase;                           // first tile of the current unit
+  int rt, h;
+  {
+    const long long in_b = start - misc->base;
+    const int u = (int)(in_b / rq.nt);
+    rt = u / p.Hkv;
+    h = u % p.Hkv;
+    ubase = misc->base + (long long)u * rq.nt;
+  }
+  auto next_unit = [&]() {                   // x has reached the unit's end
+    ubase += rq.nt;
+    if (++h < p.Hkv) return;
+    h = 0;
+    if (++rt < rq.nrt) return;
+    rt = 0;
+    do rq = load_req<UR>(p, a, ++b, G);
+    while (rq.nt == 0);                      // (some request follows: x < stop)
+  };
+
+  if (warp == kWarps) {
+    // --------------------------------------------------------- producer
+    const int box_rows = p.P < kTile ? p.P : kTile;
+    const int nbox = kTile / box_rows;       // page pieces of a tile
+    constexpr int kHalves = E4M3 ? 1 : D / 64;   // 64-column atoms of a bf16 tile
+    const uint32_t box_bytes = (uint32_t)(box_rows * (E4M3 ? D : 128));
+    const long long layer0 = (long long)a.layer * p.num_pages;
+    const int none = p.L * p.num_pages * p.Hkv;   // past the map: reads as zeros
+    int n = 0;                               // slots filled so far
+    bool stopped = a.debug_stall;            // a wait gave up (or test support: nothing is copied)
+    while (x < stop && !stopped) {
+      long long ue = ubase + rq.nt;
+      const int32_t* tab = p.tables + (size_t)__ldcg(p.rows + b) * p.W;
+      ue = ue < stop ? ue : stop;
+      // one lane per page piece; the next tile's page id is read a tile ahead
+      int tile = rq.t0 + (int)(x - ubase);
+      auto page_of = [&](int t) -> int {
+        const int tok = t * kTile + lane * box_rows;
+        if (lane >= nbox || tok >= rq.hi || tok + box_rows <= rq.lo) return -2;   // nothing any row sees
+        return __ldcg(tab + (tok >> p.logP));
+      };
+      int page = page_of(tile);
+      for (; x < ue && !stopped; ++x, ++tile) {
+        const int ahead = x + 1 < ue ? page_of(tile + 1) : -2;
+        const unsigned there = __ballot_sync(0xFFFFFFFFu, page != -2);
+        const int row0 = (tile * kTile + lane * box_rows) & (p.P - 1);
+        const bool ok = page >= 0 && page < p.num_pages;
+        if (page != -2 && !ok) atomicOr(reinterpret_cast<unsigned*>(p.state + PST_ERROR), KVRING_PAGES_ERR_TABLE);
+        const int c2 = ok ? (int)((layer0 + page) * p.Hkv + h) : none;
+#pragma unroll
+        for (int kv = 0; kv < 2 && !stopped; ++kv, ++n) {
+          const int s = n % L::kSlots, ph = (n / L::kSlots) & 1;
+          stopped = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ph ^ 1, abort, a.wait_ns));
+          if (stopped) break;
+          if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)__popc(there) * kHalves * box_bytes);
+          __syncwarp();
+          if (page != -2) {
+            const uint32_t dst = sbase + s * L::kSlot + lane * box_bytes;
+#pragma unroll
+            for (int hf = 0; hf < kHalves; ++hf)
+              tma_load_3d(dst + hf * (kTile * 128), kv ? &tmV : &tmK, hf * 64, row0, c2, full(s));
+          }
+        }
+        page = ahead;
+      }
+      if (x < stop && !stopped) next_unit();
+    }
+    // every copy lands before the CTA may exit
+    volatile int none_aborted = 0;
+    for (int i = n - L::kSlots < 0 ? 0 : n - L::kSlots; i < n; ++i)
+      mbar_wait_bounded(full(i % L::kSlots), (i / L::kSlots) & 1, &none_aborted, a.wait_ns);
+    return;
+  }
+
+  // ----------------------------------------------------------- consumers
+  // A wait that gives up raises the abort flag; from then on nobody waits
+  // and the rest of the range runs through on whatever the slots hold, so
+  // every barrier is still met and every ticket still drawn.
+  auto wait_full = [&](int s, int n) {
+    if (!*abort) mbar_wait_bounded(full(s), (n / L::kSlots) & 1, abort, a.wait_ns);
+  };
+  const int g = lane >> 2, c = lane & 3;
+  float* s_max = reinterpret_cast<float*>(fix + L::kMax);
+  float* s_sum = reinterpret_cast<float*>(fix + L::kSum);
+  int4* s_row = reinterpret_cast<int4*>(fix + L::kRow);
+  const uint32_t sQ = fbase + L::kQ, sP = fbase + L::kP;
+  const float* sc = p.scales + (size_t)a.layer * 4 * p.Hkv;
+  constexpr int kChunksQ = D / 8;                       // 16-byte chunks of a query row
+  constexpr int kDw = D == 128 ? 8 : 4;                 // warps that share the columns
+  const int dchunk = warp % kDw;                        // this warp's 16 columns
+  const int kk0 = D == 128 ? 0 : 4 * (warp / 4);   // its first 16-token step
+  int n = 0;
+  while (x < stop) {
+    const long long uend = ubase + rq.nt;
+    const long long ue = uend < stop ? uend : stop;
+    const int r0 = rt * UR;
+    const int rows = rq.nrows - r0 < UR ? rq.nrows - r0 : UR;
+    // ---- queries and row data into shared memory
+    sync_consumers();                                    // the previous unit is done with it
+    const float scale_k = E4M3 ? __ldcg(sc + h) : 1.0f;
+    for (int i = threadIdx.x; i < UR * kChunksQ; i += kConsumers) {
+      const int r = i / kChunksQ, ch = i % kChunksQ;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        const int row = r0 + r, tok = rq.q0 + row / G, head = h * G + row % G;
+        w = __ldcg(reinterpret_cast<const uint4*>(a.q + (long long)tok * a.q_stride + (size_t)head * D) + ch);
+      }
+      float fac = a.sm_log2;
+      if constexpr (E4M3) {
+        // the row's largest exponent, over the lanes that hold the row
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t em = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) em = max(em, max((u[e] >> 7) & 0xFFu, (u[e] >> 23) & 0xFFu));
+#pragma unroll
+        for (int o = kChunksQ / 2; o > 0; o >>= 1) em = max(em, __shfl_xor_sync(0xFFFFFFFFu, em, o));
+        // 2^(127 - em) and its inverse; infinities and NaN keep a factor of 1
+        // (and stay what they are), and so does a row of zeros
+        const bool plain = em == 0 || em >= 254;
+        const float down = plain ? 1.0f : __uint_as_float((254u - em) << 23);
+        fac *= scale_k * (plain ? 1.0f : __uint_as_float(em << 23));
+        uint32_t hq[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          hq[e] = f32x2_to_f16x2(__uint_as_float(u[e] << 16) * down, __uint_as_float(u[e] & 0xFFFF0000u) * down);
+        // columns 8 (ch & 1) + 0..7 of a group of 16: pair (4j, 4j+1) to place
+        // 2j, pair (4j+2, 4j+3) to place 2j + 8
+        const uint32_t rowb = sQ + r * (D * 2);
+        const int j0 = 2 * (ch & 1), cb = ch & ~1;
+        auto put = [&](int place, uint32_t v) {          // place: even column of the 16
+          const int k = cb + (place >> 3);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(rowb + ((uint32_t)(k ^ (r & 7)) << 4) + (place & 7) * 2), "r"(v)
+                       : "memory");
+        };
+        put(2 * j0, hq[0]);
+        put(2 * j0 + 8, hq[1]);
+        put(2 * j0 + 2, hq[2]);
+        put(2 * j0 + 10, hq[3]);
+      } else {
+        *reinterpret_cast<uint4*>(fix + L::kQ + r * (D * 2) + ((ch ^ (r & 7)) << 4)) = w;
+      }
+      if (ch == 0) {
+        int lo = 0, hi = 0;
+        if (r < rows) {
+          const int pos = rq.pos0 + (r0 + r) / G;
+          hi = a.causal ? pos + 1 : rq.klen;
+          lo = a.window > 0 && pos + 1 - a.window > 0 ? pos + 1 - a.window : 0;
+        }
+        s_row[r] = make_int4(lo, hi, __float_as_int(fac), 0);
+      }
+    }
+    sync_consumers();
+    float m_run[2 * MT], l_run[2 * MT], fac[2 * MT];
+    float acc[MT][2][4];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+      m_run[i] = -INFINITY;
+      l_run[i] = 0.f;
+      fac[i] = __int_as_float(s_row[8 * i + g].z);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][0][e] = acc[i][1][e] = 0.f;
+    // tokens that every row of the unit sees: tiles inside need no mask
+    const int all_hi = s_row[0].y, all_lo = s_row[rows - 1].x;
+
+    for (int tile = rq.t0 + (int)(x - ubase); x < ue; ++x, ++tile) {
+      const int tok0 = tile * kTile;
+      // ---- scores of this warp's 16 tokens
+      int s = n % L::kSlots;
+      wait_full(s, n);
+      float sc_[MT][2][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc_[i][0][e] = sc_[i][1][e] = 0.f;
+      const uint32_t sK = sbase + s * L::kSlot;
+      if constexpr (!E4M3) {
+        const int tok = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t kb[4];
+          const int ch = 2 * ks + ((lane >> 3) & 1);
+          ldsm4(kb, sK + (ch >> 3) * (kTile * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t qa[4];
+            const int r = 16 * i + (lane & 15);
+            ldsm4(qa, sQ + r * (D * 2) + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
+            mma16816<false>(sc_[i][0], qa, kb[0], kb[1]);
+            mma16816<false>(sc_[i][1], qa, kb[2], kb[3]);
+          }
+        }
+      } else {
+        const int tok = warp * 16 + (lane & 15);
+#pragma unroll
+        for (int k2 = 0; k2 < D / 32; ++k2) {
+          uint32_t kb[4];
+          ldsm4(kb, sK + swz_offset(tok, 2 * k2 + (lane >> 4), D));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int ks = 2 * k2 + half;
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              b[2 * e] = e4m3x2_to_f16x2((uint16_t)(kb[2 * half + e] & 0xFFFFu));
+              b[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(kb[2 * half + e] >> 16));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              uint32_t qa[4];
+              const int r = 16 * i + (lane & 15);
+              ldsm4(qa, sQ + r * (D * 2) + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
+              mma16816<true>(sc_[i][0], qa, b[0], b[1]);
+              mma16816<true>(sc_[i][1], qa, b[2], b[3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(s));
+      ++n;
+      const bool masked = tok0 < all_lo || tok0 + kTile > all_hi;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const float f = fac[2 * i + hr];
+          float mx = -INFINITY;
+          int lo = 0, hi = INT32_MAX;
+          if (masked) {
+            const int4 ri = s_row[16 * i + 8 * hr + g];
+            lo = ri.x;
+            hi = ri.y;
+          }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = sc_[i][nt][2 * hr + e];
+              const int tok = tok0 + warp * 16 + nt * 8 + 2 * c + e;
+              v = tok >= lo && tok < hi ? v * f : -INFINITY;
+              mx = fmaxf(mx, v);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+          if (c == 0) s_max[(16 * i + 8 * hr + g) * 8 + warp] = mx;
+        }
+      }
+      sync_consumers();
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          const int r = 16 * i + 8 * hr + g;
+          const float4 ma = *reinterpret_cast<const float4*>(s_max + r * 8);
+          const float4 mb = *reinterpret_cast<const float4*>(s_max + r * 8 + 4);
+          float& mr = m_run[2 * i + hr];
+          const float m = fmaxf(fmaxf(fmax3(ma.x, ma.y, ma.z), fmax3(ma.w, mb.x, mb.y)), fmax3(mb.z, mb.w, mr));
+          const float mu = m == -INFINITY ? 0.f : m;      // nothing seen yet: p = 2^-inf = 0
+          const float alpha = ex2_approx(mr - mu);
+          mr = m;
+          float sum = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const float p0 = ex2_approx(sc_[i][nt][2 * hr] - mu), p1 = ex2_approx(sc_[i][nt][2 * hr + 1] - mu);
+            sum += p0 + p1;
+            uint32_t w;
+            if constexpr (E4M3) {
+              w = f32x2_to_f16x2(p0, p1);
+            } else {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+              w = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            const int ch = 2 * warp + nt;                 // 16-byte chunk of the probability row
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sP + r * (kTile * 2) + ((ch ^ (r & 7)) << 4) + 4 * c), "r"(w)
+                         : "memory");
+          }
+          l_run[2 * i + hr] = l_run[2 * i + hr] * alpha + sum;
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            acc[i][nt][2 * hr] *= alpha;
+            acc[i][nt][2 * hr + 1] *= alpha;
+          }
+        }
+      }
+      sync_consumers();
+      // ---- values: this warp's 16 columns
+      s = n % L::kSlots;
+      wait_full(s, n);
+      const uint32_t sV = sbase + s * L::kSlot;
+      // tokens that no row sees may hold anything: their values become zeros
+      const bool vmask = tok0 < rq.lo || tok0 + kTile > rq.hi;
+      auto keep = [&](uint32_t w, int tok) {              // (tok, tok + 1) in the halves of w
+        const uint32_t m0 = tok >= rq.lo && tok < rq.hi ? 0xFFFFu : 0u;
+        const uint32_t m1 = tok + 1 >= rq.lo && tok + 1 < rq.hi ? 0xFFFF0000u : 0u;
+        return w & (m0 | m1);
+      };
+      auto pv = [&](int kk, uint32_t (&b)[4]) {           // b0, b1 of the two column tiles
+        if (vmask) {
+          const int tok = tok0 + 16 * kk + 2 * c;
+          b[0] = keep(b[0], tok);
+          b[1] = keep(b[1], tok + 8);
+          b[2] = keep(b[2], tok);
+          b[3] = keep(b[3], tok + 8);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          uint32_t pa[4];
+          const int r = 16 * i + (lane & 15);
+          ldsm4(pa, sP + r * (kTile * 2) + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4));
+          mma16816<E4M3>(acc[i][0], pa, b[0], b[1]);
+          mma16816<E4M3>(acc[i][1], pa, b[2], b[3]);
+        }
+      };
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int kq = 0; kq < (D == 128 ? 8 : 4); ++kq) {
+          const int kk = kk0 + kq;
+          const int tok = 16 * kk + (lane & 15), ch = 2 * dchunk + (lane >> 4);
+          uint32_t vb[4];
+          ldsm4t(vb, sV + (ch >> 3) * (kTile * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+          pv(kk, vb);
+        }
+      } else {
+#pragma unroll
+        for (int kq = 0; kq < (D == 128 ? 4 : 2); ++kq) {
+          const int kk = kk0 + 2 * kq;
+          uint32_t vr[4];
+          ldsm4t(vr, sV + swz_offset(16 * kk + lane, dchunk, D));
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t vb[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              vb[2 * e] = e4m3x2_to_f16x2((uint16_t)__byte_perm(vr[2 * half], 0u, e ? 0x31 : 0x20));
+              vb[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)__byte_perm(vr[2 * half + 1], 0u, e ? 0x31 : 0x20));
+            }
+            pv(kk + half, vb);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(s));
+      ++n;
+    }
+
+    // ---- end of the unit, or of this CTA's part of it
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+      float l = l_run[i];
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+      if (c == 0) s_sum[(8 * i + g) * 8 + warp] = l;
+    }
+    if constexpr (D == 64) {
+      // add the two token halves (through the probabilities' space)
+      sync_consumers();
+      float* half = reinterpret_cast<float*>(fix + L::kP);       // [UR][64]
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* cell = half + (16 * i + 8 * (e >> 1) + g) * 64 + 16 * dchunk + nt * 8 + 2 * c + (e & 1);
+            if (warp >= 4) *cell = acc[i][nt][e];
+          }
+      sync_consumers();
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (warp < 4)
+              acc[i][nt][e] += half[(16 * i + 8 * (e >> 1) + g) * 64 + 16 * dchunk + nt * 8 + 2 * c + (e & 1)];
+    } else {
+      sync_consumers();
+    }
+    const bool whole = ubase >= start && uend <= stop;
+    const float scale_v = E4M3 ? __ldcg(sc + p.Hkv + h) : 1.0f;
+    // column of accumulator (nt, e): bf16 16 w + 8 nt + 2 c + e, E4M3 16 w + 4 c + 2 e + nt
+    auto out_row = [&](int r) -> uint16_t* {
+      const int row = r0 + r;
+      return a.out + ((size_t)(rq.q0 + row / G) * p.Hq + h * G + row % G) * D;
+    };
+    auto bf2 = [](float lo, float hi) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+      return *reinterpret_cast<const uint32_t*>(&b2);
+    };
+    const int part = 2 * blockIdx.x + (ubase < start ? 0 : 1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const int r = 16 * i + 8 * hr + g;
+        if (r >= rows || (D == 64 && warp >= 4)) continue;
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) l += s_sum[r * 8 + w];
+        float v0 = acc[i][0][2 * hr], v1 = acc[i][0][2 * hr + 1];
+        float v2 = acc[i][1][2 * hr], v3 = acc[i][1][2 * hr + 1];
+        if (whole) {
+          const float inv = l > 0.f || l != l ? scale_v / l : 0.f;
+          uint16_t* o = out_row(r) + 16 * dchunk;
+          if constexpr (E4M3) {
+            *reinterpret_cast<uint2*>(o + 4 * c) = make_uint2(bf2(v0 * inv, v2 * inv), bf2(v1 * inv, v3 * inv));
+          } else {
+            *reinterpret_cast<uint32_t*>(o + 2 * c) = bf2(v0 * inv, v1 * inv);
+            *reinterpret_cast<uint32_t*>(o + 8 + 2 * c) = bf2(v2 * inv, v3 * inv);
+          }
+        } else {
+          float* o = p.part_o + ((size_t)part * kPartRows + r) * D + 16 * dchunk;
+          if constexpr (E4M3) {
+            *reinterpret_cast<float4*>(o + 4 * c) = make_float4(v0, v2, v1, v3);
+          } else {
+            *reinterpret_cast<float2*>(o + 2 * c) = make_float2(v0, v1);
+            *reinterpret_cast<float2*>(o + 8 + 2 * c) = make_float2(v2, v3);
+          }
+          if (c == 0 && dchunk == 0)
+            *reinterpret_cast<float2*>(p.part_ml + ((size_t)part * kPartRows + r) * 2) =
+                make_float2(m_run[2 * i + hr], l);
+        }
+      }
+    }
+    if (!whole) {
+      // CTAs whose ranges hold a tile of this unit: owner(t) is the last CTA
+      // whose range starts at or before tile t
+      const int first = (int)(((ubase + 1) * parts - 1) / total), last = (int)((uend * parts - 1) / total);
+      __threadfence();
+      sync_consumers();
+      if (threadIdx.x == 0) {
+        const int old = atomicAdd(p.tickets + first, 1);
+        misc->last = old == last - first;
+        if (misc->last) p.tickets[first] = 0;
+      }
+      sync_consumers();
+      if (misc->last) {
+        __threadfence();
+        for (int k = threadIdx.x; k < rows * (D / 4); k += kConsumers) {
+          const int r = k / (D / 4), d4 = k % (D / 4);
+          auto slot = [&](int cta) { return (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + r; };
+          float m = -INFINITY, l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int cta = first; cta <= last; ++cta) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(cta) * 2));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(cta) * D) + d4);
+            const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+            const float wa = ex2_approx(m - mu), wb = ex2_approx(ml.x - mu);
+            l = l * wa + ml.y * wb;
+            o.x = o.x * wa + v.x * wb;
+            o.y = o.y * wa + v.y * wb;
+            o.z = o.z * wa + v.z * wb;
+            o.w = o.w * wa + v.w * wb;
+            m = mn;
+          }
+          const float inv = l > 0.f || l != l ? scale_v / l : 0.f;
+          *reinterpret_cast<uint2*>(out_row(r) + 4 * d4) = make_uint2(bf2(o.x * inv, o.y * inv), bf2(o.z * inv, o.w * inv));
+        }
+      }
+    }
+    if (x < stop) next_unit();
+  }
+  if (threadIdx.x == 0 && *abort)
+    atomicOr(reinterpret_cast<unsigned*>(p.state + PST_ERROR), KVRING_PAGES_ERR_TIMEOUT);
+}
+
+template <int D, bool E4M3, int MT>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(k_paged_few<D, E4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              FewLayout<D, E4M3, MT>::kBytes);
+}
+template <int D, bool E4M3>
+cudaError_t prepare_rows() {
+  cudaError_t e = prepare_one<D, E4M3, 1>();
+  if (e == cudaSuccess) e = prepare_one<D, E4M3, 2>();
+  if (e == cudaSuccess) e = prepare_one<D, E4M3, 4>();
+  return e;
+}
+template <int D, bool E4M3, int MT>
+cudaError_t go(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s) {
+  return launch_pdl(k_paged_few<D, E4M3, MT>, dim3((unsigned)a.ctas), dim3(kFewThreads), FewLayout<D, E4M3, MT>::kBytes,
+                    s, *tmK, *tmV, p, a);
+}
+template <int D, bool E4M3>
+cudaError_t go_rows(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a, int unit_rows,
+                    cudaStream_t s) {
+  return unit_rows <= 16   ? go<D, E4M3, 1>(p, tmK, tmV, a, s)
+         : unit_rows <= 32 ? go<D, E4M3, 2>(p, tmK, tmV, a, s)
+                           : go<D, E4M3, 4>(p, tmK, tmV, a, s);
+}
+
+}  // namespace
+
+cudaError_t paged_few_prepare() {
+  cudaError_t e = prepare_rows<128, true>();
+  if (e == cudaSuccess) e = prepare_rows<128, false>();
+  if (e == cudaSuccess) e = prepare_rows<64, true>();
+  if (e == cudaSuccess) e = prepare_rows<64, false>();
+  return e;
+}
+
+cudaError_t launch_paged_few(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a,
+                             int unit_rows, cudaStream_t s) {
+  if (p.D == 128)
+    return p.e4m3 ? go_rows<128, true>(p, tmK, tmV, a, unit_rows, s) : go_rows<128, false>(p, tmK, tmV, a, unit_rows, s);
+  return p.e4m3 ? go_rows<64, true>(p, tmK, tmV, a, unit_rows, s) : go_rows<64, false>(p, tmK, tmV, a, unit_rows, s);
+}
+
+}  // namespace kvr

@@ -1,0 +1,444 @@
+"""The paged cache on the GPU against plain 64-bit forms: plan, commit and
+release against a host allocator, the write, the attention, and steps of
+all of them together."""
+import math
+import random
+
+import pytest
+import torch
+
+import ring_kv_cache_gb300 as kv
+from _pagescheck import Allocator, attention_64, close, errors, filled, i32, norm_rope_64
+
+pytestmark = pytest.mark.gpu
+
+
+def pool(page=16, num_pages=40, rows=6, most=200, tokens=64, **kw):
+    return kv.KvPages(kw.pop("hq", 2), kw.pop("hkv", 1), kw.pop("d", 64), page_size=page, num_pages=num_pages,
+                      max_requests=rows, max_request_tokens=most, max_tokens=tokens, **kw)
+
+
+def check_state(p, a):
+    torch.cuda.synchronize()
+    assert p.lengths.tolist() == a.lens
+    n = p.state[kv.PAGES_STATE["free"]].item()
+    assert p.free_pages[:n].tolist() == a.free
+    tab = p.tables.tolist()
+    for r, ln in enumerate(a.lens):
+        w = -(-ln // a.page)
+        assert tab[r][:w] == a.table[r][:w], r
+
+
+# ------------------------------------------------------------------- plan
+@pytest.mark.parametrize("page,rows,tokens,seed", [(16, 6, 64, 0), (64, 33, 500, 1), (128, 5, 3000, 2), (256, 3, 700, 3),
+                                                   (16, 700, 5000, 4), (32, 1, 1, 5), (16, 1500, 2049, 6)])
+def test_steps_follow_a_host_allocator(page, rows, tokens, seed):
+    rng = random.Random(seed)
+    most = max(3 * page + 5, 4 * tokens // rows + 40)
+    num = max(4, rows * 2 + tokens // page)
+    p = pool(page, num, rows, most, tokens)
+    a = Allocator(rows, p.W, page, num)
+    for step in range(12):
+        n = rng.randint(1, rows)
+        which = rng.sample(range(rows), n)
+        left, new = tokens, []
+        for _ in which:
+            x = rng.choice([0, 1, 1, 2, rng.randint(0, max(1, 3 * tokens // n))])
+            new.append(min(left, x))
+            left -= new[-1]
+        want = a.plan(which, new, tokens)
+        got = p.plan(i32(new), tokens, rows=i32(which), max_new=max(1, max(new)))
+        if want is None:   # no room: refused, and end some requests
+            assert errors(p) & (kv.PAGES_ERR_PAGES | kv.PAGES_ERR_LENGTH)
+            assert got.cu.tolist() == [0] * (n + 1) and set(got.slots.tolist()) == {-1}
+            p.state[kv.PAGES_STATE["error"]] = 0
+            p.commit()
+            check_state(p, a)
+            done = rng.sample(range(rows), max(1, rows // 2))
+            p.release(i32(done))
+            a.release(done)
+        else:
+            cu, lens, pos, slots, fresh, taken = want
+            assert got.cu.tolist() == cu and got.lengths.tolist() == lens
+            assert got.positions.tolist() == pos and got.slots.tolist() == slots
+            assert p.state[kv.PAGES_STATE["taken"]].item() == taken
+            if rng.random() < 0.7:   # a plan that is not committed costs nothing
+                p.commit()
+                a.commit(which, want)
+        check_state(p, a)
+    assert errors(p) == 0
+
+
+@pytest.mark.parametrize("rows,new,tokens,max_new,bit", [
+    ([0, 0], [1, 1], 8, None, kv.PAGES_ERR_ROW), ([0, 6], [1, 1], 8, None, kv.PAGES_ERR_ROW),
+    ([-1, 2], [1, 1], 8, None, kv.PAGES_ERR_ROW), ([0, 1], [1, -1], 8, None, kv.PAGES_ERR_TOKENS),
+    ([0, 1], [5, 4], 8, None, kv.PAGES_ERR_TOKENS), ([0, 1], [5, 1], 8, 4, kv.PAGES_ERR_TOKENS),
+    ([0, 1], [2 ** 31 - 1, 2 ** 31 - 1], 8, None, kv.PAGES_ERR_TOKENS), ([4, 1], [30, 2], 64, None, kv.PAGES_ERR_LENGTH),
+    ([0, 1], [50, 14], 64, None, kv.PAGES_ERR_PAGES)])
+def test_plans_that_cannot_be_made(rows, new, tokens, max_new, bit):
+    p = pool(16, 4, 6, 64, 64)
+    p.restore(i32([0, 0, 0, 0, 40, 0]), torch.full((6, 4), -1, dtype=torch.int32, device="cuda"), i32([0, 1, 2, 3]))
+    step = p.plan(i32(new), tokens, rows=i32(rows), max_new=max_new)
+    assert errors(p) == bit
+    assert step.cu.tolist() == [0, 0, 0] and step.slots.tolist() == [-1] * tokens
+    p.commit()
+    assert p.lengths.tolist() == [0, 0, 0, 0, 40, 0] and p.state[kv.PAGES_STATE["free"]].item() == 4
+    q = torch.ones((tokens, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 3.0)
+    p.attention(0, q, out=out)   # nothing planned: nothing written
+    assert bool((out == 3.0).all())
+
+
+def test_pages_that_the_pool_does_not_have_are_reported_and_skipped():
+    p = pool(16, 4, 2, 64, 64, cache_dtype=torch.bfloat16)
+    p.restore(i32([20, 5]), i32([[0, 99, -1, -1], [-7, -1, -1, -1]]), i32([1, 77]))
+    step = p.plan(i32([3, 14]), 20)
+    # request 0: page id 99; request 1: -7, then from the free list 77
+    assert step.slots.tolist() == [-1] * 20
+    assert errors(p) == kv.PAGES_ERR_TABLE
+    q = torch.ones((20, 2, 64), dtype=torch.bfloat16, device="cuda")
+    p.k_cache(0).fill_(1.0)
+    p.v_cache(0).fill_(1.0)
+    k = torch.ones((20, 1, 64), dtype=torch.bfloat16, device="cuda")
+    p.write(0, q, k, k * 5)
+    out = p.attention(0, q)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out[:17]).all()) and bool((p.v_cache(0) == 1.0).all())
+
+
+def test_commit_and_release_refusals():
+    p = pool(16, 8, 4, 64, 64)
+    p.commit()
+    assert errors(p) == kv.PAGES_ERR_COMMIT
+    p.state[kv.PAGES_STATE["error"]] = 0
+    p.plan(i32([20, 3]), 23)
+    p.commit()
+    for bad in ([0, 0], [0, 4], [-1]):
+        p.release(i32(bad))
+        assert errors(p) == kv.PAGES_ERR_ROW
+        p.state[kv.PAGES_STATE["error"]] = 0
+        assert p.lengths.tolist() == [20, 3, 0, 0] and p.state[kv.PAGES_STATE["free"]].item() == 5
+    p.release(i32([1, 3]))   # an empty row is no error
+    assert errors(p) == 0 and p.lengths.tolist() == [20, 0, 0, 0] and p.state[kv.PAGES_STATE["free"]].item() == 6
+    p.plan(i32([1]), 1)
+    p.release(i32([0]))      # drops the plan
+    p.commit()
+    assert errors(p) == kv.PAGES_ERR_COMMIT and p.lengths.tolist() == [0, 0, 0, 0]
+    assert sorted(p.free_pages.tolist()) == list(range(8))
+
+
+# ------------------------------------------------------------------ write
+def check_write(p, s, qkv, norm, pairing, tokens, wq, wk, eps=1e-6):
+    hq, hkv, d = p.Hq, p.Hkv, p.d
+    n = qkv.shape[0]
+    q, k, v = qkv.view(n, hq + 2 * hkv, d).split([hq, hkv, hkv], dim=1)
+    before_k, before_v = p.k_cache(s["layer"]).clone(), p.v_cache(s["layer"]).clone()
+    q_out = torch.full((n, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    p.write(s["layer"], q, k, v, q_norm=wq, k_norm=wk, eps=eps, q_out=q_out)
+    torch.cuda.synchronize()
+    assert bool((q_out[tokens:] == 7.0).all()), "rows past the plan"
+    pos, slots = p._pos[:tokens].long(), p._slots[:tokens].long()
+    fp = 2.0 ** -19   # fp32: the sum over d, rsqrt, the products
+    want, m = norm_rope_64(q[:tokens], wq, pos, pairing, eps)
+    close(q_out[:tokens], want, 2.0 ** -8 * want.abs() + fp * m + 1e-30, "q")
+    e4m3 = p.cache_dtype == torch.float8_e4m3fn
+    for name, x, w, cache, before in (("k", k, wk, p.k_cache(s["layer"]), before_k),
+                                      ("v", v, None, p.v_cache(s["layer"]), before_v)):
+        want, m = norm_rope_64(x[:tokens], w, pos if name == "k" else None, pairing, eps)
+        raw = cache.view(torch.uint8) if e4m3 else cache
+        got = raw[slots // p.P, :, slots % p.P]
+        if e4m3:
+            sc = s["s" + name].double()[:, None]
+            want, m = want / sc, m / sc
+            tol = 2.0 ** -4 * want.abs() + 2.0 ** -10 + fp * m
+            want = want.clamp(-448, 448)
+            got = got.view(cache.dtype)
+        else:
+            tol = (2.0 ** -8 * want.abs() + fp * m) * (1 if name == "k" else 0)
+        close(got.to(torch.float64), want, tol + 1e-30, name)
+        # nothing else has changed
+        other = torch.ones((p.num_pages, p.P), dtype=torch.bool, device="cuda")
+        other[slots // p.P, slots % p.P] = False
+        a, b = [t.view(torch.uint8).view(p.num_pages, hkv, p.P, -1).transpose(1, 2)[other] for t in (cache, before)]
+        assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d,page,total,new,pad", [
+    (4, 2, 64, 16, [37, 1, 64, 20], [3, 1, 0, 17], 5), (10, 10, 128, 64, [1], [1], 0), (7, 1, 128, 128, [300, 129], [150, 1], 1),
+    (40, 8, 64, 256, [700], [500], 0), (3, 3, 64, 32, [33] * 9, [1] * 9, 3)])
+def test_write(hq, hkv, d, page, total, new, pad, cache, pairing):
+    p, s = filled(hq, hkv, d, page, total, new, cache, seed=1, layers=2, layer=1, pairing=pairing, pad=pad)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    n = sum(new) + pad
+    for norm in (True, False):
+        qkv = (3.0 * torch.randn((n, (hq + 2 * hkv) * d), generator=g, device="cuda")).to(torch.bfloat16)
+        qkv[sum(new):] = math.nan   # padding is not read
+        wq, wk = [(0.5 + torch.rand(d, generator=g, device="cuda")).to(torch.bfloat16) if norm else None for _ in "qk"]
+        check_write(p, s, qkv, norm, pairing, sum(new), wq, wk)
+    assert errors(p) == 0
+
+
+def test_write_extremes():
+    """Zero rows, saturation, infinities and NaN stay in their own rows."""
+    p, s = filled(2, 2, 64, 16, [8], [8], "e4m3", seed=3)
+    x = torch.ones((8, 6, 64), dtype=torch.bfloat16, device="cuda")
+    x[0] = 0.0
+    x[1] = 3e38
+    x[2, :, 5] = math.inf
+    x[3, :, 9] = math.nan
+    q, k, v = x.split([2, 2, 2], dim=1)
+    one = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    q_out = p.write(0, q, k, v, q_norm=one, k_norm=one)
+    sl = p._slots[:8].long()
+    kc = p.k_cache(0).view(torch.uint8)[sl // 16, :, sl % 16].view(torch.float8_e4m3fn).float()
+    vc = p.v_cache(0).view(torch.uint8)[sl // 16, :, sl % 16].view(torch.float8_e4m3fn).float()
+    assert bool((q_out[0] == 0).all()) and bool((kc[0] == 0).all()) and bool((vc[0] == 0).all())
+    assert bool((vc[1] == 448).all())
+    assert bool((vc[2, :, 5] == 448).all()) and bool(torch.isnan(vc[3, :, 9]).all())
+    for t in (4, 5, 6, 7):
+        assert bool(torch.isfinite(q_out[t]).all()) and bool(torch.isfinite(kc[t]).all())
+    assert bool(torch.isnan(q_out[3]).all())
+
+
+# -------------------------------------------------------------- attention
+CASES = [
+    # hq, hkv, d, page, total, new
+    (4, 4, 64, 16, [1], [1]),
+    (8, 2, 128, 64, [127, 128, 129, 1, 300], [1, 1, 1, 1, 1]),
+    (7, 1, 128, 16, [500, 33, 17], [1, 1, 1]),
+    (32, 4, 64, 32, [1000, 77], [2, 0]),
+    (10, 10, 128, 128, [2500], [1]),
+    (64, 1, 64, 256, [400, 3], [1, 2]),
+    (6, 3, 64, 64, [70, 5, 200], [9, 5, 12]),
+    (5, 1, 128, 16, [130, 64], [13, 64]),
+    (2, 2, 128, 64, [700, 260], [300, 129]),
+    (12, 4, 64, 128, [513, 1, 90], [257, 1, 40]),
+]
+
+
+@pytest.mark.parametrize("mask", ["causal", "window", "all"])
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
+def test_attention(case, cache, mask):
+    hq, hkv, d, page, total, new = case
+    p, s = filled(hq, hkv, d, page, total, new, cache, seed=11, layers=2, layer=1, pad=2)
+    kw = dict(causal=mask != "all", window=50 if mask == "window" else 0)
+    n = sum(new)
+    out = torch.full((n + 2, hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    p.attention(1, s["q"], out=out, **kw)
+    want, tol = attention_64(p, s, **kw)
+    close(out[:n], want[:n], tol[:n], mask)
+    assert bool((out[n:] == 9.0).all()) and errors(p) == 0
+    again = p.attention(1, s["q"], **kw)
+    assert torch.equal(again[:n], out[:n]), "not the same twice"
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("total,new,hq,hkv", [([20000], [1], 4, 2), ([9000, 40, 3000, 1, 12000], [1, 1, 1, 1, 1], 8, 8),
+                                              ([6000, 100], [40, 30], 8, 1), ([4000], [700], 4, 1)])
+def test_attention_split_over_many_ranges(total, new, hq, hkv, cache):
+    p, s = filled(hq, hkv, 128, 64, total, new, cache, seed=5)
+    out = p.attention(0, s["q"])
+    want, tol = attention_64(p, s)
+    close(out, want, tol)
+    assert errors(p) == 0
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_attention_strided_queries_scale_and_large_scores(cache):
+    p, s = filled(4, 2, 128, 64, [300, 150], [1, 5], cache, seed=6, magnitude=40.0)
+    wide = torch.randn((6, 9, 128), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(torch.bfloat16)
+    q = wide[:, 3:7]
+    assert not q.is_contiguous()
+    out = p.attention(0, q, scale=0.3)
+    want, tol = attention_64(p, s, q=q, scale=0.3)
+    close(out, want, tol)
+
+
+def test_tensors_shorter_than_the_plan():
+    """The planned tokens that the tensors hold, at their own positions."""
+    p, s = filled(4, 2, 64, 16, [40, 30, 9], [3, 5, 4], "bf16", seed=8)
+    want, tol = attention_64(p, s)
+    for n in (1, 3, 6, 8, 11):
+        out = p.attention(0, s["q"][:n])
+        close(out, want[:n], tol[:n], n)
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_queries_of_any_size(cache):
+    """Tiny, zero and huge query rows: the 8-bit cache's queries change type."""
+    p, s = filled(2, 1, 64, 16, [100], [5], cache, seed=7)
+    q = s["q"].clone()
+    q[0] = 0.0
+    q[1] *= 2.0 ** -100
+    q[2] *= 2.0 ** 40
+    q[3, 0, 0] = math.nan
+    out = p.attention(0, q)
+    want, tol = attention_64(p, s, q=q)
+    ok = [0, 1, 4]
+    close(out[ok], want[ok], tol[ok])
+    assert bool(torch.isnan(out[3, 0]).all()) and bool(torch.isfinite(out[3, 1]).all())
+    # row 2 is one-hot on its largest score
+    close(out[2], want[2], 2.0 ** -7 * want[2].abs() + 1e-6)
+
+
+# --------------------------------------------------------------- together
+def plain_step(hist, qkv, cu, hq, hkv, d, pairing, wq, wk, cache, sk, sv):
+    """One layer's step on host lists of (k, v) float64 per request."""
+    q, k, v = qkv.view(-1, hq + 2 * hkv, d).split([hq, hkv, hkv], dim=1)
+    outs = []
+    for r, (a, b) in hist["span"].items():
+        n = b - a
+        pos = torch.arange(hist["len"][r], hist["len"][r] + n, device="cuda")
+        qq = norm_rope_64(q[a:b], wq, pos, pairing)[0].to(torch.bfloat16).double()
+        kk, vv = norm_rope_64(k[a:b], wk, pos, pairing)[0], v[a:b].double()
+        if cache == "e4m3":
+            rnd = lambda x, sc: ((x / sc[:, None].double()).clamp(-448, 448).float().to(torch.float8_e4m3fn).double()  # noqa: E731
+                                 * sc[:, None].double())
+            kk, vv = rnd(kk, sk), rnd(vv, sv)
+        else:
+            kk = kk.to(torch.bfloat16).double()
+        old = hist["kv"].get(r)
+        kk, vv = (kk, vv) if old is None else (torch.cat([old[0], kk]), torch.cat([old[1], vv]))
+        hist["kv"][r] = (kk, vv)
+        G = hq // hkv
+        w = torch.einsum("ihd,jhd->hij", qq, kk.repeat_interleave(G, 1)) / math.sqrt(d)
+        j = torch.arange(kk.shape[0], device="cuda")
+        w = torch.softmax(w.masked_fill(j[None, None] > pos[None, :, None], -math.inf), -1)
+        outs.append((r, torch.einsum("hij,jhd->ihd", w, vv.repeat_interleave(G, 1))))
+    return dict(outs)
+
+
+@pytest.mark.parametrize("cache,pairing,graph", [("bf16", "halves", False), ("e4m3", "adjacent", False),
+                                                 ("e4m3", "halves", True)])
+def test_steps_of_all_operators_together(cache, pairing, graph):
+    """Prompts, single tokens, ended and restarted requests, as a serving
+    loop runs them; decode steps captured once and replayed."""
+    hq, hkv, d, rows = 6, 2, 64, 5
+    dt = torch.float8_e4m3fn if cache == "e4m3" else torch.bfloat16
+    p = kv.KvPages(hq, hkv, d, page_size=16, num_pages=60, max_requests=rows, max_request_tokens=300, max_tokens=260,
+                   cache_dtype=dt, rope_pairing=pairing)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    sk, sv = torch.full((hkv,), 0.02, device="cuda"), torch.full((hkv,), 0.01, device="cuda")
+    if cache == "e4m3":
+        p.set_scales(0, sk, sv)
+    wq, wk = [(0.8 + 0.4 * torch.rand(d, generator=g, device="cuda")).to(torch.bfloat16) for _ in "qk"]
+    hist = dict(len=[0] * rows, kv={}, span={})
+    decode = {}
+
+    def run(qkv, q_out, out):
+        q, k, v = qkv.view(-1, hq + 2 * hkv, d).split([hq, hkv, hkv], dim=1)
+        p.write(0, q, k, v, q_norm=wq, k_norm=wk, q_out=q_out)
+        p.attention(0, q_out, out=out)
+        p.commit()
+
+    plan = [([0, 1, 2], [130, 7, 40]), ([2, 0, 1], [1, 1, 1]), ([0, 1, 2], [1, 1, 1]), ([0, 1, 2], [1, 1, 1]), "end 0",
+            ([0, 3, 1], [33, 64, 1]), ([1, 3, 0], [1, 1, 1]), ([0, 4, 2, 3], [3, 90, 0, 1])]
+    for step in plan:
+        if step == "end 0":
+            p.release(i32([0]))
+            hist["len"][0] = 0
+            del hist["kv"][0]
+            continue
+        which, new = step
+        n = sum(new)
+        qkv = (2 * torch.randn((n, (hq + 2 * hkv) * d), generator=g, device="cuda")).to(torch.bfloat16)
+        hist["span"], at = {}, 0
+        for r, m in zip(which, new):
+            if m:
+                hist["span"][r] = (at, at + m)
+            at += m
+        if graph and new == [1, 1, 1]:
+            if not decode:
+                st = dict(rows=i32(which), new=i32(new), qkv=qkv.clone(),
+                          q_out=torch.empty((3, hq, d), dtype=torch.bfloat16, device="cuda"),
+                          out=torch.empty((3, hq, d), dtype=torch.bfloat16, device="cuda"))
+                torch.cuda.synchronize()
+                cg = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(cg):
+                    p.plan(st["new"], 3, rows=st["rows"])
+                    run(st["qkv"], st["q_out"], st["out"])
+                decode.update(st, g=cg)
+            decode["rows"].copy_(i32(which))
+            decode["qkv"].copy_(qkv)
+            decode["g"].replay()
+            out = decode["out"].clone()
+        else:
+            p.plan(i32(new), n, rows=i32(which), max_new=max(new))
+            q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device="cuda")
+            out = torch.empty_like(q_out)
+            run(qkv, q_out, out)
+        want = plain_step(hist, qkv, None, hq, hkv, d, pairing, wq, wk, cache, sk, sv)
+        torch.cuda.synchronize()
+        for r, (a, b) in hist["span"].items():
+            # codes and bf16 values may fall on the other side of a rounding
+            # border in fp32: a relative norm, not a value's bound
+            o = out[a:b].double()
+            assert float((o - want[r]).norm() / want[r].norm()) < 2.0 ** -7, (step, r)
+            hist["len"][r] += b - a
+        assert p.lengths.tolist() == hist["len"]
+    assert errors(p) == 0
+
+
+def test_calls_on_a_stream_of_their_own_and_a_wait_that_gives_up():
+    p, s = filled(4, 2, 64, 32, [400, 3], [1, 1], "bf16", seed=9)
+    want, tol = attention_64(p, s)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(s["q"])
+    p.attention(0, s["q"], out=out, stream=st)
+    st.synchronize()
+    close(out, want, tol)
+    p.set_wait(2_000_000, stall=True)
+    p.attention(0, s["q"], out=out)
+    torch.cuda.synchronize()
+    assert errors(p) == kv.PAGES_ERR_TIMEOUT
+    p.set_wait()
+    p.attention(0, s["q"], out=out)
+    close(out, want, tol)
+
+
+# ---------------------------------------------------------------- refusals
+def test_refusals_of_the_binding():
+    p, s = filled(4, 2, 64, 16, [20], [4], "bf16", seed=1)
+    q = s["q"]
+    k = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for bad in (dict(causal=False, window=3), dict(window=-1), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan)):
+        with pytest.raises(kv.KvRingError):
+            p.attention(0, q, **bad)
+    for bad in (q.float(), q[:, :3], q[..., :32], q.cpu(), q.transpose(0, 1).contiguous().transpose(0, 1), q[0]):
+        with pytest.raises(ValueError):
+            p.attention(0, bad)
+    with pytest.raises(kv.KvRingError):
+        p.attention(1, q)
+    with pytest.raises(kv.KvRingError):
+        p.attention(0, q, out=q)
+    with pytest.raises(kv.KvRingError):   # 4 tokens of 9, off by 8 bytes
+        p.attention(0, torch.zeros(4 * 256 + 8, dtype=torch.bfloat16, device="cuda")[4:4 + 1024].view(4, 4, 64))
+    with pytest.raises(kv.KvRingError):
+        p.attention(0, torch.zeros((5, 4, 64), dtype=torch.bfloat16, device="cuda"))   # beyond max_tokens
+    with pytest.raises(kv.KvRingError):
+        p.write(0, q, k, k, q_out=q)
+    with pytest.raises(kv.KvRingError):
+        p.write(0, q, k, k, eps=-1.0)
+    with pytest.raises(ValueError):
+        p.write(0, q, k[:3], k)
+    with pytest.raises(ValueError):
+        p.write(0, q, k, k, q_norm=torch.ones(64, device="cuda"))
+    with pytest.raises(kv.KvRingError):
+        p.set_scales(0, torch.ones(2, device="cuda"), torch.ones(2, device="cuda"))   # a bf16 cache has none
+    with pytest.raises(ValueError):
+        p.plan(torch.ones(1, dtype=torch.int64, device="cuda"), 4)
+    with pytest.raises(ValueError):
+        p.plan(i32([1]), 4, rows=i32([0, 1]))
+    for args in ((i32([1]), 0), (i32([1]), 5), (i32([1, 1]), 2)):
+        with pytest.raises(kv.KvRingError):
+            p.plan(*args)
+    with pytest.raises(kv.KvRingError):
+        p.plan(i32([1]), 4, max_new=0)
+    with pytest.raises(ValueError):
+        p.restore(i32([1, 2]), p.tables, i32([0]))
+    assert errors(p) == 0
