@@ -476,8 +476,10 @@ kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const voi
 kvring_status kvring_pages_attention(kvring_pages_t* pages, int32_t layer, const void* q, int64_t q_stride, void* out,
                                      int32_t num_tokens, int32_t causal, int32_t window, float scale, void* stream);
 
-/* Test support for the chunk kernel's bounded waits: as
- * kvring_debug_set_attention_wait (limit_ns in [1000, 6e10], stall 0 or 1). */
+/* Test support for the bounded waits of the attention kernels: as
+ * kvring_debug_set_attention_wait (limit_ns in [1000, 6e10], stall 0 or 1).
+ * A call whose waits gave up sets KVRING_PAGES_ERR_TIMEOUT and leaves `out`
+ * undefined; plan again before the next call. */
 kvring_status kvring_pages_debug_set_wait(kvring_pages_t* pages, int64_t limit_ns, int32_t stall);
 
 /* Copy the ring out for inspection (tests, snapshots).  Any pointer may be

@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(kPlanThreads)
       p.cu[i] = bad ? 0 : s_cu[i];
       p.klen[i] = bad ? s_len[i] : s_len[i] + s_cu[i + 1] - s_cu[i];
     }
+    // (only an attention whose waits gave up leaves tickets behind)
+    for (int i = threadIdx.x; i < 2 * kPagedMaxCtas; i += kPlanThreads) p.tickets[i] = 0;
     if (threadIdx.x == 0) {
       p.cu[B] = tokens;
       p.state[PST_PLANNED] = 1;

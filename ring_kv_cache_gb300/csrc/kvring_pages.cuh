@@ -36,7 +36,7 @@ struct PagesDev {
   const float* table;     // [W * P][D/2][2] fp32 (cos, sin)
   float* part_o;          // [2 * kPagedMaxCtas][kPartRows][D] attention partials
   float* part_ml;         // [2 * kPagedMaxCtas][kPartRows][2] their running maxima and sums
-  int32_t* tickets;       // [kPagedMaxCtas] arrivals per split unit (0 between calls)
+  int32_t* tickets;       // [2 * kPagedMaxCtas] arrivals per split unit (0 between calls)
   int Hq, Hkv, D, L, P, logP, num_pages, R, W, max_tokens;
   int e4m3;               // cache type
   int halves;             // rotation pairs (i, i + d/2)
@@ -80,6 +80,11 @@ cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_co
 cudaError_t paged_few_prepare();
 cudaError_t launch_paged_few(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a,
                              int unit_rows, cudaStream_t s);
+
+// ... and many (chunks).
+cudaError_t paged_chunk_prepare();
+cudaError_t launch_paged_chunk(const PagesDev& p, const CUtensorMap* tmQ, const CUtensorMap* tmK,
+                               const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s);
 
 // One launch with the programmatic-stream-serialisation attribute.
 template <typename... KP, typename... A>

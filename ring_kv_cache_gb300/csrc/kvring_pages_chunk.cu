@@ -1,0 +1,812 @@
+// Attention over the paged cache for requests with many query rows (chunks
+// of a prompt, whole frames), on the tcgen05 tensor cores.
+//
+//   out[r] = sum_j softmax_j(s_rj) V[j],  s_rj = scale q[r] . K[j]
+// in one pass over the keys with a running maximum per row, raised only when
+// a tile's maximum exceeds it by more than 8 (log2 units): then and only then
+// is the accumulator rescaled.  Probabilities carry 2^7 relative to that
+// maximum, so that the largest is 2^15 (inside f16) and small ones stay
+// normal numbers; they are rounded once to the 16-bit type of the values'
+// operand, the normaliser sums them unrounded in fp32.
+//
+// Bound by the tensor cores: 4 rows keys d operations against
+// 2 keys d cached values per 256 rows.  A unit is 256 query rows of one
+// request and key/value head, a row being one query head of one token, so
+// all query heads of a key/value head share its tiles and the causal
+// diagonal is as fine as the tokens of a unit; two row groups of 128 take
+// turns on the tensor cores: while one group's scores are turned into
+// probabilities, the other's products run.  Per 128-token tile and group:
+//   S_g = Q_g K^T  (kind::f16, both operands from shared memory)
+//   O_g += P_g V   (P from TMEM, over S_g's columns; V MN-major from shared
+//                   memory, as the TMA wrote it)
+// TMEM: S_0, S_1, O_0, O_1, 128 columns each.
+//
+// The (request, row tile, head, key tile) space is flattened and cut into
+// one contiguous range per CTA, as in the kernel for few rows; units cut by a
+// range's border leave partial (m, l, O) in the workspace and the last CTA to
+// arrive merges them in range order.
+//
+// Warps: 0-7 softmax (group = warp / 4, thread = row), 8 copies (walks the
+// units, writes their descriptors into a small queue, TMA), 9 the MMA issuer,
+// 10.. helpers: over an E4M3 cache they widen each landed tile, exactly, to
+// f16 (K and V); over a bf16 cache they only touch tiles at the borders of
+// what a request may read, whose values at other places become zeros.
+//
+// Queries over an E4M3 cache: f16 after scaling each row by a power of two
+// into [1, 2) at its largest value (bf16's 8 significant bits fit f16's 11).
+//
+// Every wait, those between the threads of a group included, is an mbarrier
+// wait with a limit; after one gives up nobody waits any more, every warp
+// leaves at its next unit, copies and MMAs in flight are drained, TMEM is
+// freed and KVRING_PAGES_ERR_TIMEOUT is set.  Tickets that were then not
+// drawn are cleared by the next plan.
+#include "kvring_pages.cuh"
+
+namespace kvr {
+namespace {
+
+constexpr int kWarpCopy = 8, kWarpIssue = 9;
+constexpr int kUnitQueue = 4;
+constexpr float kRaise = 8.0f;    // log2 units
+constexpr float kShift = 7.0f;
+constexpr int kChunkSmem = 232448;
+
+template <int D, bool E4M3>
+struct ChunkLayout {
+  // Over an E4M3 cache the helpers are a warpgroup of their own (warps
+  // 12-15, 10 and 11 idle), so that registers can move between warpgroups.
+  static constexpr int kWarpHelp = E4M3 ? 12 : 10;
+  static constexpr int kHelpers = E4M3 ? 4 : 2;                  // warps
+  static constexpr int kThreads = 32 * (kWarpHelp + kHelpers);
+  static constexpr int kAtom = kTile * 128;                      // 128 rows x 64 16-bit columns
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kQGroup = kAtoms * kAtom;
+  static constexpr int kSlot = kAtoms * kAtom;                   // one 16-bit K or V tile
+  static constexpr int kRaw = E4M3 ? kTile * D : 0;              // one E4M3 tile
+  static constexpr int kSlots = D == 128 ? (E4M3 ? 4 : 5) : (E4M3 ? 8 : 11);
+  static constexpr int kRaws = E4M3 ? (D == 128 ? 2 : 6) : 0;
+  static constexpr int kQ = 0;
+  static constexpr int kKV = 2 * kQGroup;
+  static constexpr int kRawAt = kKV + kSlots * kSlot;
+  static constexpr int kMisc = kRawAt + kRaws * kRaw;
+  static constexpr int kBytes = 1024 + kMisc + 1024;
+  static_assert(kBytes <= kChunkSmem, "fits one CTA per SM");
+};
+
+// One unit, or the part of it in this CTA's range.
+struct Unit {
+  int q_tok;       // first token in q and out
+  int pos0;        // its position
+  int ntok;        // tokens of the unit
+  int klen;        // the request's length
+  int vlo, vhi;    // tokens any row of the unit sees: [vlo, vhi)
+  int tile0, ntile;
+  int h;
+  int whole;       // all of its tiles are this CTA's
+  int part;        // workspace slot, if not
+  int first, last; // the CTAs that share it
+  int end;         // no unit follows
+};
+
+struct ChunkMisc {
+  uint64_t u_full[kUnitQueue], u_empty[kUnitQueue];
+  uint64_t q_full, q_ready, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  // ring slots: the copy landed (bf16 only), the helpers are done with it,
+  // its MMAs have read it; and the E4M3 tiles before they are widened
+  uint64_t full[11], ready[11], empty[11], raw_full[6], raw_empty[6];
+  uint64_t done, grp[2];
+  unsigned long long ws[16];
+  long long total, base;
+  Unit u[kUnitQueue];
+  uint32_t tmem;
+  int b0, rt0, parts, abort, last[2];
+};
+static_assert(sizeof(ChunkMisc) <= 1024, "misc block");
+
+struct ChunkReq {
+  int q0, nq, klen, pos0, nrt;
+};
+
+__device__ __forceinline__ ChunkReq load_chunk_req(const PagesDev& p, const PagedAttn& a, int b, int G, int tpu) {
+  ChunkReq r;
+  r.q0 = __ldcg(p.cu + b);
+  const int end = __ldcg(p.cu + b + 1);
+  r.klen = __ldcg(p.klen + b);
+  r.pos0 = r.klen - (end - r.q0);
+  r.nq = (end < a.T ? end : a.T) - r.q0;
+  if (r.nq < 0 || r.klen <= 0 || (end - r.q0) * (long long)G <= a.min_rows || (end - r.q0) * (long long)G > a.max_rows)
+    r.nq = 0;
+  r.nrt = (r.nq + tpu - 1) / tpu;
+  return r;
+}
+// The key tiles [t0, t0 + nt) of row tile rt.
+__device__ __forceinline__ int chunk_tiles(const PagedAttn& a, const ChunkReq& r, int rt, int tpu, int* t0) {
+  const int i0 = rt * tpu, i1 = i0 + tpu < r.nq ? i0 + tpu : r.nq;
+  const int hi = a.causal ? r.pos0 + i1 : r.klen;
+  int lo = a.window > 0 ? r.pos0 + i0 + 1 - a.window : 0;
+  lo = lo > 0 ? lo : 0;
+  *t0 = lo / kTile;
+  return (hi + kTile - 1) / kTile - *t0;
+}
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                           uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// idesc of kind::f16: bf16 operands have type code 1, f16 code 0.
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool b_mn_major, bool bf16) {
+  return idesc_f16(M, N, b_mn_major) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
+    k_paged_chunk(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PagesDev p, const PagedAttn a) {
+  using L = ChunkLayout<D, E4M3>;
+  constexpr int kThreads = L::kThreads, kHelpThreads = 32 * L::kHelpers;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(sm);
+  ChunkMisc* misc = reinterpret_cast<ChunkMisc*>(sm + L::kMisc);
+  volatile int* abort = &misc->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv, TG = kTile / G, tpu = 2 * TG;   // tokens of a group, of a unit
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+  auto wait = [&](uint64_t& b, uint32_t parity) {
+    if (!*abort) mbar_wait_bounded(smem_u32(&b), parity, abort, a.wait_ns);
+  };
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+    for (int i = 0; i < kUnitQueue; ++i) {
+      mbar_init(bar(misc->u_full[i]), 1);
+      mbar_init(bar(misc->u_empty[i]), 8 + 1 + L::kHelpers);
+    }
+    mbar_init(bar(misc->q_full), 1);
+    mbar_init(bar(misc->q_ready), 256);
+    mbar_init(bar(misc->q_empty), 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(misc->s_full[g]), 1);
+      mbar_init(bar(misc->p_full[g]), 128);
+      mbar_init(bar(misc->o_full[g]), 1);
+      mbar_init(bar(misc->o_free[g]), 128);
+    }
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(bar(misc->full[i]), 1);
+      mbar_init(bar(misc->empty[i]), 1);
+      mbar_init(bar(misc->ready[i]), E4M3 ? kHelpThreads : L::kHelpers);
+    }
+    for (int i = 0; i < L::kRaws; ++i) {
+      mbar_init(bar(misc->raw_full[i]), 1);
+      mbar_init(bar(misc->raw_empty[i]), kHelpThreads);
+    }
+    mbar_init(bar(misc->done), 1);
+    for (int g = 0; g < 2; ++g) mbar_init(bar(misc->grp[g]), 128);
+    misc->abort = 0;
+    mbar_fence_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ------------------------------------------------- this CTA's range
+  const int B = __ldcg(p.state + PST_REQUESTS);
+  {
+    const int per = (B + kThreads - 1) / kThreads;
+    const int i0 = threadIdx.x * per, i1 = i0 + per < B ? i0 + per : B;
+    unsigned long long mine = 0;
+    int t0;
+    for (int i = i0; i < i1; ++i) {
+      const ChunkReq r = load_chunk_req(p, a, i, G, tpu);
+      for (int rt = 0; rt < r.nrt; ++rt) mine += (unsigned)chunk_tiles(a, r, rt, tpu, &t0);
+    }
+    unsigned long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) misc->ws[warp] = x;
+    __syncthreads();
+    unsigned long long before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += misc->ws[w];
+      total += misc->ws[w];
+    }
+    total *= (unsigned)p.Hkv;
+    before = (before + x - mine) * (unsigned)p.Hkv;
+    mine *= (unsigned)p.Hkv;
+    unsigned long long parts = total / (unsigned)a.min_tiles;
+    parts = parts < 1 ? 1 : (parts > gridDim.x ? gridDim.x : parts);
+    const unsigned long long start = blockIdx.x < parts ? total * blockIdx.x / parts : total;
+    if (mine && start >= before && start < before + mine) {   // exactly one thread, unless total is 0
+      bool found = false;
+      for (int i = i0; i < i1 && !found; ++i) {
+        const ChunkReq r = load_chunk_req(p, a, i, G, tpu);
+        for (int rt = 0; rt < r.nrt; ++rt) {
+          const unsigned long long n = (unsigned long long)chunk_tiles(a, r, rt, tpu, &t0) * (unsigned)p.Hkv;
+          if (start < before + n) {
+            misc->b0 = i;
+            misc->rt0 = rt;
+            misc->base = (long long)before;
+            found = true;
+            break;
+          }
+          before += n;
+        }
+      }
+    }
+    if (threadIdx.x == 0) {
+      misc->total = (long long)total;
+      misc->parts = (int)parts;
+    }
+    __syncthreads();
+  }
+  const long long total = misc->total, parts = misc->parts;
+  const long long start = total * blockIdx.x / parts, stop = total * (blockIdx.x + 1) / parts;
+  if (blockIdx.x >= parts || start >= stop) return;
+  if (warp == kWarpIssue) {
+    tmem_alloc(smem_u32(&misc->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+  // whether a tile holds tokens outside [vlo, vhi), or tokens that some row
+  // of the unit does not see
+  auto edge_tile = [&](const Unit& u, int j) {
+    const int t = (u.tile0 + j) * kTile;
+    const int seen = a.causal ? u.pos0 + 1 : u.klen;                 // every row sees up to here
+    const int from = a.window > 0 ? u.pos0 + u.ntok - a.window : 0;  // and from here
+    return t + kTile > seen || t < from;
+  };
+
+  // Over an E4M3 cache 512 threads x 128 registers become 256 x 176 for the
+  // softmax and 256 x 80 for the rest (65,536 in all, before and after).
+  if (warp >= 8) {
+    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp == kWarpCopy) {
+    // ------------------------------------------------------------ copies
+    const int box_rows = p.P < kTile ? p.P : kTile, nbox = kTile / box_rows;
+    constexpr int kBoxes = E4M3 ? 1 : L::kAtoms;
+    const uint32_t box_bytes = (uint32_t)(box_rows * (E4M3 ? D : 128));
+    const long long layer0 = (long long)a.layer * p.num_pages;
+    const int none = p.L * p.num_pages * p.Hkv;
+    constexpr int kRing = E4M3 ? L::kRaws : L::kSlots;
+    uint64_t* full = E4M3 ? misc->raw_full : misc->full;
+    uint64_t* empty = E4M3 ? misc->raw_empty : misc->empty;
+    constexpr int kRingAt = E4M3 ? L::kRawAt : L::kKV, kRingSize = E4M3 ? L::kRaw : L::kSlot;
+    bool stopped = a.debug_stall;
+    int b = misc->b0, rt = misc->rt0, t0;
+    ChunkReq rq = load_chunk_req(p, a, b, G, tpu);
+    int nt = chunk_tiles(a, rq, rt, tpu, &t0);
+    int h = (int)((start - misc->base) / nt);
+    long long ubase = misc->base + (long long)h * nt, x = start;
+    int n = 0, nu = 0, nq = 0;   // ring entries filled, units begun, query copies issued
+    auto try_wait = [&](uint64_t& br, uint32_t parity) {
+      const bool ok = !stopped && !*abort && mbar_wait_bounded(smem_u32(&br), parity, abort, a.wait_ns);
+      stopped = !__all_sync(0xFFFFFFFFu, ok);
+    };
+    for (;; ++nu) {
+      const int uq = nu % kUnitQueue;
+      try_wait(misc->u_empty[uq], ((nu / kUnitQueue) & 1) ^ 1);
+      if (stopped && (nu > 0 || !a.debug_stall)) break;
+      const bool end = x >= stop;
+      const long long uend = ubase + nt, ue = uend < stop ? uend : stop;
+      const int tile0 = t0 + (int)(x - ubase), ntile = (int)(ue - x);
+      const int i0 = rt * tpu, ntok = rq.nq - i0 < tpu ? rq.nq - i0 : tpu;
+      if (lane == 0) {
+        Unit& u = misc->u[uq];
+        u.end = end;
+        u.q_tok = rq.q0 + i0;
+        u.pos0 = rq.pos0 + i0;
+        u.ntok = ntok;
+        u.klen = rq.klen;
+        const int lo = rq.pos0 + i0 + 1 - a.window;
+        u.vlo = a.window > 0 && lo > 0 ? lo : 0;
+        u.vhi = a.causal ? rq.pos0 + i0 + ntok : rq.klen;
+        u.tile0 = tile0;
+        u.ntile = ntile;
+        u.h = h;
+        u.whole = ubase >= start && uend <= stop;
+        u.part = 2 * blockIdx.x + (ubase < start ? 0 : 1);
+        u.first = (int)(((ubase + 1) * parts - 1) / total);
+        u.last = (int)((uend * parts - 1) / total);
+        mbar_arrive(bar(misc->u_full[uq]));
+      }
+      __syncwarp();
+      if (end) break;
+      const int32_t* tab = p.tables + (size_t)__ldcg(p.rows + b) * p.W;
+      const int hi_u = a.causal ? rq.pos0 + i0 + ntok : rq.klen;   // what the unit's rows see
+      int lo_u = a.window > 0 ? rq.pos0 + i0 + 1 - a.window : 0;
+      lo_u = lo_u > 0 ? lo_u : 0;
+      auto page_of = [&](int t) -> int {
+        const int tok = t * kTile + lane * box_rows;
+        if (lane >= nbox || tok >= hi_u || tok + box_rows <= lo_u) return -2;
+        return __ldcg(tab + (tok >> p.logP));
+      };
+      int page = page_of(tile0);
+      for (int j = 0; j < ntile && !stopped; ++j) {
+        const int tile = tile0 + j;
+        const int ahead = j + 1 < ntile ? page_of(tile + 1) : -2;
+        const unsigned there = __ballot_sync(0xFFFFFFFFu, page != -2);
+        const int row0 = (tile * kTile + lane * box_rows) & (p.P - 1);
+        const bool ok = page >= 0 && page < p.num_pages;
+        if (page != -2 && !ok) atomicOr(reinterpret_cast<unsigned*>(p.state + PST_ERROR), KVRING_PAGES_ERR_TABLE);
+        const int c2 = ok ? (int)((layer0 + page) * p.Hkv + h) : none;
+        for (int kv = 0; kv < 2 && !stopped; ++kv, ++n) {
+          const int s = n % kRing;
+          try_wait(empty[s], ((n / kRing) & 1) ^ 1);
+          if (stopped) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(full[s]), (uint32_t)__popc(there) * kBoxes * box_bytes);
+          __syncwarp();
+          if (page != -2) {
+            const uint32_t dst = sbase + kRingAt + s * kRingSize + lane * box_bytes;
+#pragma unroll
+            for (int c = 0; c < kBoxes; ++c)
+              tma_load_3d(dst + c * L::kAtom, kv ? &tmV : &tmK, c * 64, row0, c2, bar(full[s]));
+          }
+          // the queries behind the unit's first keys: their place is free
+          // once the previous unit's last scores have been computed
+          if (j == 0 && kv == 0) {
+            try_wait(misc->q_empty, (nu & 1) ^ 1);
+            if (stopped) {
+              ++n;
+              break;
+            }
+            if (lane == 0) {
+              const int ng = ntok > TG ? 2 : 1;
+              mbar_arrive_expect_tx(bar(misc->q_full), (uint32_t)(ng * L::kAtoms * TG * G * 128));
+              for (int g = 0; g < ng; ++g)
+#pragma unroll
+                for (int c = 0; c < L::kAtoms; ++c)
+                  tma_load_3d(sbase + L::kQ + g * L::kQGroup + c * L::kAtom, &tmQ, c * 64, h * G,
+                              rq.q0 + i0 + g * TG, bar(misc->q_full));
+            }
+            ++nq;
+            __syncwarp();
+          }
+        }
+        page = ahead;
+      }
+      x = ue;
+      if (x < stop) {
+        ubase = uend;
+        if (++h == p.Hkv) {
+          h = 0;
+          if (++rt >= rq.nrt) {
+            rt = 0;
+            do rq = load_chunk_req(p, a, ++b, G, tpu);
+            while (rq.nrt == 0);
+          }
+          nt = chunk_tiles(a, rq, rt, tpu, &t0);
+        }
+      }
+    }
+    // every copy lands before the CTA may exit
+    volatile int no_abort = 0;
+    for (int i = n - kRing < 0 ? 0 : n - kRing; i < n; ++i)
+      mbar_wait_bounded(bar(full[i % kRing]), (i / kRing) & 1, &no_abort, a.wait_ns);
+    if (nq > 0) mbar_wait_bounded(bar(misc->q_full), (nq - 1) & 1, &no_abort, a.wait_ns);
+  } else if (warp == kWarpIssue) {
+    // --------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_16(128, 128, false, !E4M3), idesc_pv = idesc_16(128, D, true, !E4M3);
+      const uint64_t dq = smem_desc(sbase + L::kQ, 16, 1024, 2u), dk = smem_desc(sbase + L::kKV, 16, 1024, 2u);
+      const uint64_t dv = smem_desc(sbase + L::kKV, (uint32_t)L::kAtom, 1024, 2u);
+      const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
+      const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+      constexpr uint32_t kSlotStep = L::kSlot >> 4, kQStep = L::kQGroup >> 4, kAtomStep = L::kAtom >> 4;
+      int n = 0;
+      int nt_g[2] = {0, 0}, nu_g[2] = {0, 0};   // tiles and units of each group so far
+      auto qk = [&](int g, int slot) {
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ss(tmem + 128 * g, q_lo + g * kQStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), q_hi,
+                     k_lo + slot * kSlotStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), k_hi, idesc_qk, kk != 0);
+        mma_commit(bar(misc->s_full[g]));
+      };
+      for (int nu = 0;; ++nu) {
+        const int uq = nu % kUnitQueue;
+        wait(misc->u_full[uq], (nu / kUnitQueue) & 1);
+        const Unit u = misc->u[uq];
+        if (u.end || *abort) break;
+        const int ng = u.ntok > TG ? 2 : 1;
+        wait(E4M3 ? misc->q_ready : misc->q_full, nu & 1);
+        int ks = n % L::kSlots;
+        wait(misc->ready[ks], (n / L::kSlots) & 1);
+        for (int g = 0; g < ng; ++g) qk(g, ks);
+        mma_commit(bar(misc->empty[ks]));
+        if (u.ntile == 1) mma_commit(bar(misc->q_empty));
+        for (int j = 0; j < u.ntile; ++j) {
+          const int nv = n + 2 * j + 1, vs = nv % L::kSlots, nk = nv + 1;
+          const bool more = j + 1 < u.ntile;
+          ks = nk % L::kSlots;
+          for (int g = 0; g < ng; ++g) {
+            if (g == 0) {
+              wait(misc->ready[vs], (nv / L::kSlots) & 1);
+            }
+            wait(misc->p_full[g], nt_g[g] & 1);
+            if (j == 0) wait(misc->o_free[g], (nu_g[g] & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_f16_ts_w(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, v_lo + vs * kSlotStep + kk * 128, v_hi,
+                           idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            ++nt_g[g];
+            if (!more) {
+              mma_commit(bar(misc->o_full[g]));
+              ++nu_g[g];
+            }
+            if (g == ng - 1) mma_commit(bar(misc->empty[vs]));
+            if (more) {
+              if (g == 0) wait(misc->ready[ks], (nk / L::kSlots) & 1);
+              qk(g, ks);
+              if (g == ng - 1) {
+                mma_commit(bar(misc->empty[ks]));
+                if (j + 2 == u.ntile) mma_commit(bar(misc->q_empty));
+              }
+            }
+          }
+        }
+        n += 2 * u.ntile;
+        mbar_arrive(bar(misc->u_empty[uq]));
+      }
+      // every MMA issued above has finished before TMEM is freed
+      mma_commit(bar(misc->done));
+      volatile int no_abort = 0;
+      mbar_wait_bounded(bar(misc->done), 0, &no_abort, a.wait_ns);
+    }
+    __syncwarp();
+  } else if (warp >= L::kWarpHelp) {
+    // ------------------------------------------------------------ helpers
+    const int ht = threadIdx.x - 32 * L::kWarpHelp;
+    int n = 0;
+    for (int nu = 0;; ++nu) {
+      const int uq = nu % kUnitQueue;
+      wait(misc->u_full[uq], (nu / kUnitQueue) & 1);
+      const Unit u = misc->u[uq];
+      if (__any_sync(0xFFFFFFFFu, u.end || *abort)) break;
+      if constexpr (E4M3) {
+        // E4M3 tile [128 tokens][d] (128- or 64-byte swizzle) to f16 atoms
+        // [128 tokens][64] (128-byte swizzle); task i: token i / CPR, 16
+        // values i % CPR
+        constexpr int CPR = D / 16, PER = kTile * CPR / kHelpThreads;
+        for (int j = 0; j < 2 * u.ntile; ++j, ++n) {
+          const int rs = n % L::kRaws, s = n % L::kSlots;
+          wait(misc->raw_full[rs], (n / L::kRaws) & 1);
+          const uint8_t* src = sm + L::kRawAt + rs * L::kRaw;
+          uint4 w[PER];
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int k = ht + i * kHelpThreads;
+            w[i] = *reinterpret_cast<const uint4*>(src + swz_offset(k / CPR, k % CPR, D));
+          }
+          mbar_arrive(bar(misc->raw_empty[rs]));
+          if (j & 1) {   // values: what no row may read becomes zeros
+            const int t = (u.tile0 + (j >> 1)) * kTile;
+            if (t < u.vlo || t + kTile > u.vhi) {
+#pragma unroll
+              for (int i = 0; i < PER; ++i) {
+                const int tok = t + (ht + i * kHelpThreads) / CPR;
+                if (tok < u.vlo || tok >= u.vhi) w[i] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+          }
+          wait(misc->empty[s], ((n / L::kSlots) & 1) ^ 1);
+          uint8_t* dst = sm + L::kKV + s * L::kSlot;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int k = ht + i * kHelpThreads, row = k / CPR, c = k % CPR;
+            const uint32_t wi[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t hv[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              hv[2 * e] = e4m3x2_to_f16x2((uint16_t)(wi[e] & 0xFFFFu));
+              hv[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(wi[e] >> 16));
+            }
+            uint8_t* atom = dst + (c >> 2) * L::kAtom;
+            *reinterpret_cast<uint4*>(atom + swz_offset(row, 2 * (c & 3), 128)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4*>(atom + swz_offset(row, 2 * (c & 3) + 1, 128)) =
+                make_uint4(hv[4], hv[5], hv[6], hv[7]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(misc->ready[s]));
+        }
+      } else {
+        // every landed tile passes through the helpers, nearly always untouched
+        for (int j = 0; j < 2 * u.ntile; ++j, ++n) {
+          const int s = n % L::kSlots;
+          wait(misc->full[s], (n / L::kSlots) & 1);
+          if ((j & 1) && edge_tile(u, j >> 1)) {
+            uint8_t* v = sm + L::kKV + s * L::kSlot;
+            const int t = (u.tile0 + (j >> 1)) * kTile;
+            for (int k = ht; k < kTile * L::kAtoms * 8; k += kHelpThreads) {
+              const int tok = t + ((k >> 3) & (kTile - 1));
+              if (tok < u.vlo || tok >= u.vhi) *reinterpret_cast<uint4*>(v + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(misc->ready[s]));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(misc->u_empty[uq]));
+    }
+  }
+  } else {
+    if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    // ------------------------------------------------------------ softmax
+    const int g = warp >> 2, row = threadIdx.x & (kTile - 1);
+    const int ri = row / G, head = row % G;            // the row's token in its group, its query head
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = trow + 128 * g, tO = trow + 256 + 128 * g;
+    const float* sc = p.scales + (size_t)a.layer * 4 * p.Hkv;
+    int syncs = 0;
+    auto sync_group = [&]() {
+      mbar_arrive(bar(misc->grp[g]));
+      wait(misc->grp[g], syncs++ & 1);
+      __syncwarp();
+    };
+    int nt_done = 0, nu_done = 0;
+    for (int nu = 0;; ++nu) {
+      const int uq = nu % kUnitQueue;
+      wait(misc->u_full[uq], (nu / kUnitQueue) & 1);
+      const Unit& u = misc->u[uq];
+      if (__any_sync(0xFFFFFFFFu, u.end || *abort)) break;
+      const bool active = g == 0 || u.ntok > TG;
+      const int tok = g * TG + ri;
+      const bool live = ri < TG && tok < u.ntok;
+      float f_row = a.sm_log2;
+      if constexpr (E4M3) {
+        wait(misc->q_full, nu & 1);
+        if (live) {
+          // this row's queries, in place: 8 D/64 chunks of 16 bytes
+          uint8_t* qg = sm + L::kQ + g * L::kQGroup;
+          uint32_t em = 0;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qg + (c >> 3) * L::kAtom + swz_offset(row, c & 7, 128));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) em = max(em, max((ww[e] >> 7) & 0xFFu, (ww[e] >> 23) & 0xFFu));
+          }
+          const bool plain = em == 0 || em >= 254;   // zeros, infinities, NaN: a factor of 1
+          const float down = plain ? 1.0f : __uint_as_float((254u - em) << 23);
+          f_row *= __ldcg(sc + u.h) * (plain ? 1.0f : __uint_as_float(em << 23));
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(qg + (c >> 3) * L::kAtom + swz_offset(row, c & 7, 128));
+            const uint4 w = *at;
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = f32x2_to_f16x2(__uint_as_float(ww[e] << 16) * down, __uint_as_float(ww[e] & 0xFFFF0000u) * down);
+            *at = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(misc->q_ready));
+      }
+      if (active) {
+        // what this row sees, and what every row of the group sees
+        const int pos = u.pos0 + tok;
+        const int hi = live ? (a.causal ? pos + 1 : u.klen) : 0;
+        const int lo = a.window > 0 && pos + 1 - a.window > 0 ? pos + 1 - a.window : 0;
+        const int ntok_g = u.ntok - g * TG < TG ? u.ntok : (g + 1) * TG;
+        const int all_hi = a.causal ? u.pos0 + g * TG + 1 : u.klen;
+        const int all_lo = a.window > 0 ? u.pos0 + ntok_g - a.window : 0;
+        const int ntile = u.ntile;
+        float m_run = -INFINITY, ell = 0.f;
+        for (int j = 0; j < ntile; ++j, ++nt_done) {
+          wait(misc->s_full[g], nt_done & 1);
+          __syncwarp();
+          tc_fence_after();
+          uint32_t sr[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
+          tmem_wait_ld();
+          const int t = (u.tile0 + j) * kTile;
+          if (t + kTile > all_hi || t < all_lo) {
+            const int vh = hi - t, vl = lo - t;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c >= vh || c < vl) sr[c] = __float_as_uint(-INFINITY);
+          }
+          float mx[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
+#pragma unroll
+          for (int i = 1; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mx[k] = fmax3(mx[k], __uint_as_float(sr[16 * i + 2 * k]), __uint_as_float(sr[16 * i + 2 * k + 1]));
+          const float tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
+          const bool need = tmax > m_run + kRaise || (m_run == -INFINITY && tmax > m_run);
+          const float m_new = need ? tmax : m_run;
+          // S(j) complete means PV(j - 1), issued before it, is complete too
+          if (j > 0 && __any_sync(0xFFFFFFFFu, need)) {
+            const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t rr[16];
+              tmem_ld_n<16>(tO + 16 * c, rr);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float2 y = __fmul2_rn(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])),
+                                            make_float2(alpha, alpha));
+                rr[i] = __float_as_uint(y.x);
+                rr[i + 1] = __float_as_uint(y.y);
+              }
+              tmem_st16(tO + 16 * c, rr);
+            }
+            ell *= alpha;
+          }
+          m_run = m_new;
+          const float moff = kShift - (m_run == -INFINITY ? 0.f : m_run);   // nothing seen yet: 2^-inf = 0
+          const float2 fr2 = make_float2(f_row, f_row), mo2 = make_float2(moff, moff);
+          float2 lsum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float2 e[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(sr[32 * c + 2 * i]), __uint_as_float(sr[32 * c + 2 * i + 1])), fr2, mo2);
+              e[i] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            }
+            uint32_t pw[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if constexpr (E4M3) {
+                pw[i] = f32x2_to_f16x2(e[i].x, e[i].y);
+              } else {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(e[i].x, e[i].y);
+                pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+            }
+            tmem_st16(tS + 16 * c, pw);
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+              for (int i = 0; i < w; ++i) e[i] = __fadd2_rn(e[i], e[i + w]);
+            lsum = __fadd2_rn(lsum, e[0]);
+          }
+          ell += lsum.x + lsum.y;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(misc->p_full[g]));
+        }
+        // ------------------------------------------------------- epilogue
+        wait(misc->o_full[g], nu_done & 1);
+        ++nu_done;
+        __syncwarp();
+        tc_fence_after();
+        const float scale_v = E4M3 ? __ldcg(sc + p.Hkv + u.h) : 1.0f;
+        const float inv = ell > 0.f || ell != ell ? scale_v / ell : 0.f;
+        const bool whole = u.whole;
+        uint16_t* o16 = a.out + ((size_t)(u.q_tok + tok) * p.Hq + u.h * G + head) * D;
+        float* o32 = p.part_o + ((size_t)u.part * kPartRows + g * kTile + row) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t rr[32];
+          __syncwarp();
+          tmem_ld32(tO + 32 * c, rr);
+          tmem_wait_ld();
+          if (live && whole) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(rr[8 * k + 2 * e]) * inv,
+                                                                __uint_as_float(rr[8 * k + 2 * e + 1]) * inv);
+                w[e] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(o16 + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(o32 + 32 * c + 4 * k) = make_uint4(rr[4 * k], rr[4 * k + 1], rr[4 * k + 2], rr[4 * k + 3]);
+          }
+        }
+        __syncwarp();
+        tc_fence_before();
+        mbar_arrive(bar(misc->o_free[g]));
+        if (!whole) {
+          if (live)
+            *reinterpret_cast<float2*>(p.part_ml + ((size_t)u.part * kPartRows + g * kTile + row) * 2) =
+                make_float2(m_run, ell);
+          const int first = u.first, last = u.last;
+          __threadfence();
+          sync_group();
+          if (row == 0) {
+            const int old = atomicAdd(p.tickets + 2 * first + g, 1);
+            misc->last[g] = old == last - first;
+            if (misc->last[g]) p.tickets[2 * first + g] = 0;
+          }
+          sync_group();
+          if (misc->last[g]) {
+            __threadfence();
+            const int rows = (u.ntok - g * TG < TG ? u.ntok - g * TG : TG) * G;
+            for (int k = row; k < rows * (D / 4); k += kTile) {
+              const int r = k / (D / 4), d4 = k % (D / 4);
+              auto slot = [&](int cta) { return (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + g * kTile + r; };
+              float m = -INFINITY, l = 0.f;
+              float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int cta = first; cta <= last; ++cta) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(cta) * 2));
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(cta) * D) + d4);
+                const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+                const float wa = ex2_approx(m - mu), wb = ex2_approx(ml.x - mu);
+                l = l * wa + ml.y * wb;
+                o.x = o.x * wa + v.x * wb;
+                o.y = o.y * wa + v.y * wb;
+                o.z = o.z * wa + v.z * wb;
+                o.w = o.w * wa + v.w * wb;
+                m = mn;
+              }
+              const float iv = l > 0.f || l != l ? scale_v / l : 0.f;
+              uint16_t* dst = a.out + ((size_t)(u.q_tok + g * TG + r / G) * p.Hq + u.h * G + r % G) * D + 4 * d4;
+              const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * iv, o.y * iv), b1 = __floats2bfloat162_rn(o.z * iv, o.w * iv);
+              *reinterpret_cast<uint2*>(dst) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(misc->u_empty[uq]));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpIssue) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && *abort)
+    atomicOr(reinterpret_cast<unsigned*>(p.state + PST_ERROR), KVRING_PAGES_ERR_TIMEOUT);
+}
+
+template <int D, bool E4M3>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(k_paged_chunk<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ChunkLayout<D, E4M3>::kBytes);
+}
+template <int D, bool E4M3>
+cudaError_t go(const PagesDev& p, const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
+               const PagedAttn& a, cudaStream_t s) {
+  return launch_pdl(k_paged_chunk<D, E4M3>, dim3((unsigned)a.ctas), dim3(ChunkLayout<D, E4M3>::kThreads),
+                    ChunkLayout<D, E4M3>::kBytes, s, *tmQ, *tmK, *tmV, p, a);
+}
+
+}  // namespace
+
+cudaError_t paged_chunk_prepare() {
+  cudaError_t e = prepare_one<128, true>();
+  if (e == cudaSuccess) e = prepare_one<128, false>();
+  if (e == cudaSuccess) e = prepare_one<64, true>();
+  if (e == cudaSuccess) e = prepare_one<64, false>();
+  return e;
+}
+
+cudaError_t launch_paged_chunk(const PagesDev& p, const CUtensorMap* tmQ, const CUtensorMap* tmK,
+                               const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s) {
+  if (p.D == 128) return p.e4m3 ? go<128, true>(p, tmQ, tmK, tmV, a, s) : go<128, false>(p, tmQ, tmK, tmV, a, s);
+  return p.e4m3 ? go<64, true>(p, tmQ, tmK, tmV, a, s) : go<64, false>(p, tmQ, tmK, tmV, a, s);
+}
+
+}  // namespace kvr

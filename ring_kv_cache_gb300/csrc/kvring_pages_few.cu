@@ -123,7 +123,8 @@ __device__ __forceinline__ Req load_req(const PagesDev& p, const PagedAttn& a, i
   r.nq = (end < a.T ? end : a.T) - r.q0;
   if (r.nq < 0) r.nq = 0;
   r.nrows = r.nq * G;
-  if (r.nrows <= a.min_rows || r.nrows > a.max_rows || r.klen <= 0) r.nrows = 0;
+  const long long all = (long long)(end - r.q0) * G;
+  if (all <= a.min_rows || all > a.max_rows || r.klen <= 0) r.nrows = 0;
   r.nrt = (r.nrows + UR - 1) / UR;
   r.hi = r.klen;
   r.lo = 0;

@@ -14,7 +14,7 @@ struct kvring_pages {
   CUtensorMap tmK, tmV;   // [L * num_pages * Hkv][P][d] in boxes of a page, or 128 rows of one
   int sm_count;
   int device;
-  int max_new;            // the last plan's bound on new tokens per request (picks kernels only)
+  int max_new, requests;  // of the last plan: bound on new tokens per request, requests (they pick kernels only)
   unsigned long long wait_ns;
   int debug_stall;
 };
@@ -23,6 +23,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr unsigned long long kDefaultWaitNs = 1000000000ull;
+constexpr int kFewRows = 64;   // most query rows of a request for the kernel for few rows
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -77,7 +78,7 @@ Plan plan_for(const kvring_pages_config* c) {
   p.table = take(W * c->page_size * D * 4);
   p.part_o = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * D * 4);
   p.part_ml = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * 8);
-  p.tickets = take(kvr::kPagedMaxCtas * 4);
+  p.tickets = take((size_t)2 * kvr::kPagedMaxCtas * 4);
   p.pub.total = off;
   return p;
 }
@@ -104,6 +105,22 @@ bool make_pool_map(CUtensorMap* m, void* base, const kvring_pages_config* c) {
   const CUtensorMapSwizzle sw = e4m3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   return fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Queries [n][Hq][d] with a token stride, in boxes of 64 columns x the query
+// heads of one key/value head x the tokens of a row group (128 rows at most).
+bool make_query_map(CUtensorMap* m, const void* q, int64_t stride, int n, const kvring_pages_config& c) {
+  auto fn = kvr::encode_tiled();
+  if (!fn) return false;
+  const int G = c.num_q_heads / c.num_kv_heads;
+  const cuuint64_t D = (cuuint64_t)c.head_dim;
+  const cuuint64_t dims[3] = {D, (cuuint64_t)c.num_q_heads, (cuuint64_t)n};
+  const cuuint64_t strides[2] = {D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(kvr::kTile / G)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -153,6 +170,7 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   h->device = dev;
   h->sm_count = sms < 1 ? 1 : (sms > kvr::kPagedMaxCtas ? kvr::kPagedMaxCtas : sms);
   h->max_new = cfg->max_tokens;
+  h->requests = cfg->max_requests;
   h->wait_ns = kDefaultWaitNs;
   h->debug_stall = 0;
   uint8_t* b = static_cast<uint8_t*>(dev_buf);
@@ -194,9 +212,10 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   if (!make_pool_map(&h->tmK, d.k, cfg) || !make_pool_map(&h->tmV, d.v, cfg)) st = KVRING_ERR_UNSUPPORTED;
   if (st == KVRING_OK) st = cuda_status(kvr::pages_prepare());
   if (st == KVRING_OK) st = cuda_status(kvr::paged_few_prepare());
+  if (st == KVRING_OK) st = cuda_status(kvr::paged_chunk_prepare());
   // everything but the caches and the workspace's partial rows starts as zeros
   if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(b + p.pub.scales, 0, p.table - p.pub.scales, s));
-  if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(d.tickets, 0, kvr::kPagedMaxCtas * 4, s));
+  if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(d.tickets, 0, 2 * kvr::kPagedMaxCtas * 4, s));
   if (st == KVRING_OK)
     st = recorded(s, [&] {
       const cudaError_t e = kvr::launch_pages_table(d, reinterpret_cast<float*>(b + p.table), theta, s);
@@ -253,7 +272,10 @@ kvring_status kvring_pages_plan(kvring_pages_t* h, const int32_t* rows, const in
   if (max_new > num_tokens) max_new = num_tokens;
   const kvring_status st =
       recorded(s, [&] { return kvr::launch_pages_plan(h->dev, rows, new_tokens, n, num_tokens, max_new, s); });
-  if (st == KVRING_OK) h->max_new = max_new;
+  if (st == KVRING_OK) {
+    h->max_new = max_new;
+    h->requests = n;
+  }
   return st;
 }
 
@@ -327,16 +349,38 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   a.causal = causal;
   a.window = window;
   a.sm_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.0f / sqrtf((float)h->cfg.head_dim));
-  a.min_rows = 0;
-  a.max_rows = INT32_MAX;
   a.ctas = h->sm_count;
-  a.min_tiles = 2;
   a.wait_ns = h->wait_ns;
   a.debug_stall = h->debug_stall;
-  const int64_t rows = (int64_t)h->max_new * (h->cfg.num_q_heads / h->cfg.num_kv_heads);
-  const int unit_rows = rows > 64 ? 64 : (int)rows;
+  // Which kernel takes a request: up to kFewRows query rows (tokens x G) the
+  // one for few rows, beyond that the one for chunks.  One kernel alone when
+  // the plan's bound, or its single request, leaves nothing for the other;
+  // that one then takes every request, whatever the device's lengths are.
+  const int G = h->cfg.num_q_heads / h->cfg.num_kv_heads;
+  const int64_t rows = (int64_t)h->max_new * G;
+  const bool few = rows <= kFewRows || h->requests > 1, chunk = rows > kFewRows;
+  // in a batch with chunks, requests beyond one m = 16 row tile (two or four
+  // for many query heads per key/value head) go with the chunks
+  const int split_rows = G <= 16 ? 16 : (G <= 32 ? 32 : 64);
+  CUtensorMap tmQ;
+  if (chunk && !make_query_map(&tmQ, q, q_stride, n, h->cfg)) return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return recorded(s, [&] { return kvr::launch_paged_few(h->dev, &h->tmK, &h->tmV, a, unit_rows, s); }, out, out_bytes);
+  return recorded(s, [&] {
+    cudaError_t e = cudaSuccess;
+    if (chunk) {
+      a.min_rows = few ? split_rows : 0;
+      a.max_rows = INT32_MAX;
+      a.min_tiles = 4;
+      e = kvr::launch_paged_chunk(h->dev, &tmQ, &h->tmK, &h->tmV, a, s);
+    }
+    if (few && e == cudaSuccess) {
+      a.min_rows = 0;
+      a.max_rows = chunk ? split_rows : INT32_MAX;
+      a.min_tiles = 2;
+      e = kvr::launch_paged_few(h->dev, &h->tmK, &h->tmV, a, chunk ? split_rows : (int)rows, s);
+    }
+    return e;
+  }, out, out_bytes);
 }
 
 kvring_status kvring_pages_debug_set_wait(kvring_pages_t* h, int64_t limit_ns, int32_t stall) {
