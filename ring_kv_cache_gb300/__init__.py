@@ -28,8 +28,6 @@ __all__ = [
     "kvring_export",
     "kvring_status_string", "encode_e4m3", "STATE",
     "KvPages", "KvStep", "PAGES_STATE", "kvring_pages_get_layout", "kvring_pages_create", "kvring_pages_destroy",
-    "kvring_pages_restore", "kvring_pages_set_scales", "kvring_pages_plan", "kvring_pages_commit",
-    "kvring_pages_release", "kvring_pages_write", "kvring_pages_attention",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -537,42 +535,6 @@ def kvring_pages_destroy(handle: int) -> None:
     _check(lib().kvring_pages_destroy(handle), "kvring_pages_destroy")
 
 
-def kvring_pages_restore(handle, lengths, tables, free_pages, n_free, stream_ptr) -> None:
-    _check(lib().kvring_pages_restore(handle, _ptr(lengths), _ptr(tables), _ptr(free_pages), int(n_free), stream_ptr),
-           "kvring_pages_restore")
-
-
-def kvring_pages_set_scales(handle, layer, scale_k, scale_v, stream_ptr) -> None:
-    _check(lib().kvring_pages_set_scales(handle, int(layer), _ptr(scale_k), _ptr(scale_v), stream_ptr),
-           "kvring_pages_set_scales")
-
-
-def kvring_pages_plan(handle, rows, new_tokens, num_requests, num_tokens, max_new, stream_ptr) -> None:
-    _check(lib().kvring_pages_plan(handle, _ptr(rows), _ptr(new_tokens), int(num_requests), int(num_tokens),
-                                   int(max_new), stream_ptr), "kvring_pages_plan")
-
-
-def kvring_pages_commit(handle, stream_ptr) -> None:
-    _check(lib().kvring_pages_commit(handle, stream_ptr), "kvring_pages_commit")
-
-
-def kvring_pages_release(handle, rows, num_requests, stream_ptr) -> None:
-    _check(lib().kvring_pages_release(handle, _ptr(rows), int(num_requests), stream_ptr), "kvring_pages_release")
-
-
-def kvring_pages_write(handle, layer, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, q_out,
-                       num_tokens, stream_ptr) -> None:
-    _check(lib().kvring_pages_write(handle, int(layer), _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride,
-                                    _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(q_out), int(num_tokens),
-                                    stream_ptr), "kvring_pages_write")
-
-
-def kvring_pages_attention(handle, layer, q, q_stride, out, num_tokens, causal, window, scale, stream_ptr) -> None:
-    _check(lib().kvring_pages_attention(handle, int(layer), _ptr(q), q_stride, _ptr(out), int(num_tokens),
-                                        int(bool(causal)), int(window), float(scale), stream_ptr),
-           "kvring_pages_attention")
-
-
 # What a plan made, as views of the cache's own buffer (valid until the next
 # plan): cu [requests + 1], lengths [requests] with the new tokens, positions
 # and slots [num_tokens] (slot -1: padding).
@@ -628,15 +590,26 @@ class KvPages:
         self.state = self._ints(lay.state, PAGES_STATE_WORDS)
         self._cu, self._klen = self._ints(lay.step_cu, self.R + 1), self._ints(lay.step_lengths, self.R)
         self._pos, self._slots = self._ints(lay.positions, self.max_tokens), self._ints(lay.slots, self.max_tokens)
-        self._steps = {}
+        self._steps, self._caches, self._index = {}, {}, self.device.index
 
     def _ints(self, off: int, n: int) -> torch.Tensor:
         return self.buf[off:off + 4 * n].view(torch.int32)
 
-    def _s(self, stream) -> int:
-        return _stream_ptr(stream, self.device)
+    def _call(self, f, what: str, stream, *args) -> None:
+        """A library call on the object's device and the given (or its current) stream."""
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
+        if torch.cuda.current_device() == self._index:
+            _check(f(self.handle, *args, s), what)
+        else:
+            with torch.cuda.device(self.device):
+                _check(f(self.handle, *args, s), what)
 
     def _cache(self, off: int, layer: int) -> torch.Tensor:
+        if (off, layer) not in self._caches:
+            self._caches[off, layer] = self._cache_view(off, layer)
+        return self._caches[off, layer]
+
+    def _cache_view(self, off: int, layer: int) -> torch.Tensor:
         if not 0 <= layer < self.L:
             raise ValueError(f"layer must be in [0, {self.L})")
         shape = (self.num_pages, self.Hkv, self.P, self.d)
@@ -667,8 +640,8 @@ class KvPages:
         n = self._int_arg(free_pages, "free_pages").numel()
         if n > self.num_pages:
             raise ValueError(f"free_pages holds {n} pages, the cache {self.num_pages}")
-        with torch.cuda.device(self.device):
-            kvring_pages_restore(self.handle, lengths, tables, free_pages if n else None, n, self._s(stream))
+        self._call(_LIB.kvring_pages_restore, "kvring_pages_restore", stream, lengths.data_ptr(), tables.data_ptr(),
+                   free_pages.data_ptr() if n else None, n)
 
     def set_scales(self, layer: int, scale_k, scale_v, stream=None) -> None:
         """Per-head scales (float32 [Hkv]) of one layer of an E4M3 cache."""
@@ -676,8 +649,8 @@ class KvPages:
             if not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype != torch.float32 \
                     or tuple(t.shape) != (self.Hkv,) or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 tensor [{self.Hkv}] on {self.device}")
-        with torch.cuda.device(self.device):
-            kvring_pages_set_scales(self.handle, layer, scale_k, scale_v, self._s(stream))
+        self._call(_LIB.kvring_pages_set_scales, "kvring_pages_set_scales", stream, int(layer), scale_k.data_ptr(),
+                   scale_v.data_ptr())
 
     def plan(self, new_tokens, num_tokens: int, rows=None, max_new: int | None = None, stream=None) -> KvStep:
         """Plan a step: request i (row ``rows[i]``, or row i) gets
@@ -687,9 +660,8 @@ class KvPages:
         n = self._int_arg(new_tokens, "new_tokens").numel()
         if rows is not None:
             self._int_arg(rows, "rows", (n,))
-        with torch.cuda.device(self.device):
-            kvring_pages_plan(self.handle, rows, new_tokens, n, num_tokens, num_tokens if max_new is None else max_new,
-                              self._s(stream))
+        self._call(_LIB.kvring_pages_plan, "kvring_pages_plan", stream, _ptr(rows), new_tokens.data_ptr(), n, num_tokens,
+                   num_tokens if max_new is None else max_new)
         step = self._steps.get((n, num_tokens))
         if step is None:
             if len(self._steps) >= 256:
@@ -700,29 +672,33 @@ class KvPages:
 
     def commit(self, stream=None) -> None:
         """Make the last plan final: the lengths and the free list."""
-        with torch.cuda.device(self.device):
-            kvring_pages_commit(self.handle, self._s(stream))
+        self._call(_LIB.kvring_pages_commit, "kvring_pages_commit", stream)
 
     def release(self, rows, stream=None) -> None:
         """End the requests in ``rows`` (int32): their pages become free."""
         n = self._int_arg(rows, "rows").numel()
-        with torch.cuda.device(self.device):
-            kvring_pages_release(self.handle, rows, n, self._s(stream))
+        self._call(_LIB.kvring_pages_release, "kvring_pages_release", stream, rows.data_ptr(), n)
 
-    def _heads(self, x, heads: int, name: str) -> int:
+    def _heads(self, x, heads: int, name: str):
         """Check bf16 [n, heads, d] with whole rows of heads (a slice of a
-        packed projection output is one); returns n."""
-        if not isinstance(x, torch.Tensor) or x.device != self.device or x.dtype != torch.bfloat16:
+        packed projection output is one); returns n and the token stride."""
+        if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.device != self.device:
             raise ValueError(f"{name} must be a bfloat16 tensor on {self.device}")
-        if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != self.d:
-            raise ValueError(f"{name} must have shape [n, {heads}, {self.d}], got {tuple(x.shape)}")
-        if x.stride(2) != 1 or (heads > 1 and x.stride(1) != self.d) \
-                or (x.shape[0] > 1 and x.stride(0) < heads * self.d):
+        shape, row = x.shape, heads * self.d
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.d:
+            raise ValueError(f"{name} must have shape [n, {heads}, {self.d}], got {tuple(shape)}")
+        n = shape[0]
+        st, sh, s1 = x.stride()
+        if s1 != 1 or (heads > 1 and sh != self.d) or (n > 1 and st < row):
             raise ValueError(f"{name}: the heads of a token must be contiguous, and tokens must not overlap")
-        return x.shape[0]
+        return n, st if n > 1 else row
 
-    def _stride(self, x, heads: int) -> int:
-        return x.stride(0) if x.shape[0] > 1 else heads * self.d
+    def _result(self, x, n: int, name: str):
+        if x is None:
+            return torch.empty((n, self.Hq, self.d), dtype=torch.bfloat16, device=self.device)
+        if self._heads(x, self.Hq, name) != (n, self.Hq * self.d):
+            raise ValueError(f"{name} must be contiguous, [{n}, {self.Hq}, {self.d}]")
+        return x
 
     def write(self, layer: int, q, k, v, q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None,
               stream=None) -> torch.Tensor:
@@ -730,21 +706,18 @@ class KvPages:
         the planned tokens' keys and values; returns the rotated queries
         (bf16 [n, Hq, d]).  Rows of ``q_out`` past the plan's tokens are left
         as they were (undefined in a new tensor)."""
-        n = self._heads(q, self.Hq, "q")
-        if self._heads(k, self.Hkv, "k") != n or self._heads(v, self.Hkv, "v") != n:
+        n, qs = self._heads(q, self.Hq, "q")
+        nk, ks = self._heads(k, self.Hkv, "k")
+        nv, vs = self._heads(v, self.Hkv, "v")
+        if nk != n or nv != n:
             raise ValueError("q, k and v must hold the same number of tokens")
         for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-            if t is not None and (not isinstance(t, torch.Tensor) or t.device != self.device
-                                  or t.dtype != torch.bfloat16 or tuple(t.shape) != (self.d,)
-                                  or not t.is_contiguous()):
+            if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16
+                                  or t.device != self.device or t.shape != (self.d,) or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{self.d}] on {self.device}")
-        if q_out is None:
-            q_out = torch.empty((n, self.Hq, self.d), dtype=torch.bfloat16, device=self.device)
-        elif self._heads(q_out, self.Hq, "q_out") != n or not q_out.is_contiguous():
-            raise ValueError(f"q_out must be contiguous, [{n}, {self.Hq}, {self.d}]")
-        with torch.cuda.device(self.device):
-            kvring_pages_write(self.handle, layer, q, k, v, self._stride(q, self.Hq), self._stride(k, self.Hkv),
-                               self._stride(v, self.Hkv), q_norm, k_norm, eps, q_out, n, self._s(stream))
+        q_out = self._result(q_out, n, "q_out")
+        self._call(_LIB.kvring_pages_write, "kvring_pages_write", stream, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                   qs, ks, vs, _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr(), n)
         return q_out
 
     def attention(self, layer: int, q, out=None, causal: bool = True, window: int = 0, scale: float = 0.0,
@@ -754,14 +727,10 @@ class KvPages:
         limits a causal query to its last ``window`` tokens; ``scale`` 0 means
         1/sqrt(d).  Rows of ``out`` past the plan's tokens are left as they
         were (undefined in a new tensor)."""
-        n = self._heads(q, self.Hq, "q")
-        if out is None:
-            out = torch.empty((n, self.Hq, self.d), dtype=torch.bfloat16, device=self.device)
-        elif self._heads(out, self.Hq, "out") != n or not out.is_contiguous():
-            raise ValueError(f"out must be contiguous, [{n}, {self.Hq}, {self.d}]")
-        with torch.cuda.device(self.device):
-            kvring_pages_attention(self.handle, layer, q, self._stride(q, self.Hq), out, n, causal, window, scale,
-                                   self._s(stream))
+        n, qs = self._heads(q, self.Hq, "q")
+        out = self._result(out, n, "out")
+        self._call(_LIB.kvring_pages_attention, "kvring_pages_attention", stream, layer, q.data_ptr(), qs, out.data_ptr(),
+                   n, 1 if causal else 0, window, scale)
         return out
 
     def set_wait(self, limit_ns: int = 1_000_000_000, stall: bool = False) -> None:

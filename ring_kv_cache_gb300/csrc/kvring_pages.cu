@@ -327,34 +327,30 @@ __global__ void k_pages_table(float* table, const Thetas th, int half, size_t n)
 // shuffle reduction; a lane's values are four whole rotation pairs in either
 // pairing (adjacent: one 16-byte chunk; halves: 8 bytes of each half), so the
 // rotation needs no exchange and both pairings read the same 32 bytes of the
-// cos/sin row.  A block takes the tokens of one warp (2 or 4) and its eight
-// warps walk the heads, so that row is read once per warp and kept in
-// registers for all heads; four heads' loads are in flight at a time.
+// cos/sin row.  Norm weight and rotation make one 2 x 2 matrix per pair,
+// r (x0 w0 c - x1 w1 s, x0 w0 s + x1 w1 c), formed once per token for the
+// queries and once for the keys and kept for all heads: with the weights
+// applied separately the kernel was bound by issuing instructions (153 per
+// warp and head row).  A block takes the tokens of one warp (2 or 4) and its
+// eight warps walk the heads; loads of a batch of heads go out together,
+// those of the first batch and of the first key and value before anything
+// else is known.
 constexpr int kWriteWarps = 8;
-constexpr int kWriteBatch = 4;
+constexpr int kWriteBatch = 2;
 
 template <int D, bool E4M3, bool HALVES>
-__global__ void __launch_bounds__(kWriteWarps * 32)
+__global__ void __launch_bounds__(kWriteWarps * 32, 4)
     k_pages_write(const PagesDev p, const PagesWrite w) {
   constexpr int LPR = D / 8, TPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LPR;
+  const int lane = threadIdx.x & 31, c = lane % LPR;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);   // (uniform, and known to be)
   const int t = blockIdx.x * TPW + lane / LPR;
   const int e0 = HALVES ? 4 * c : 8 * c;            // the lane's first 4 values
   const int e1 = HALVES ? D / 2 + 4 * c : 8 * c + 4;
-  const int Htot = p.Hq + 2 * p.Hkv;
-  griddep_wait();
-  griddep_launch_dependents();
-  int tokens = __ldcg(p.state + PST_TOKENS);
-  tokens = tokens < w.T ? tokens : w.T;
-  if (blockIdx.x * TPW >= tokens) return;
-  const bool valid = t < tokens;
-  const int slot = valid ? __ldcg(p.slots + t) : -1;
-  const int pos = valid ? __ldcg(p.pos + t) : 0;
-  const float4 cs0 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c));
-  const float4 cs1 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c + 4));
-  const float cc[4] = {cs0.x, cs0.z, cs1.x, cs1.z}, ss[4] = {cs0.y, cs0.w, cs1.y, cs1.w};
-  auto widen = [](uint2 a, uint2 b, float (&x)[8]) {
-    const uint32_t u[4] = {a.x, a.y, b.x, b.y};
+  const bool mine = t < w.T;
+  const int gw = blockIdx.y * kWriteWarps + warp, step = kWriteWarps * gridDim.y;
+  auto widen = [](uint4 v, float (&x)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(u[i] << 16);
@@ -363,97 +359,145 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
   };
   // (past L1: the rows may have been written by a kernel that still ran when
   // this one started)
-  auto load = [&](const uint16_t* row, uint2& a, uint2& b) {
+  auto load = [&](const uint16_t* row) -> uint4 {
     if constexpr (HALVES) {
-      a = __ldcg(reinterpret_cast<const uint2*>(row + e0));
-      b = __ldcg(reinterpret_cast<const uint2*>(row + e1));
+      const uint2 a = __ldcg(reinterpret_cast<const uint2*>(row + e0));
+      const uint2 b = __ldcg(reinterpret_cast<const uint2*>(row + e1));
+      return make_uint4(a.x, a.y, b.x, b.y);
     } else {
-      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(row + e0));
-      a = make_uint2(v.x, v.y);
-      b = make_uint2(v.z, v.w);
+      return __ldcg(reinterpret_cast<const uint4*>(row + e0));
     }
   };
+  const uint16_t* q = w.q + (mine ? (long long)t * w.q_stride : 0);
+  const uint16_t* k = w.k + (mine ? (long long)t * w.k_stride : 0);
+  const uint16_t* v = w.v + (mine ? (long long)t * w.v_stride : 0);
   const float* inv = p.scales + ((size_t)w.layer * 4 + 2) * p.Hkv;
-  const size_t layer0 = (size_t)w.layer * p.num_pages * p.Hkv;
-  const int page = slot >> p.logP, off = slot & (p.P - 1);
-  const int step = kWriteWarps * gridDim.y;
-  for (int h0 = blockIdx.y * kWriteWarps + warp; h0 < Htot; h0 += kWriteBatch * step) {
-    uint2 ra[kWriteBatch], rb[kWriteBatch];
+  uint4 raw[kWriteBatch], kraw, vraw;
+  float inv_k = 1.0f, inv_v = 1.0f;
+  auto load_q = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < kWriteBatch; ++i) {
-      const int h = h0 + i * step;
-      ra[i] = rb[i] = make_uint2(0u, 0u);
-      if (h < Htot && valid) {
-        const uint16_t* row = h < p.Hq            ? w.q + (long long)t * w.q_stride + (size_t)h * D
-                              : h < p.Hq + p.Hkv ? w.k + (long long)t * w.k_stride + (size_t)(h - p.Hq) * D
-                                                 : w.v + (long long)t * w.v_stride + (size_t)(h - p.Hq - p.Hkv) * D;
-        load(row, ra[i], rb[i]);
-      }
+    for (int i = 0; i < kWriteBatch; ++i)
+      if (h0 + i * step < p.Hq) raw[i] = load(q + (h0 + i * step) * D);
+  };
+  auto load_kv = [&](int h) {
+    kraw = load(k + h * D);
+    vraw = load(v + h * D);
+    if constexpr (E4M3) {
+      inv_k = __ldcg(inv + h);
+      inv_v = __ldcg(inv + p.Hkv + h);
+    }
+  };
+  griddep_wait();
+  griddep_launch_dependents();
+  // Everything that depends on nothing else is asked for at once; only the
+  // cos/sin row waits, for the position.  Key/value heads are dealt out from
+  // the other end, so that warps without a query head take them first.
+  const int hk0 = step - 1 - gw;
+  load_q(gw);
+  if (hk0 < p.Hkv) load_kv(hk0);
+  int tokens = __ldcg(p.state + PST_TOKENS);
+  int slot = mine ? __ldcg(p.slots + t) : -1;
+  int pos = mine ? __ldcg(p.pos + t) : 0;
+  const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // bf16 ones
+  const uint4 gq = w.qw ? load(w.qw) : one, gk = w.kw ? load(w.kw) : one;
+  tokens = tokens < w.T ? tokens : w.T;
+  if (blockIdx.x * TPW >= tokens) return;
+  const bool valid = t < tokens;
+  if (!valid) {
+    slot = -1;
+    pos = 0;
+  }
+  const float4 cs0 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c));
+  const float4 cs1 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c + 4));
+  // pair e: values lo(e), hi(e) of the lane's eight
+  auto lo = [](int e) { return HALVES ? e : 2 * e; };
+  auto hi = [](int e) { return HALVES ? 4 + e : 2 * e + 1; };
+  float m[4][4];
+  auto matrix = [&](uint4 g4) {
+    float g[8];
+    widen(g4, g);
+    const float cc[4] = {cs0.x, cs0.z, cs1.x, cs1.z}, ss[4] = {cs0.y, cs0.w, cs1.y, cs1.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m[e][0] = g[lo(e)] * cc[e];
+      m[e][1] = -g[hi(e)] * ss[e];
+      m[e][2] = g[lo(e)] * ss[e];
+      m[e][3] = g[hi(e)] * cc[e];
+    }
+  };
+  auto turn = [&](uint4 r4, bool norm, float (&x)[8]) {
+    widen(r4, x);
+    float r = 1.0f;
+    if (norm) {
+      float sq = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+      r = rsqrtf(sq * (1.0f / D) + w.eps);
     }
 #pragma unroll
-    for (int i = 0; i < kWriteBatch; ++i) {
-      const int h = h0 + i * step;
-      if (h >= Htot) break;   // (the same for the whole warp)
-      const int kind = h < p.Hq ? 0 : (h < p.Hq + p.Hkv ? 1 : 2);
-      float x[8];
-      widen(ra[i], rb[i], x);
-      const uint16_t* nw = kind == 0 ? w.qw : (kind == 1 ? w.kw : nullptr);
-      if (nw) {
-        float sq = 0.f;
+    for (int e = 0; e < 4; ++e) {
+      const float a = x[lo(e)] * r, b = x[hi(e)] * r;   // (scaled first: huge rows stay finite)
+      x[lo(e)] = a * m[e][0] + b * m[e][1];
+      x[hi(e)] = a * m[e][2] + b * m[e][3];
+    }
+  };
+  auto store_bf16 = [&](uint16_t* dst, const float (&x)[8]) {
+    uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-        const float r = rsqrtf(sq * (1.0f / D) + w.eps);
-        uint2 wa, wb;
-        float g[8];
-        load(nw, wa, wb);
-        widen(wa, wb, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= r * g[e];
-      }
-      if (kind != 2) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i0 = HALVES ? e : 2 * e, i1 = HALVES ? 4 + e : 2 * e + 1;
-          const float a = x[i0], b = x[i1];
-          x[i0] = a * cc[e] - b * ss[e];
-          x[i1] = a * ss[e] + b * cc[e];
-        }
-      }
-      if (!valid) continue;
-      const bool to_cache = kind != 0;
-      if (to_cache && slot < 0) continue;
-      const int hk = h - (kind == 1 ? p.Hq : p.Hq + p.Hkv);
-      const size_t row = to_cache ? ((layer0 + (size_t)page * p.Hkv + hk) << p.logP) + off : 0;
-      if (E4M3 && to_cache) {
-        const float s = __ldcg(inv + (kind == 1 ? 0 : p.Hkv) + hk);
-        uint32_t lo = f32x2_to_e4m3x2(x[0] * s, x[1] * s) | ((uint32_t)f32x2_to_e4m3x2(x[2] * s, x[3] * s) << 16);
-        uint32_t hi = f32x2_to_e4m3x2(x[4] * s, x[5] * s) | ((uint32_t)f32x2_to_e4m3x2(x[6] * s, x[7] * s) << 16);
-        uint8_t* dst = (kind == 1 ? p.k : p.v) + row * D;
-        if constexpr (HALVES) {
-          *reinterpret_cast<uint32_t*>(dst + e0) = lo;
-          *reinterpret_cast<uint32_t*>(dst + e1) = hi;
-        } else {
-          *reinterpret_cast<uint2*>(dst + e0) = make_uint2(lo, hi);
-        }
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      o[e] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    if constexpr (HALVES) {
+      *reinterpret_cast<uint2*>(dst + e0) = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint2*>(dst + e1) = make_uint2(o[2], o[3]);
+    } else {
+      *reinterpret_cast<uint4*>(dst + e0) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  };
+  auto store_cache = [&](uint8_t* cache, size_t row, const float (&x)[8], float s) {
+    if constexpr (E4M3) {
+      const uint32_t a = f32x2_to_e4m3x2(x[0] * s, x[1] * s) | ((uint32_t)f32x2_to_e4m3x2(x[2] * s, x[3] * s) << 16);
+      const uint32_t b = f32x2_to_e4m3x2(x[4] * s, x[5] * s) | ((uint32_t)f32x2_to_e4m3x2(x[6] * s, x[7] * s) << 16);
+      uint8_t* dst = cache + row * D;
+      if constexpr (HALVES) {
+        *reinterpret_cast<uint32_t*>(dst + e0) = a;
+        *reinterpret_cast<uint32_t*>(dst + e1) = b;
       } else {
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-          o[e] = *reinterpret_cast<const uint32_t*>(&b2);
-        }
-        uint16_t* dst = to_cache ? reinterpret_cast<uint16_t*>(kind == 1 ? p.k : p.v) + row * D
-                                 : w.q_out + ((size_t)t * p.Hq + h) * D;
-        if constexpr (HALVES) {
-          *reinterpret_cast<uint2*>(dst + e0) = make_uint2(o[0], o[1]);
-          *reinterpret_cast<uint2*>(dst + e1) = make_uint2(o[2], o[3]);
-        } else {
-          *reinterpret_cast<uint4*>(dst + e0) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        *reinterpret_cast<uint2*>(dst + e0) = make_uint2(a, b);
       }
+    } else {
+      store_bf16(reinterpret_cast<uint16_t*>(cache) + row * D, x);
     }
+  };
+  matrix(gq);
+  uint16_t* q_out = w.q_out + (size_t)t * p.Hq * D;
+  for (int h0 = gw; h0 < p.Hq; h0 += kWriteBatch * step) {
+    if (h0 != gw) load_q(h0);
+#pragma unroll
+    for (int i = 0; i < kWriteBatch; ++i) {
+      const int h = h0 + i * step;
+      if (h >= p.Hq) break;   // (the same for the whole warp)
+      float x[8];
+      turn(raw[i], w.qw != nullptr, x);
+      if (valid) store_bf16(q_out + h * D, x);
+    }
+  }
+  if (hk0 >= p.Hkv) return;
+  matrix(gk);
+  // row of (page, head 0, offset) in the layer's caches; heads are P rows apart
+  const size_t row0 =
+      (((size_t)w.layer * p.num_pages + (slot >> p.logP)) * p.Hkv << p.logP) + (slot & (p.P - 1));
+  for (int h = hk0; h < p.Hkv; h += step) {
+    if (h != hk0) load_kv(h);
+    float x[8];
+    turn(kraw, w.kw != nullptr, x);
+    const size_t row = row0 + ((size_t)h << p.logP);
+    if (slot >= 0) store_cache(p.k, row, x, inv_k);
+    widen(vraw, x);
+    if (slot >= 0) store_cache(p.v, row, x, inv_v);
   }
 }
 
@@ -503,8 +547,9 @@ cudaError_t launch_pages_release(const PagesDev& p, const int32_t* rows, int B, 
 cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_count, cudaStream_t s) {
   const int tpw = 32 / (p.D / 8), blocks = (w.T + tpw - 1) / tpw;
   const int htot = p.Hq + 2 * p.Hkv, most = (htot + kWriteWarps - 1) / kWriteWarps;
-  // few tokens: split the heads over blocks too, until every SM has a block
-  int split = (sm_count + blocks - 1) / blocks;
+  // few tokens: split the heads over blocks too, until every SM has the four
+  // blocks that it holds
+  int split = (4 * sm_count + blocks - 1) / blocks;
   split = split < 1 ? 1 : (split > most ? most : split);
   const dim3 grid((unsigned)blocks, (unsigned)split), block(kWriteWarps * 32);
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, s, p, w); };

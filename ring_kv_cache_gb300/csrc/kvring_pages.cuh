@@ -34,7 +34,7 @@ struct PagesDev {
   int32_t* pos;           // [max_tokens]
   int32_t* slots;         // [max_tokens]
   const float* table;     // [W * P][D/2][2] fp32 (cos, sin)
-  float* part_o;          // [2 * kPagedMaxCtas][kPartRows][D] attention partials
+  float* part_o;          // [2 * kPagedMaxCtas][kPartRows x D] attention partials, laid out by the kernel
   float* part_ml;         // [2 * kPagedMaxCtas][kPartRows][2] their running maxima and sums
   int32_t* tickets;       // [2 * kPagedMaxCtas] arrivals per split unit (0 between calls)
   int Hq, Hkv, D, L, P, logP, num_pages, R, W, max_tokens;

@@ -47,6 +47,10 @@ namespace {
 
 constexpr int kWarpCopy = 8, kWarpIssue = 9;
 constexpr int kUnitQueue = 4;
+// A unit's start and end cost about as much as this many of its tiles (its
+// queries' way to the tensor cores, the last probabilities' and the results'
+// way out); ranges are cut by tiles plus this.
+constexpr int kUnitCost = 3;
 constexpr float kRaise = 8.0f;    // log2 units
 constexpr float kShift = 7.0f;
 constexpr int kChunkSmem = 232448;
@@ -63,8 +67,8 @@ struct ChunkLayout {
   static constexpr int kQGroup = kAtoms * kAtom;
   static constexpr int kSlot = kAtoms * kAtom;                   // one 16-bit K or V tile
   static constexpr int kRaw = E4M3 ? kTile * D : 0;              // one E4M3 tile
-  static constexpr int kSlots = D == 128 ? (E4M3 ? 4 : 5) : (E4M3 ? 8 : 11);
-  static constexpr int kRaws = E4M3 ? (D == 128 ? 2 : 6) : 0;
+  static constexpr int kSlots = D == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 8 : 11);
+  static constexpr int kRaws = E4M3 ? (D == 128 ? 4 : 6) : 0;
   static constexpr int kQ = 0;
   static constexpr int kKV = 2 * kQGroup;
   static constexpr int kRawAt = kKV + kSlots * kSlot;
@@ -146,6 +150,29 @@ __host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool b_mn_major, b
   return idesc_f16(M, N, b_mn_major) | (bf16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
+// 32 fp32 values to bf16 in a row of the output: whole 32-byte sectors where
+// the output is aligned for them.
+__device__ __forceinline__ void store_row32(uint16_t* dst, const float (&x)[32], bool out32) {
+  uint32_t w[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&b2);
+  }
+  if (out32) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * k), "r"(w[8 * k]),
+                   "r"(w[8 * k + 1]), "r"(w[8 * k + 2]), "r"(w[8 * k + 3]), "r"(w[8 * k + 4]), "r"(w[8 * k + 5]),
+                   "r"(w[8 * k + 6]), "r"(w[8 * k + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+  }
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -206,7 +233,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     int t0;
     for (int i = i0; i < i1; ++i) {
       const ChunkReq r = load_chunk_req(p, a, i, G, tpu);
-      for (int rt = 0; rt < r.nrt; ++rt) mine += (unsigned)chunk_tiles(a, r, rt, tpu, &t0);
+      for (int rt = 0; rt < r.nrt; ++rt) mine += (unsigned)(kUnitCost + chunk_tiles(a, r, rt, tpu, &t0));
     }
     unsigned long long x = mine;
 #pragma unroll
@@ -232,7 +259,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       for (int i = i0; i < i1 && !found; ++i) {
         const ChunkReq r = load_chunk_req(p, a, i, G, tpu);
         for (int rt = 0; rt < r.nrt; ++rt) {
-          const unsigned long long n = (unsigned long long)chunk_tiles(a, r, rt, tpu, &t0) * (unsigned)p.Hkv;
+          const unsigned long long n = (unsigned long long)(kUnitCost + chunk_tiles(a, r, rt, tpu, &t0)) * (unsigned)p.Hkv;
           if (start < before + n) {
             misc->b0 = i;
             misc->rt0 = rt;
@@ -289,21 +316,24 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     int b = misc->b0, rt = misc->rt0, t0;
     ChunkReq rq = load_chunk_req(p, a, b, G, tpu);
     int nt = chunk_tiles(a, rq, rt, tpu, &t0);
-    int h = (int)((start - misc->base) / nt);
-    long long ubase = misc->base + (long long)h * nt, x = start;
+    int h = (int)((start - misc->base) / (nt + kUnitCost));
+    long long ubase = misc->base + (long long)h * (nt + kUnitCost), x = start;   // x: next place of the range
     int n = 0, nu = 0, nq = 0;   // ring entries filled, units begun, query copies issued
     auto try_wait = [&](uint64_t& br, uint32_t parity) {
       const bool ok = !stopped && !*abort && mbar_wait_bounded(smem_u32(&br), parity, abort, a.wait_ns);
       stopped = !__all_sync(0xFFFFFFFFu, ok);
     };
-    for (;; ++nu) {
+    for (;;) {
+      // the unit's tiles lie at [t_at, uend) of the flattened space
+      const long long t_at = ubase + kUnitCost, uend = t_at + nt;
+      const bool end = x >= stop;
+      const long long from = x > t_at ? x : t_at, ue = uend < stop ? uend : stop;
+      const int tile0 = t0 + (int)(from - t_at), ntile = (int)(ue - from);
+      const int i0 = rt * tpu, ntok = rq.nq - i0 < tpu ? rq.nq - i0 : tpu;
+      if (end || ntile > 0) {
       const int uq = nu % kUnitQueue;
       try_wait(misc->u_empty[uq], ((nu / kUnitQueue) & 1) ^ 1);
       if (stopped && (nu > 0 || !a.debug_stall)) break;
-      const bool end = x >= stop;
-      const long long uend = ubase + nt, ue = uend < stop ? uend : stop;
-      const int tile0 = t0 + (int)(x - ubase), ntile = (int)(ue - x);
-      const int i0 = rt * tpu, ntok = rq.nq - i0 < tpu ? rq.nq - i0 : tpu;
       if (lane == 0) {
         Unit& u = misc->u[uq];
         u.end = end;
@@ -317,10 +347,12 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         u.tile0 = tile0;
         u.ntile = ntile;
         u.h = h;
-        u.whole = ubase >= start && uend <= stop;
-        u.part = 2 * blockIdx.x + (ubase < start ? 0 : 1);
-        u.first = (int)(((ubase + 1) * parts - 1) / total);
+        u.whole = ntile == nt;
+        // the CTAs whose ranges hold a tile of this unit (the owner of place x
+        // is the last CTA whose range starts at or before x)
+        u.first = (int)(((t_at + 1) * parts - 1) / total);
         u.last = (int)((uend * parts - 1) / total);
+        u.part = 2 * blockIdx.x + (u.first == (int)blockIdx.x ? 1 : 0);
         mbar_arrive(bar(misc->u_full[uq]));
       }
       __syncwarp();
@@ -377,6 +409,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           }
         }
         page = ahead;
+      }
+      ++nu;
       }
       x = ue;
       if (x < stop) {
@@ -560,6 +594,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       __syncwarp();
     };
     int nt_done = 0, nu_done = 0;
+    const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // 32-byte stores
     for (int nu = 0;; ++nu) {
       const int uq = nu % kUnitQueue;
       wait(misc->u_full[uq], (nu / kUnitQueue) & 1);
@@ -699,37 +734,32 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         const float inv = ell > 0.f || ell != ell ? scale_v / ell : 0.f;
         const bool whole = u.whole;
         uint16_t* o16 = a.out + ((size_t)(u.q_tok + tok) * p.Hq + u.h * G + head) * D;
-        float* o32 = p.part_o + ((size_t)u.part * kPartRows + g * kTile + row) * D;
+        // partial rows lie column group by column group, [D/4][128 rows] of
+        // four floats, so that a warp writes and reads whole lines
+        float4* o32 = reinterpret_cast<float4*>(p.part_o + ((size_t)u.part * kPartRows + g * kTile) * D) + row;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t rr[32];
           __syncwarp();
           tmem_ld32(tO + 32 * c, rr);
           tmem_wait_ld();
-          if (live && whole) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(rr[8 * k + 2 * e]) * inv,
-                                                                __uint_as_float(rr[8 * k + 2 * e + 1]) * inv);
-                w[e] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-              *reinterpret_cast<uint4*>(o16 + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (live) {
+          if (!whole) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(o32 + 32 * c + 4 * k) = make_uint4(rr[4 * k], rr[4 * k + 1], rr[4 * k + 2], rr[4 * k + 3]);
+              o32[(8 * c + k) * kTile] = make_float4(__uint_as_float(rr[4 * k]), __uint_as_float(rr[4 * k + 1]),
+                                                     __uint_as_float(rr[4 * k + 2]), __uint_as_float(rr[4 * k + 3]));
+          } else if (live) {
+            float x[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(rr[k]) * inv;
+            store_row32(o16 + 32 * c, x, out32);
           }
         }
         __syncwarp();
         tc_fence_before();
         mbar_arrive(bar(misc->o_free[g]));
         if (!whole) {
-          if (live)
-            *reinterpret_cast<float2*>(p.part_ml + ((size_t)u.part * kPartRows + g * kTile + row) * 2) =
+          *reinterpret_cast<float2*>(p.part_ml + ((size_t)u.part * kPartRows + g * kTile + row) * 2) =
                 make_float2(m_run, ell);
           const int first = u.first, last = u.last;
           __threadfence();
@@ -742,29 +772,42 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           sync_group();
           if (misc->last[g]) {
             __threadfence();
-            const int rows = (u.ntok - g * TG < TG ? u.ntok - g * TG : TG) * G;
-            for (int k = row; k < rows * (D / 4); k += kTile) {
-              const int r = k / (D / 4), d4 = k % (D / 4);
-              auto slot = [&](int cta) { return (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + g * kTile + r; };
-              float m = -INFINITY, l = 0.f;
-              float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            // thread = row again: the parts' weights, then 32 columns at a time
+            float m = -INFINITY, l = 0.f;
+            auto ml_of = [&](int cta) {
+              const size_t slot = (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + g * kTile + row;
+              return __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot * 2));
+            };
+            for (int cta = first; cta <= last; ++cta) {
+              const float2 ml = ml_of(cta);
+              const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+              l = l * ex2_approx(m - mu) + ml.y * ex2_approx(ml.x - mu);
+              m = mn;
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            const float iv = l > 0.f || l != l ? scale_v / l : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float x[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = 0.f;
+#pragma unroll 2
               for (int cta = first; cta <= last; ++cta) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(cta) * 2));
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(cta) * D) + d4);
-                const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-                const float wa = ex2_approx(m - mu), wb = ex2_approx(ml.x - mu);
-                l = l * wa + ml.y * wb;
-                o.x = o.x * wa + v.x * wb;
-                o.y = o.y * wa + v.y * wb;
-                o.z = o.z * wa + v.z * wb;
-                o.w = o.w * wa + v.w * wb;
-                m = mn;
+                const float4* src = reinterpret_cast<const float4*>(
+                    p.part_o + ((size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + g * kTile) * D) + row;
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (8 * c + k) * kTile);
+                const float w = ex2_approx(ml_of(cta).x - mu) * iv;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  x[4 * k] = fmaf(v[k].x, w, x[4 * k]);
+                  x[4 * k + 1] = fmaf(v[k].y, w, x[4 * k + 1]);
+                  x[4 * k + 2] = fmaf(v[k].z, w, x[4 * k + 2]);
+                  x[4 * k + 3] = fmaf(v[k].w, w, x[4 * k + 3]);
+                }
               }
-              const float iv = l > 0.f || l != l ? scale_v / l : 0.f;
-              uint16_t* dst = a.out + ((size_t)(u.q_tok + g * TG + r / G) * p.Hq + u.h * G + r % G) * D + 4 * d4;
-              const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * iv, o.y * iv), b1 = __floats2bfloat162_rn(o.z * iv, o.w * iv);
-              *reinterpret_cast<uint2*>(dst) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+              if (live) store_row32(o16 + 32 * c, x, out32);
             }
           }
         }

@@ -670,17 +670,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           auto slot = [&](int cta) { return (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + r; };
           float m = -INFINITY, l = 0.f;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int cta = first; cta <= last; ++cta) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(cta) * 2));
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(cta) * D) + d4);
-            const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-            const float wa = ex2_approx(m - mu), wb = ex2_approx(ml.x - mu);
-            l = l * wa + ml.y * wb;
-            o.x = o.x * wa + v.x * wb;
-            o.y = o.y * wa + v.y * wb;
-            o.z = o.z * wa + v.z * wb;
-            o.w = o.w * wa + v.w * wb;
-            m = mn;
+          for (int c0 = first; c0 <= last; c0 += 8) {     // eight parts' loads in flight at a time
+            float2 ml[8];
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int cta = c0 + i <= last ? c0 + i : last;
+              ml[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(cta) * 2));
+              v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(cta) * D) + d4);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (c0 + i > last) break;
+              const float mn = fmaxf(m, ml[i].x), mu = mn == -INFINITY ? 0.f : mn;
+              const float wa = ex2_approx(m - mu), wb = ex2_approx(ml[i].x - mu);
+              l = l * wa + ml[i].y * wb;
+              o.x = o.x * wa + v[i].x * wb;
+              o.y = o.y * wa + v[i].y * wb;
+              o.z = o.z * wa + v[i].z * wb;
+              o.w = o.w * wa + v[i].w * wb;
+              m = mn;
+            }
           }
           const float inv = l > 0.f || l != l ? scale_v / l : 0.f;
           *reinterpret_cast<uint2*>(out_row(r) + 4 * d4) = make_uint2(bf2(o.x * inv, o.y * inv), bf2(o.z * inv, o.w * inv));
