@@ -17,9 +17,15 @@
 // turns on the tensor cores: while one group's scores are turned into
 // probabilities, the other's products run.  Per 128-token tile and group:
 //   S_g = Q_g K^T  (kind::f16, both operands from shared memory)
-//   O_g += P_g V   (P from TMEM, over S_g's columns; V MN-major from shared
-//                   memory, as the TMA wrote it)
-// TMEM: S_0, S_1, O_0, O_1, 128 columns each.
+//   O_g += P_g V   (P from TMEM; V MN-major from shared memory, as the TMA
+//                   wrote it)
+// TMEM at d = 128: S_0, S_1, O_0, O_1, 128 columns each, P_g over S_g's
+// columns, so S_g of the next tile follows P_g V of this one.  At d = 64 the
+// products are half as long and that chain (scores, probabilities, product,
+// scores) bounded the kernel, with 36 % of the issue slots used; the
+// accumulators leave room there for P_g columns of their own, and S_g of the
+// next tile is made as soon as this one's scores are in registers.  There is
+// room for two units' queries in shared memory then, too.
 //
 // The (request, row tile, head, key tile) space is flattened and cut into
 // one contiguous range per CTA, as in the kernel for few rows; units cut by a
@@ -27,8 +33,8 @@
 // arrive merges them in range order.
 //
 // Warps: 0-7 softmax (group = warp / 4, thread = row), 8 copies (walks the
-// units, writes their descriptors into a small queue, TMA), 9 the MMA issuer,
-// 10.. helpers: over an E4M3 cache they widen each landed tile, exactly, to
+// units, writes their descriptors into a small queue, TMA), 9 (and 10 at
+// d = 64) the MMA issuers, the rest helpers: over an E4M3 cache they widen each landed tile, exactly, to
 // f16 (K and V); over a bf16 cache they only touch tiles at the borders of
 // what a request may read, whose values at other places become zeros.
 //
@@ -58,19 +64,24 @@ constexpr int kChunkSmem = 232448;
 template <int D, bool E4M3>
 struct ChunkLayout {
   // Over an E4M3 cache the helpers are a warpgroup of their own (warps
-  // 12-15, 10 and 11 idle), so that registers can move between warpgroups.
-  static constexpr int kWarpHelp = E4M3 ? 12 : 10;
-  static constexpr int kHelpers = E4M3 ? 4 : 2;                  // warps
+  // 12-15, 11 idle), so that registers can move between warpgroups.
+  static constexpr int kWarpHelp = E4M3 ? 12 : 11;
+  static constexpr int kHelpers = E4M3 ? 4 : 1;                  // warps
   static constexpr int kThreads = 32 * (kWarpHelp + kHelpers);
   static constexpr int kAtom = kTile * 128;                      // 128 rows x 64 16-bit columns
   static constexpr int kAtoms = D / 64;
   static constexpr int kQGroup = kAtoms * kAtom;
   static constexpr int kSlot = kAtoms * kAtom;                   // one 16-bit K or V tile
   static constexpr int kRaw = E4M3 ? kTile * D : 0;              // one E4M3 tile
-  static constexpr int kSlots = D == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 8 : 11);
-  static constexpr int kRaws = E4M3 ? (D == 128 ? 4 : 6) : 0;
+  static constexpr int kSlots = D == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 7 : 9);
+  static constexpr int kRaws = E4M3 ? (D == 128 ? 4 : 5) : 0;
+  static constexpr int kQBufs = D == 128 ? 1 : 2;                // units whose queries fit
+  static constexpr bool kOwnP = D == 64;                         // P has columns of its own
+  static constexpr int kIssuers = kOwnP ? 2 : 1;                 // MMA-issuing threads
+  static constexpr uint32_t kColO = 256, kColOStep = D == 128 ? 128 : 64;
+  static constexpr uint32_t kColP = kOwnP ? 384 : 0, kColPStep = kOwnP ? 64 : 128;
   static constexpr int kQ = 0;
-  static constexpr int kKV = 2 * kQGroup;
+  static constexpr int kKV = kQBufs * 2 * kQGroup;
   static constexpr int kRawAt = kKV + kSlots * kSlot;
   static constexpr int kMisc = kRawAt + kRaws * kRaw;
   static constexpr int kBytes = 1024 + kMisc + 1024;
@@ -94,12 +105,13 @@ struct Unit {
 
 struct ChunkMisc {
   uint64_t u_full[kUnitQueue], u_empty[kUnitQueue];
-  uint64_t q_full, q_ready, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t q_full[2], q_ready[2], q_empty[2];
+  // s_free: the scores are in registers (kOwnP); pv: P_g V has finished
+  uint64_t s_full[2], s_free[2], p_full[2], pv[2], o_free[2];
   // ring slots: the copy landed (bf16 only), the helpers are done with it,
   // its MMAs have read it; and the E4M3 tiles before they are widened
   uint64_t full[11], ready[11], empty[11], raw_full[6], raw_empty[6];
-  uint64_t done, grp[2];
+  uint64_t done[2], grp[2];
   unsigned long long ws[16];
   long long total, base;
   Unit u[kUnitQueue];
@@ -196,27 +208,28 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     prefetch_tensormap(&tmV);
     for (int i = 0; i < kUnitQueue; ++i) {
       mbar_init(bar(misc->u_full[i]), 1);
-      mbar_init(bar(misc->u_empty[i]), 8 + 1 + L::kHelpers);
+      mbar_init(bar(misc->u_empty[i]), 8 + L::kIssuers + L::kHelpers);
     }
-    mbar_init(bar(misc->q_full), 1);
-    mbar_init(bar(misc->q_ready), 256);
-    mbar_init(bar(misc->q_empty), 1);
     for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(misc->q_full[g]), 1);
+      mbar_init(bar(misc->q_ready[g]), 256);
+      mbar_init(bar(misc->q_empty[g]), L::kIssuers);
       mbar_init(bar(misc->s_full[g]), 1);
+      mbar_init(bar(misc->s_free[g]), 4);
       mbar_init(bar(misc->p_full[g]), 128);
-      mbar_init(bar(misc->o_full[g]), 1);
+      mbar_init(bar(misc->pv[g]), 1);
       mbar_init(bar(misc->o_free[g]), 128);
     }
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(misc->full[i]), 1);
-      mbar_init(bar(misc->empty[i]), 1);
+      mbar_init(bar(misc->empty[i]), L::kIssuers);
       mbar_init(bar(misc->ready[i]), E4M3 ? kHelpThreads : L::kHelpers);
     }
     for (int i = 0; i < L::kRaws; ++i) {
       mbar_init(bar(misc->raw_full[i]), 1);
       mbar_init(bar(misc->raw_empty[i]), kHelpThreads);
     }
-    mbar_init(bar(misc->done), 1);
+    for (int g = 0; g < 2; ++g) mbar_init(bar(misc->done[g]), 1);
     for (int g = 0; g < 2; ++g) mbar_init(bar(misc->grp[g]), 128);
     misc->abort = 0;
     mbar_fence_init();
@@ -390,19 +403,28 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           // the queries behind the unit's first keys: their place is free
           // once the previous unit's last scores have been computed
           if (j == 0 && kv == 0) {
-            try_wait(misc->q_empty, (nu & 1) ^ 1);
+            const int qb = nu % L::kQBufs;
+            try_wait(misc->q_empty[qb], ((nu / L::kQBufs) & 1) ^ 1);
             if (stopped) {
               ++n;
               break;
             }
             if (lane == 0) {
               const int ng = ntok > TG ? 2 : 1;
-              mbar_arrive_expect_tx(bar(misc->q_full), (uint32_t)(ng * L::kAtoms * TG * G * 128));
+              mbar_arrive_expect_tx(bar(misc->q_full[qb]), (uint32_t)(ng * L::kAtoms * TG * G * 128));
               for (int g = 0; g < ng; ++g)
 #pragma unroll
                 for (int c = 0; c < L::kAtoms; ++c)
-                  tma_load_3d(sbase + L::kQ + g * L::kQGroup + c * L::kAtom, &tmQ, c * 64, h * G,
-                              rq.q0 + i0 + g * TG, bar(misc->q_full));
+                  tma_load_3d(sbase + L::kQ + (2 * qb + g) * L::kQGroup + c * L::kAtom, &tmQ, c * 64, h * G,
+                              rq.q0 + i0 + g * TG, bar(misc->q_full[qb]));
+              // the next unit's queries on their way into L2, if it is of the
+              // same request
+              const bool next_h = h + 1 < p.Hkv;
+              if (uend < stop && (next_h || rt + 1 < rq.nrt))
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                  for (int c = 0; c < L::kAtoms; ++c)
+                    tma_prefetch_3d(&tmQ, c * 64, next_h ? (h + 1) * G : 0, rq.q0 + i0 + (next_h ? 0 : tpu) + g * TG);
             }
             ++nq;
             __syncwarp();
@@ -430,76 +452,110 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     volatile int no_abort = 0;
     for (int i = n - kRing < 0 ? 0 : n - kRing; i < n; ++i)
       mbar_wait_bounded(bar(full[i % kRing]), (i / kRing) & 1, &no_abort, a.wait_ns);
-    if (nq > 0) mbar_wait_bounded(bar(misc->q_full), (nq - 1) & 1, &no_abort, a.wait_ns);
-  } else if (warp == kWarpIssue) {
-    // --------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    for (int i = nq - L::kQBufs < 0 ? 0 : nq - L::kQBufs; i < nq; ++i)
+      mbar_wait_bounded(bar(misc->q_full[i % L::kQBufs]), (i / L::kQBufs) & 1, &no_abort, a.wait_ns);
+  } else if (warp == kWarpIssue || warp == kWarpIssue + 1) {
+    // ------------------------------------------------- MMA issuers
+    // d = 64: a thread per group.  d = 128: one thread for both (two threads'
+    // products interleave there, which cost 25 %), no commit between a
+    // product and the next scores (each had cost 8 %).
+    if (lane == 0 && warp - kWarpIssue < L::kIssuers) {
       constexpr uint32_t idesc_qk = idesc_16(128, 128, false, !E4M3), idesc_pv = idesc_16(128, D, true, !E4M3);
       const uint64_t dq = smem_desc(sbase + L::kQ, 16, 1024, 2u), dk = smem_desc(sbase + L::kKV, 16, 1024, 2u);
       const uint64_t dv = smem_desc(sbase + L::kKV, (uint32_t)L::kAtom, 1024, 2u);
-      const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
-      const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
       constexpr uint32_t kSlotStep = L::kSlot >> 4, kQStep = L::kQGroup >> 4, kAtomStep = L::kAtom >> 4;
-      int n = 0;
-      int nt_g[2] = {0, 0}, nu_g[2] = {0, 0};   // tiles and units of each group so far
-      auto qk = [&](int g, int slot) {
+      const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32);
+      const uint32_t k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+      int n = 0;   // slots so far
+      auto slot_ready = [&](int i) { wait(misc->ready[i % L::kSlots], (i / L::kSlots) & 1); };
+      auto qk = [&](int g, int slot, uint32_t q_at) {
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ss(tmem + 128 * g, q_lo + g * kQStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), q_hi,
+          mma_f16_ss(tmem + 128 * g, q_at + g * kQStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), q_hi,
                      k_lo + slot * kSlotStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), k_hi, idesc_qk, kk != 0);
         mma_commit(bar(misc->s_full[g]));
       };
+      auto pv = [&](int g, int slot, bool first) {
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_f16_ts_w(tmem + L::kColO + L::kColOStep * g, tmem + L::kColP + L::kColPStep * g + 8 * kk,
+                       v_lo + slot * kSlotStep + kk * 128, v_hi, idesc_pv, (!first || kk > 0) ? 1u : 0u);
+      };
+      auto free_slot = [&](int slot) { mma_commit(bar(misc->empty[slot])); };
+      int np[2] = {0, 0}, no[2] = {0, 0}, ns[2] = {0, 0};   // each group's P V, units, Q K so far
       for (int nu = 0;; ++nu) {
         const int uq = nu % kUnitQueue;
         wait(misc->u_full[uq], (nu / kUnitQueue) & 1);
         const Unit u = misc->u[uq];
         if (u.end || *abort) break;
-        const int ng = u.ntok > TG ? 2 : 1;
-        wait(E4M3 ? misc->q_ready : misc->q_full, nu & 1);
-        int ks = n % L::kSlots;
-        wait(misc->ready[ks], (n / L::kSlots) & 1);
-        for (int g = 0; g < ng; ++g) qk(g, ks);
-        mma_commit(bar(misc->empty[ks]));
-        if (u.ntile == 1) mma_commit(bar(misc->q_empty));
-        for (int j = 0; j < u.ntile; ++j) {
-          const int nv = n + 2 * j + 1, vs = nv % L::kSlots, nk = nv + 1;
-          const bool more = j + 1 < u.ntile;
-          ks = nk % L::kSlots;
-          for (int g = 0; g < ng; ++g) {
-            if (g == 0) {
-              wait(misc->ready[vs], (nv / L::kSlots) & 1);
+        const int qb = nu % L::kQBufs;
+        const uint32_t q_at = q_lo + 2 * qb * kQStep;
+        wait(E4M3 ? misc->q_ready[qb] : misc->q_full[qb], (nu / L::kQBufs) & 1);
+        const int last = n + 2 * u.ntile - 1;
+        if constexpr (L::kOwnP) {
+          const int g = warp - kWarpIssue;
+          if (g == 1 && u.ntok <= TG) {
+            // no rows for this group: pass everything on as it comes
+            mbar_arrive(bar(misc->q_empty[qb]));
+            for (; n <= last; ++n) {
+              slot_ready(n);
+              mbar_arrive(bar(misc->empty[n % L::kSlots]));
             }
-            wait(misc->p_full[g], nt_g[g] & 1);
-            if (j == 0) wait(misc->o_free[g], (nu_g[g] & 1) ^ 1);
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_f16_ts_w(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk, v_lo + vs * kSlotStep + kk * 128, v_hi,
-                           idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-            ++nt_g[g];
-            if (!more) {
-              mma_commit(bar(misc->o_full[g]));
-              ++nu_g[g];
-            }
-            if (g == ng - 1) mma_commit(bar(misc->empty[vs]));
-            if (more) {
-              if (g == 0) wait(misc->ready[ks], (nk / L::kSlots) & 1);
-              qk(g, ks);
-              if (g == ng - 1) {
-                mma_commit(bar(misc->empty[ks]));
-                if (j + 2 == u.ntile) mma_commit(bar(misc->q_empty));
-              }
+          } else {
+            auto scores = [&](int i) {   // of the tile in place i
+              slot_ready(i);
+              wait(misc->s_free[g], (ns[g]++ & 1) ^ 1);
+              qk(g, i % L::kSlots, q_at);
+              free_slot(i % L::kSlots);
+              if (i + 1 == last) mma_commit(bar(misc->q_empty[qb]));
+            };
+            scores(n);
+            for (int j = 0; j < u.ntile; ++j, n += 2) {
+              if (n + 2 < last) scores(n + 2);
+              slot_ready(n + 1);
+              wait(misc->p_full[g], np[g]++ & 1);
+              if (j == 0) wait(misc->o_free[g], (no[g]++ & 1) ^ 1);
+              pv(g, (n + 1) % L::kSlots, j == 0);
+              mma_commit(bar(misc->pv[g]));
+              free_slot((n + 1) % L::kSlots);
             }
           }
+        } else {
+          const int ng = u.ntok > TG ? 2 : 1;
+          slot_ready(n);
+          for (int g = 0; g < ng; ++g) qk(g, n % L::kSlots, q_at);
+          free_slot(n % L::kSlots);
+          if (u.ntile == 1) mma_commit(bar(misc->q_empty[qb]));
+          for (int j = 0; j < u.ntile; ++j, n += 2) {
+            const bool more = j + 1 < u.ntile;
+            for (int g = 0; g < ng; ++g) {
+              if (g == 0) slot_ready(n + 1);
+              wait(misc->p_full[g], np[g]++ & 1);
+              if (j == 0) wait(misc->o_free[g], (no[g]++ & 1) ^ 1);
+              pv(g, (n + 1) % L::kSlots, j == 0);
+              // (the next scores' commit tells the softmax of this product
+              // too, except behind the last tile)
+              if (!more) {
+                mma_commit(bar(misc->pv[g]));
+              } else {
+                if (g == 0) slot_ready(n + 2);
+                qk(g, (n + 2) % L::kSlots, q_at);
+              }
+            }
+            free_slot((n + 1) % L::kSlots);
+            if (more) free_slot((n + 2) % L::kSlots);
+            if (j + 2 == u.ntile) mma_commit(bar(misc->q_empty[qb]));
+          }
         }
-        n += 2 * u.ntile;
         mbar_arrive(bar(misc->u_empty[uq]));
       }
       // every MMA issued above has finished before TMEM is freed
-      mma_commit(bar(misc->done));
+      uint64_t& done = misc->done[warp - kWarpIssue];
+      mma_commit(bar(done));
       volatile int no_abort = 0;
-      mbar_wait_bounded(bar(misc->done), 0, &no_abort, a.wait_ns);
+      mbar_wait_bounded(bar(done), 0, &no_abort, a.wait_ns);
     }
     __syncwarp();
   } else if (warp >= L::kWarpHelp) {
@@ -585,7 +641,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     const int g = warp >> 2, row = threadIdx.x & (kTile - 1);
     const int ri = row / G, head = row % G;            // the row's token in its group, its query head
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = trow + 128 * g, tO = trow + 256 + 128 * g;
+    const uint32_t tS = trow + 128 * g, tO = trow + L::kColO + L::kColOStep * g;
+    const uint32_t tP = trow + L::kColP + L::kColPStep * g;
     const float* sc = p.scales + (size_t)a.layer * 4 * p.Hkv;
     int syncs = 0;
     auto sync_group = [&]() {
@@ -593,7 +650,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       wait(misc->grp[g], syncs++ & 1);
       __syncwarp();
     };
-    int nt_done = 0, nu_done = 0;
+    int nt_done = 0, nu_done = 0;   // this group's tiles and units so far
     const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // 32-byte stores
     for (int nu = 0;; ++nu) {
       const int uq = nu % kUnitQueue;
@@ -605,10 +662,11 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       const bool live = ri < TG && tok < u.ntok;
       float f_row = a.sm_log2;
       if constexpr (E4M3) {
-        wait(misc->q_full, nu & 1);
+        const int qb = nu % L::kQBufs;
+        wait(misc->q_full[qb], (nu / L::kQBufs) & 1);
         if (live) {
           // this row's queries, in place: 8 D/64 chunks of 16 bytes
-          uint8_t* qg = sm + L::kQ + g * L::kQGroup;
+          uint8_t* qg = sm + L::kQ + (2 * qb + g) * L::kQGroup;
           uint32_t em = 0;
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) {
@@ -633,7 +691,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(bar(misc->q_ready));
+        mbar_arrive(bar(misc->q_ready[qb]));
       }
       if (active) {
         // what this row sees, and what every row of the group sees
@@ -653,6 +711,11 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
           tmem_wait_ld();
+          if constexpr (L::kOwnP) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(misc->s_free[g]));
+          }
           const int t = (u.tile0 + j) * kTile;
           if (t + kTile > all_hi || t < all_lo) {
             const int vh = hi - t, vl = lo - t;
@@ -671,7 +734,13 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           const float tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
           const bool need = tmax > m_run + kRaise || (m_run == -INFINITY && tmax > m_run);
           const float m_new = need ? tmax : m_run;
-          // S(j) complete means PV(j - 1), issued before it, is complete too
+          // O_g and P_g are touched once P V of the previous tile is complete;
+          // where S_g follows it, S(j) complete says so
+          if (L::kOwnP && j > 0) {
+            wait(misc->pv[g], (nt_done - 1) & 1);
+            __syncwarp();
+            tc_fence_after();
+          }
           if (j > 0 && __any_sync(0xFFFFFFFFu, need)) {
             const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
 #pragma unroll 1
@@ -713,7 +782,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
                 pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
               }
             }
-            tmem_st16(tS + 16 * c, pw);
+            tmem_st16(tP + 16 * c, pw);
 #pragma unroll
             for (int w = 8; w > 0; w >>= 1)
 #pragma unroll
@@ -726,7 +795,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           mbar_arrive(bar(misc->p_full[g]));
         }
         // ------------------------------------------------------- epilogue
-        wait(misc->o_full[g], nu_done & 1);
+        wait(misc->pv[g], (L::kOwnP ? nt_done - 1 : nu_done) & 1);
         ++nu_done;
         __syncwarp();
         tc_fence_after();
