@@ -197,6 +197,13 @@ __device__ __forceinline__ int ld_relaxed_gpu(const int32_t* p) {
   return v;
 }
 
+// A load that orders what follows it behind what the writer did before.
+__device__ __forceinline__ int ld_acquire_gpu(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // Four consecutive words by one relaxed load at device scope (16-byte aligned).
 __device__ __forceinline__ int4 ld_relaxed_gpu_v4(const int32_t* p) {
   int4 v;

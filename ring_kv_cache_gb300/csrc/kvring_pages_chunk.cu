@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
   const int G = p.Hq / p.Hkv, TG = kTile / G, tpu = 2 * TG;   // tokens of a group, of a unit
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   auto wait = [&](uint64_t& b, uint32_t parity) {
-    if (!*abort) mbar_wait_bounded(smem_u32(&b), parity, abort, a.wait_ns);
+    if (!mbar_try_wait(smem_u32(&b), parity) && !*abort) mbar_wait_bounded(smem_u32(&b), parity, abort, a.wait_ns);
   };
   if (threadIdx.x == 0) {
     prefetch_tensormap(&tmQ);
@@ -216,9 +216,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       mbar_init(bar(misc->q_empty[g]), L::kIssuers);
       mbar_init(bar(misc->s_full[g]), 1);
       mbar_init(bar(misc->s_free[g]), 4);
-      mbar_init(bar(misc->p_full[g]), 128);
+      mbar_init(bar(misc->p_full[g]), 4);
       mbar_init(bar(misc->pv[g]), 1);
-      mbar_init(bar(misc->o_free[g]), 128);
+      mbar_init(bar(misc->o_free[g]), 4);
     }
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(misc->full[i]), 1);
@@ -702,22 +702,63 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         const int all_hi = a.causal ? u.pos0 + g * TG + 1 : u.klen;
         const int all_lo = a.window > 0 ? u.pos0 + ntok_g - a.window : 0;
         const int ntile = u.ntile;
-        float m_run = -INFINITY, ell = 0.f;
-        for (int j = 0; j < ntile; ++j, ++nt_done) {
-          wait(misc->s_full[g], nt_done & 1);
-          __syncwarp();
-          tc_fence_after();
-          uint32_t sr[128];
+        // (a row that is none keeps a factor of 0 and never asks for anything)
+        float m_run = live ? -INFINITY : 0.f, ell = 0.f;
+        if (!live) f_row = 0.f;
+        // 32 scores to probabilities, as pairs of the 16-bit type; their sum
+        // is added to lsum
+        auto probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, float moff, float2& lsum) {
+          const float2 fr2 = make_float2(f_row, f_row), mo2 = make_float2(moff, moff);
+          float2 e[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
-          tmem_wait_ld();
+          for (int i = 0; i < 16; ++i) {
+            const float2 x =
+                __ffma2_rn(make_float2(__uint_as_float(s32[2 * i]), __uint_as_float(s32[2 * i + 1])), fr2, mo2);
+            e[i] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if constexpr (E4M3) {
+              pw[i] = f32x2_to_f16x2(e[i].x, e[i].y);
+            } else {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(e[i].x, e[i].y);
+              pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+          }
+#pragma unroll
+          for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+            for (int i = 0; i < w; ++i) e[i] = __fadd2_rn(e[i], e[i + w]);
+          lsum = __fadd2_rn(lsum, e[0]);
+        };
+        auto scores_read = [&]() {
           if constexpr (L::kOwnP) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(misc->s_free[g]));
           }
+        };
+        // O_g and P_g are touched once P V of the previous tile is complete;
+        // where S_g follows it, S(j) complete says so
+        auto previous_done = [&](int j) {
+          if (L::kOwnP && j > 0) {
+            wait(misc->pv[g], (nt_done - 1) & 1);
+            __syncwarp();
+            tc_fence_after();
+          }
+        };
+        for (int j = 0; j < ntile; ++j, ++nt_done) {
+          wait(misc->s_full[g], nt_done & 1);
+          __syncwarp();
+          tc_fence_after();
           const int t = (u.tile0 + j) * kTile;
-          if (t + kTile > all_hi || t < all_lo) {
+          const bool masked = t + kTile > all_hi || t < all_lo;
+          uint32_t sr[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
+          tmem_wait_ld();
+          scores_read();
+          if (masked) {
             const int vh = hi - t, vl = lo - t;
 #pragma unroll
             for (int c = 0; c < 128; ++c)
@@ -734,13 +775,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           const float tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
           const bool need = tmax > m_run + kRaise || (m_run == -INFINITY && tmax > m_run);
           const float m_new = need ? tmax : m_run;
-          // O_g and P_g are touched once P V of the previous tile is complete;
-          // where S_g follows it, S(j) complete says so
-          if (L::kOwnP && j > 0) {
-            wait(misc->pv[g], (nt_done - 1) & 1);
-            __syncwarp();
-            tc_fence_after();
-          }
+          previous_done(j);
           if (j > 0 && __any_sync(0xFFFFFFFFu, need)) {
             const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
 #pragma unroll 1
@@ -761,38 +796,18 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           }
           m_run = m_new;
           const float moff = kShift - (m_run == -INFINITY ? 0.f : m_run);   // nothing seen yet: 2^-inf = 0
-          const float2 fr2 = make_float2(f_row, f_row), mo2 = make_float2(moff, moff);
           float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float2 e[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = __ffma2_rn(
-                  make_float2(__uint_as_float(sr[32 * c + 2 * i]), __uint_as_float(sr[32 * c + 2 * i + 1])), fr2, mo2);
-              e[i] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-            }
             uint32_t pw[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if constexpr (E4M3) {
-                pw[i] = f32x2_to_f16x2(e[i].x, e[i].y);
-              } else {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(e[i].x, e[i].y);
-                pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-            }
+            probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
             tmem_st16(tP + 16 * c, pw);
-#pragma unroll
-            for (int w = 8; w > 0; w >>= 1)
-#pragma unroll
-              for (int i = 0; i < w; ++i) e[i] = __fadd2_rn(e[i], e[i + w]);
-            lsum = __fadd2_rn(lsum, e[0]);
           }
           ell += lsum.x + lsum.y;
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(bar(misc->p_full[g]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(misc->p_full[g]));
         }
         // ------------------------------------------------------- epilogue
         wait(misc->pv[g], (L::kOwnP ? nt_done - 1 : nu_done) & 1);
@@ -802,9 +817,72 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         const float scale_v = E4M3 ? __ldcg(sc + p.Hkv + u.h) : 1.0f;
         const float inv = ell > 0.f || ell != ell ? scale_v / ell : 0.f;
         const bool whole = u.whole;
+        const int first = u.first, last = u.last;
         uint16_t* o16 = a.out + ((size_t)(u.q_tok + tok) * p.Hq + u.h * G + head) * D;
-        // partial rows lie column group by column group, [D/4][128 rows] of
-        // four floats, so that a warp writes and reads whole lines
+        // Partial rows lie column group by column group, [D/4][128 rows] of
+        // four floats, so that a warp writes and reads whole lines; their
+        // (maximum, sum) in part_ml.
+        auto slot_of = [&](int cta) { return (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + g * kTile; };
+        int* ticket = p.tickets + 2 * first + g;
+        // The CTA whose part is the last to be done merges: at once, with its
+        // own accumulator, if the others' parts are all there already, else
+        // all from the workspace.
+        bool merge_now = false;
+        if (!whole) {
+          if (row == 0) misc->last[g] = ld_acquire_gpu(ticket) == last - first;
+          sync_group();
+          merge_now = misc->last[g];
+        }
+        // Parts are always taken in range order (this CTA's own, where it
+        // still has it, from registers), so the result does not depend on
+        // who merges.
+        float m_all = 0.f, iv_all = 0.f;
+        auto ml_of = [&](int cta) {
+          if (merge_now && cta == (int)blockIdx.x) return make_float2(m_run, ell);
+          return __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot_of(cta) + row) * 2));
+        };
+        auto weigh = [&]() {
+          float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+          for (int cta = first; cta <= last; ++cta) {
+            const float2 ml = ml_of(cta);
+            const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+            l = l * ex2_approx(m - mu) + ml.y * ex2_approx(ml.x - mu);
+            m = mn;
+          }
+          m_all = m == -INFINITY ? 0.f : m;
+          iv_all = l > 0.f || l != l ? scale_v / l : 0.f;
+        };
+        auto merge_columns = [&](int c, const uint32_t (&own)[32]) {
+          float x[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = 0.f;
+#pragma unroll 2
+          for (int cta = first; cta <= last; ++cta) {
+            const float4* src = reinterpret_cast<const float4*>(p.part_o + slot_of(cta) * D) + row;
+            const bool mine = merge_now && cta == (int)blockIdx.x;
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              v[k] = mine ? make_float4(__uint_as_float(own[4 * k]), __uint_as_float(own[4 * k + 1]),
+                                        __uint_as_float(own[4 * k + 2]), __uint_as_float(own[4 * k + 3]))
+                          : __ldcg(src + (8 * c + k) * kTile);
+            const float w = ex2_approx(ml_of(cta).x - m_all) * iv_all;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              x[4 * k] = fmaf(v[k].x, w, x[4 * k]);
+              x[4 * k + 1] = fmaf(v[k].y, w, x[4 * k + 1]);
+              x[4 * k + 2] = fmaf(v[k].z, w, x[4 * k + 2]);
+              x[4 * k + 3] = fmaf(v[k].w, w, x[4 * k + 3]);
+            }
+          }
+          if (live) store_row32(o16 + 32 * c, x, out32);
+        };
+        if (merge_now) {
+          __threadfence();
+          if (row == 0) *ticket = 0;
+          weigh();
+        }
         float4* o32 = reinterpret_cast<float4*>(p.part_o + ((size_t)u.part * kPartRows + g * kTile) * D) + row;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -812,11 +890,13 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           __syncwarp();
           tmem_ld32(tO + 32 * c, rr);
           tmem_wait_ld();
-          if (!whole) {
+          if (!whole && !merge_now) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               o32[(8 * c + k) * kTile] = make_float4(__uint_as_float(rr[4 * k]), __uint_as_float(rr[4 * k + 1]),
                                                      __uint_as_float(rr[4 * k + 2]), __uint_as_float(rr[4 * k + 3]));
+          } else if (merge_now) {
+            merge_columns(c, rr);
           } else if (live) {
             float x[32];
 #pragma unroll
@@ -824,60 +904,25 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             store_row32(o16 + 32 * c, x, out32);
           }
         }
-        __syncwarp();
         tc_fence_before();
-        mbar_arrive(bar(misc->o_free[g]));
-        if (!whole) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(misc->o_free[g]));
+        if (!whole && !merge_now) {
           *reinterpret_cast<float2*>(p.part_ml + ((size_t)u.part * kPartRows + g * kTile + row) * 2) =
-                make_float2(m_run, ell);
-          const int first = u.first, last = u.last;
+              make_float2(m_run, ell);
           __threadfence();
           sync_group();
           if (row == 0) {
-            const int old = atomicAdd(p.tickets + 2 * first + g, 1);
-            misc->last[g] = old == last - first;
-            if (misc->last[g]) p.tickets[2 * first + g] = 0;
+            misc->last[g] = atomicAdd(ticket, 1) == last - first;
+            if (misc->last[g]) *ticket = 0;
           }
           sync_group();
           if (misc->last[g]) {
             __threadfence();
-            // thread = row again: the parts' weights, then 32 columns at a time
-            float m = -INFINITY, l = 0.f;
-            auto ml_of = [&](int cta) {
-              const size_t slot = (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + g * kTile + row;
-              return __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot * 2));
-            };
-            for (int cta = first; cta <= last; ++cta) {
-              const float2 ml = ml_of(cta);
-              const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-              l = l * ex2_approx(m - mu) + ml.y * ex2_approx(ml.x - mu);
-              m = mn;
-            }
-            const float mu = m == -INFINITY ? 0.f : m;
-            const float iv = l > 0.f || l != l ? scale_v / l : 0.f;
+            weigh();
+            const uint32_t none[32] = {};
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float x[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = 0.f;
-#pragma unroll 2
-              for (int cta = first; cta <= last; ++cta) {
-                const float4* src = reinterpret_cast<const float4*>(
-                    p.part_o + ((size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + g * kTile) * D) + row;
-                float4 v[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = __ldcg(src + (8 * c + k) * kTile);
-                const float w = ex2_approx(ml_of(cta).x - mu) * iv;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  x[4 * k] = fmaf(v[k].x, w, x[4 * k]);
-                  x[4 * k + 1] = fmaf(v[k].y, w, x[4 * k + 1]);
-                  x[4 * k + 2] = fmaf(v[k].z, w, x[4 * k + 2]);
-                  x[4 * k + 3] = fmaf(v[k].w, w, x[4 * k + 3]);
-                }
-              }
-              if (live) store_row32(o16 + 32 * c, x, out32);
-            }
+            for (int c = 0; c < D / 32; ++c) merge_columns(c, none);
           }
         }
       }
