@@ -86,6 +86,13 @@ cudaError_t paged_chunk_prepare();
 cudaError_t launch_paged_chunk(const PagesDev& p, const CUtensorMap* tmQ, const CUtensorMap* tmK,
                                const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s);
 
+// Four E4M3 codes (low byte first) to two f16 pairs, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=&r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
 // One launch with the programmatic-stream-serialisation attribute.
 template <typename... KP, typename... A>
 inline cudaError_t launch_pdl(void (*kernel)(KP...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {

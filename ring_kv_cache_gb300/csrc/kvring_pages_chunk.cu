@@ -601,10 +601,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             const uint32_t wi[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             uint32_t hv[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              hv[2 * e] = e4m3x2_to_f16x2((uint16_t)(wi[e] & 0xFFFFu));
-              hv[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(wi[e] >> 16));
-            }
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(wi[e], hv[2 * e], hv[2 * e + 1]);
             uint8_t* atom = dst + (c >> 2) * L::kAtom;
             *reinterpret_cast<uint4*>(atom + swz_offset(row, 2 * (c & 3), 128)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
             *reinterpret_cast<uint4*>(atom + swz_offset(row, 2 * (c & 3) + 1, 128)) =

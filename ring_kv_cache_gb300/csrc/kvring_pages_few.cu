@@ -1,5 +1,5 @@
 // Attention over the paged cache for requests with few query rows: single
-// tokens, drafts, short chunks (up to 64 rows a unit, a row being one query
+// tokens, drafts, short chunks (up to 32 rows a unit, a row being one query
 // head of one token).
 //
 //   out[r] = sum_j softmax_j(s_rj) V[j],  s_rj = scale q[r] . K[j]
@@ -8,7 +8,7 @@
 // l' = l 2^(m - m') + sum p, O' = O 2^(m - m') + p V.
 //
 // Bound by HBM: every cached key and value of the request is read once per
-// key/value head (all its query heads share the tile), and with at most 64
+// key/value head (all its query heads share the tile), and with at most 32
 // rows the arithmetic is a small part of the tensor rate.  So the design is
 // about keeping copies in flight: one CTA per SM whose producer warp streams
 // page pieces by TMA into a ring of shared-memory slots (about 190 KB), and
@@ -23,10 +23,13 @@
 // The matrix products use mma.sync (m16n8k16): with 16 rows a tile of
 // 128 tokens needs 32 instructions per warp, far from any limit, and a
 // register fragment lets the row tile be 16 high where tcgen05 has 64 or
-// 128 rows.  Eight warps: for the scores each takes 16 tokens, for the
-// values each takes 16 of the d columns (at d = 64 the warps' halves take
-// half the tokens each and are added at the end), with the probabilities
-// passed through shared memory.  Two barriers of the eight warps per tile.
+// 128 rows.  Each warp takes 16 of a tile's tokens through both
+// products with a running (m, l, O) of its own: the score fragment is the
+// probability operand as it stands, and nothing is exchanged between warps
+// before the unit's end, where their states are merged in shared memory.
+// (With the columns of O split over the warps instead, and the probabilities
+// passed through shared memory, two barriers per tile bounded the kernel over
+// an E4M3 cache: 310 MB in 88 us.)
 //
 // E4M3 tiles are read as 16-bit pairs by ldmatrix and widened in registers
 // to f16, exactly.  For the scores four consecutive bytes of a key become
@@ -42,20 +45,23 @@
 namespace kvr {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kConsumers = kWarps * 32;
-constexpr int kFewThreads = kConsumers + 32;
+constexpr int kGroups = 8;       // groups of 16 tokens of a tile
 constexpr int kSmemMost = 232448;
 
 template <int D, bool E4M3, int MT>
 struct FewLayout {
   static constexpr int UR = 16 * MT;                       // query rows of a unit
+  // Consumer warps.  They take the 16-token groups in turn.  Eight keep up
+  // with HBM over a bf16 cache; an E4M3 tile is there in half the time and
+  // takes more instructions: eleven.
+  static constexpr int kWarps = E4M3 && MT == 1 ? 11 : 8;
+  static constexpr int kConsumers = kWarps * 32;
+  static constexpr int kThreads = kConsumers + 32;
   static constexpr int kSlot = kTile * D * (E4M3 ? 1 : 2); // one K or V tile
   static constexpr int kQ = 0;                             // offsets behind the slots
-  static constexpr int kP = kQ + UR * D * 2;
-  static constexpr int kMax = kP + UR * kTile * 2;         // float [UR][8]
-  static constexpr int kSum = kMax + UR * 32;              // float [UR][8]
-  static constexpr int kRow = kSum + UR * 32;              // int lo, hi; float factor; pad: [UR][4]
+  static constexpr int kO = kQ + UR * D * 2;               // float [warps][4 rows][D]: the merge of the warps
+  static constexpr int kMl = kO + kWarps * 4 * D * 4;      // float2 [warps][UR]: their maxima and sums
+  static constexpr int kRow = kMl + kWarps * UR * 8;       // int lo, hi; float factor; pad: [UR][4]
   static constexpr int kMisc = kRow + UR * 16;
   static constexpr int kFixed = kMisc + 512;
   static constexpr int kRoom = (kSmemMost - 1024 - kFixed) / kSlot;
@@ -67,7 +73,7 @@ struct FewLayout {
 struct FewMisc {
   uint64_t full[16];
   uint64_t empty[16];
-  unsigned long long ws[9];
+  unsigned long long ws[16];
   long long total;
   long long base;    // tiles before the request the CTA starts in
   int b0;
@@ -102,7 +108,13 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void ldsm2t(uint32_t (&r)[2], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void sync_consumers_n() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 // What a unit of a request needs to know.
 struct Req {
@@ -138,11 +150,12 @@ __device__ __forceinline__ Req load_req(const PagesDev& p, const PagedAttn& a, i
 }
 
 template <int D, bool E4M3, int MT>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     k_paged_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagesDev p,
                 const PagedAttn a) {
   using L = FewLayout<D, E4M3, MT>;
-  constexpr int UR = L::UR;
+  constexpr int UR = L::UR, kWarps = L::kWarps, kConsumers = L::kConsumers, kFewThreads = L::kThreads;
+  auto sync_consumers = [] { sync_consumers_n<kConsumers>(); };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sbase = smem_u32(sm);
@@ -159,7 +172,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     prefetch_tensormap(&tmV);
     for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), kWarps);
+      mbar_init(empty(s), kGroups);
     }
     misc->abort = 0;
     mbar_fence_init();
@@ -303,18 +316,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   // and the rest of the range runs through on whatever the slots hold, so
   // every barrier is still met and every ticket still drawn.
   auto wait_full = [&](int s, int n) {
-    if (!*abort) mbar_wait_bounded(full(s), (n / L::kSlots) & 1, abort, a.wait_ns);
+    if (!mbar_try_wait(full(s), (n / L::kSlots) & 1) && !*abort)
+      mbar_wait_bounded(full(s), (n / L::kSlots) & 1, abort, a.wait_ns);
   };
   const int g = lane >> 2, c = lane & 3;
-  float* s_max = reinterpret_cast<float*>(fix + L::kMax);
-  float* s_sum = reinterpret_cast<float*>(fix + L::kSum);
+  float* s_o = reinterpret_cast<float*>(fix + L::kO);
+  float2* s_ml = reinterpret_cast<float2*>(fix + L::kMl);
   int4* s_row = reinterpret_cast<int4*>(fix + L::kRow);
-  const uint32_t sQ = fbase + L::kQ, sP = fbase + L::kP;
+  const uint32_t sQ = fbase + L::kQ;
   const float* sc = p.scales + (size_t)a.layer * 4 * p.Hkv;
   constexpr int kChunksQ = D / 8;                       // 16-byte chunks of a query row
-  constexpr int kDw = D == 128 ? 8 : 4;                 // warps that share the columns
-  const int dchunk = warp % kDw;                        // this warp's 16 columns
-  const int kk0 = D == 128 ? 0 : 4 * (warp / 4);   // its first 16-token step
+  constexpr bool kQRegs = MT == 1;                      // the query operand stays in registers
+  auto load_q = [&](int i, int ks, uint32_t (&qa)[4]) {
+    const int r = 16 * i + (lane & 15);
+    ldsm4(qa, sQ + r * (D * 2) + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
+  };
+  auto pack = [](float lo, float hi) {
+    if constexpr (E4M3) {
+      return f32x2_to_f16x2(lo, hi);
+    } else {
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+      return *reinterpret_cast<const uint32_t*>(&b2);
+    }
+  };
+  auto bf2 = [](float lo, float hi) {
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b2);
+  };
   int n = 0;
   while (x < stop) {
     const long long uend = ubase + rq.nt;
@@ -376,8 +404,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     }
     sync_consumers();
-    float m_run[2 * MT], l_run[2 * MT], fac[2 * MT];
-    float acc[MT][2][4];
+    uint32_t qreg[kQRegs ? D / 16 : 1][4];
+    if constexpr (kQRegs) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) load_q(0, ks, qreg[ks]);
+    }
+    float m_run[2 * MT], l_run[2 * MT], fac[2 * MT];     // rows 16 i + g and 16 i + 8 + g
+    float acc[MT][D / 8][4];
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
       m_run[i] = -INFINITY;
@@ -387,183 +420,209 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][0][e] = acc[i][1][e] = 0.f;
+      for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][k][e] = 0.f;
     // tokens that every row of the unit sees: tiles inside need no mask
     const int all_hi = s_row[0].y, all_lo = s_row[rows - 1].x;
 
-    for (int tile = rq.t0 + (int)(x - ubase); x < ue; ++x, ++tile) {
-      const int tok0 = tile * kTile;
-      // ---- scores of this warp's 16 tokens
+    int group = warp;                                    // this warp's group of the tile, if below kGroups
+    for (int tile = rq.t0 + (int)(x - ubase); x < ue; ++x, ++tile, group += group < kGroups ? kWarps - kGroups : -kGroups) {
+      const int tok0 = tile * kTile + group * 16;        // this warp's tokens
+      // ---- scores
       int s = n % L::kSlots;
       wait_full(s, n);
+      if (kWarps > kGroups && group >= kGroups) {
+        // another's tile: only waited for, so that this warp stays within a
+        // phase of every slot's barrier
+        wait_full((n + 1) % L::kSlots, n + 1);
+        n += 2;
+        continue;
+      }
       float sc_[MT][2][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc_[i][0][e] = sc_[i][1][e] = 0.f;
       const uint32_t sK = sbase + s * L::kSlot;
+      auto score_step = [&](int ks, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          if constexpr (kQRegs) {
+            mma16816<E4M3>(sc_[i][0], qreg[ks], b0, b1);
+            mma16816<E4M3>(sc_[i][1], qreg[ks], b2, b3);
+          } else {
+            uint32_t qa[4];
+            load_q(i, ks, qa);
+            mma16816<E4M3>(sc_[i][0], qa, b0, b1);
+            mma16816<E4M3>(sc_[i][1], qa, b2, b3);
+          }
+        }
+      };
       if constexpr (!E4M3) {
-        const int tok = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+        const int tok = group * 16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           uint32_t kb[4];
           const int ch = 2 * ks + ((lane >> 3) & 1);
           ldsm4(kb, sK + (ch >> 3) * (kTile * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint32_t qa[4];
-            const int r = 16 * i + (lane & 15);
-            ldsm4(qa, sQ + r * (D * 2) + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
-            mma16816<false>(sc_[i][0], qa, kb[0], kb[1]);
-            mma16816<false>(sc_[i][1], qa, kb[2], kb[3]);
-          }
+          score_step(ks, kb[0], kb[1], kb[2], kb[3]);
         }
       } else {
-        const int tok = warp * 16 + (lane & 15);
+        const int tok = group * 16 + (lane & 15);
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
           uint32_t kb[4];
           ldsm4(kb, sK + swz_offset(tok, 2 * k2 + (lane >> 4), D));
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int ks = 2 * k2 + half;
             uint32_t b[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              b[2 * e] = e4m3x2_to_f16x2((uint16_t)(kb[2 * half + e] & 0xFFFFu));
-              b[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)(kb[2 * half + e] >> 16));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              uint32_t qa[4];
-              const int r = 16 * i + (lane & 15);
-              ldsm4(qa, sQ + r * (D * 2) + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
-              mma16816<true>(sc_[i][0], qa, b[0], b[1]);
-              mma16816<true>(sc_[i][1], qa, b[2], b[3]);
-            }
+            for (int e = 0; e < 2; ++e) e4m3x4_to_f16x4(kb[2 * half + e], b[2 * e], b[2 * e + 1]);
+            score_step(2 * k2 + half, b[0], b[1], b[2], b[3]);
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
       ++n;
-      const bool masked = tok0 < all_lo || tok0 + kTile > all_hi;
+      // ---- probabilities, in the layout of the next product's operand
+      const bool masked = tok0 < all_lo || tok0 + 16 > all_hi;
+      uint32_t pa[MT][4];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
+          if (16 * i + 8 * hr >= rows) {                 // no such rows (the same for all threads)
+            pa[i][hr] = pa[i][2 + hr] = 0u;
+            continue;
+          }
           const float f = fac[2 * i + hr];
-          float mx = -INFINITY;
           int lo = 0, hi = INT32_MAX;
           if (masked) {
             const int4 ri = s_row[16 * i + 8 * hr + g];
             lo = ri.x;
             hi = ri.y;
           }
+          float mx = -INFINITY;
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float& v = sc_[i][nt][2 * hr + e];
-              const int tok = tok0 + warp * 16 + nt * 8 + 2 * c + e;
+              const int tok = tok0 + nt * 8 + 2 * c + e;
               v = tok >= lo && tok < hi ? v * f : -INFINITY;
               mx = fmaxf(mx, v);
             }
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-          if (c == 0) s_max[(16 * i + 8 * hr + g) * 8 + warp] = mx;
-        }
-      }
-      sync_consumers();
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          const int r = 16 * i + 8 * hr + g;
-          const float4 ma = *reinterpret_cast<const float4*>(s_max + r * 8);
-          const float4 mb = *reinterpret_cast<const float4*>(s_max + r * 8 + 4);
           float& mr = m_run[2 * i + hr];
-          const float m = fmaxf(fmaxf(fmax3(ma.x, ma.y, ma.z), fmax3(ma.w, mb.x, mb.y)), fmax3(mb.z, mb.w, mr));
-          const float mu = m == -INFINITY ? 0.f : m;      // nothing seen yet: p = 2^-inf = 0
-          const float alpha = ex2_approx(mr - mu);
+          const float m = fmaxf(mr, mx), mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
+          if (__any_sync(0xFFFFFFFFu, m > mr)) {
+            const float alpha = ex2_approx(mr - mu);
+            l_run[2 * i + hr] *= alpha;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              acc[i][k][2 * hr] *= alpha;
+              acc[i][k][2 * hr + 1] *= alpha;
+            }
+          }
           mr = m;
           float sum = 0.f;
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             const float p0 = ex2_approx(sc_[i][nt][2 * hr] - mu), p1 = ex2_approx(sc_[i][nt][2 * hr + 1] - mu);
             sum += p0 + p1;
-            uint32_t w;
-            if constexpr (E4M3) {
-              w = f32x2_to_f16x2(p0, p1);
-            } else {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-              w = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            const int ch = 2 * warp + nt;                 // 16-byte chunk of the probability row
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sP + r * (kTile * 2) + ((ch ^ (r & 7)) << 4) + 4 * c), "r"(w)
-                         : "memory");
+            pa[i][2 * nt + hr] = pack(p0, p1);
           }
-          l_run[2 * i + hr] = l_run[2 * i + hr] * alpha + sum;
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            acc[i][nt][2 * hr] *= alpha;
-            acc[i][nt][2 * hr + 1] *= alpha;
-          }
+          l_run[2 * i + hr] += sum;
         }
       }
-      sync_consumers();
-      // ---- values: this warp's 16 columns
+      // ---- values
       s = n % L::kSlots;
       wait_full(s, n);
       const uint32_t sV = sbase + s * L::kSlot;
-      // tokens that no row sees may hold anything: their values become zeros
-      const bool vmask = tok0 < rq.lo || tok0 + kTile > rq.hi;
-      auto keep = [&](uint32_t w, int tok) {              // (tok, tok + 1) in the halves of w
-        const uint32_t m0 = tok >= rq.lo && tok < rq.hi ? 0xFFFFu : 0u;
-        const uint32_t m1 = tok + 1 >= rq.lo && tok + 1 < rq.hi ? 0xFFFF0000u : 0u;
-        return w & (m0 | m1);
-      };
-      auto pv = [&](int kk, uint32_t (&b)[4]) {           // b0, b1 of the two column tiles
-        if (vmask) {
-          const int tok = tok0 + 16 * kk + 2 * c;
-          b[0] = keep(b[0], tok);
-          b[1] = keep(b[1], tok + 8);
-          b[2] = keep(b[2], tok);
-          b[3] = keep(b[3], tok + 8);
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          uint32_t pa[4];
-          const int r = 16 * i + (lane & 15);
-          ldsm4(pa, sP + r * (kTile * 2) + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4));
-          mma16816<E4M3>(acc[i][0], pa, b[0], b[1]);
-          mma16816<E4M3>(acc[i][1], pa, b[2], b[3]);
-        }
-      };
-      if constexpr (!E4M3) {
-#pragma unroll
-        for (int kq = 0; kq < (D == 128 ? 8 : 4); ++kq) {
-          const int kk = kk0 + kq;
-          const int tok = 16 * kk + (lane & 15), ch = 2 * dchunk + (lane >> 4);
-          uint32_t vb[4];
+      // 16 columns (two column tiles) of the warp's 16 tokens; columns of an
+      // E4M3 cache as 16 ch + 2 n + (0, 1) for column n of the two tiles
+      auto load_v = [&](int ch2, uint32_t (&vb)[4]) {    // ch2: 16-column group
+        const int tok = group * 16 + (lane & 15);
+        if constexpr (!E4M3) {
+          const int ch = 2 * ch2 + (lane >> 4);
           ldsm4t(vb, sV + (ch >> 3) * (kTile * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
-          pv(kk, vb);
+        } else {
+          uint32_t vr[2];
+          ldsm2t(vr, sV + swz_offset(tok, ch2, D));
+          // (token, column) 00 01 10 11 in the bytes of vr: token pairs per column
+#pragma unroll
+          for (int e = 0; e < 2; ++e) e4m3x4_to_f16x4(__byte_perm(vr[e], 0u, 0x3120), vb[e], vb[2 + e]);
+        }
+      };
+      // values of tokens outside [lo, hi) to zeros
+      auto hide = [&](uint32_t (&vb)[4], int lo, int hi) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = tok0 + 8 * (e & 1) + 2 * c;    // tokens tok, tok + 1 in the halves
+          vb[e] &= (tok >= lo && tok < hi ? 0xFFFFu : 0u) | (tok + 1 >= lo && tok + 1 < hi ? 0xFFFF0000u : 0u);
+        }
+      };
+      if (!masked) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t vb[4];
+          load_v(k, vb);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            mma16816<E4M3>(acc[i][2 * k], pa[i], vb[0], vb[1]);
+            mma16816<E4M3>(acc[i][2 * k + 1], pa[i], vb[2], vb[3]);
+          }
         }
       } else {
+        // What no row sees may hold anything and becomes zeros.  What some
+        // row sees may hold infinities or NaN that must not reach the others
+        // (0 x inf): then one product per row, over that row's tokens only.
+        bool wild = false;
+#pragma unroll 1
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t vb[4];
+          load_v(k, vb);
+          hide(vb, rq.lo, rq.hi);
+          constexpr uint32_t kExp = E4M3 ? 0x7C00u : 0x7F80u;
 #pragma unroll
-        for (int kq = 0; kq < (D == 128 ? 4 : 2); ++kq) {
-          const int kk = kk0 + 2 * kq;
-          uint32_t vr[4];
-          ldsm4t(vr, sV + swz_offset(16 * kk + lane, dchunk, D));
+          for (int e = 0; e < 4; ++e)
+            wild = wild || (vb[e] & kExp) == kExp || ((vb[e] >> 16) & kExp) == kExp;
+        }
+        wild = __any_sync(0xFFFFFFFFu, wild);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t vb[4];
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t vb[4];
+          load_v(k, vb);
+          hide(vb, rq.lo, rq.hi);
+          if (!wild) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              vb[2 * e] = e4m3x2_to_f16x2((uint16_t)__byte_perm(vr[2 * half], 0u, e ? 0x31 : 0x20));
-              vb[2 * e + 1] = e4m3x2_to_f16x2((uint16_t)__byte_perm(vr[2 * half + 1], 0u, e ? 0x31 : 0x20));
+            for (int i = 0; i < MT; ++i) {
+              mma16816<E4M3>(acc[i][2 * k], pa[i], vb[0], vb[1]);
+              mma16816<E4M3>(acc[i][2 * k + 1], pa[i], vb[2], vb[3]);
             }
-            pv(kk + half, vb);
+          } else {
+#pragma unroll 1
+            for (int r = 0; r < 16; ++r) {
+#pragma unroll
+              for (int i = 0; i < MT; ++i) {
+                const int4 ri = s_row[16 * i + r];
+                uint32_t wb[4] = {vb[0], vb[1], vb[2], vb[3]};
+                hide(wb, ri.x, ri.y);
+                float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<E4M3>(t0, pa[i], wb[0], wb[1]);
+                mma16816<E4M3>(t1, pa[i], wb[2], wb[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {            // e >> 1: the thread's row g or g + 8
+                  if (8 * (e >> 1) + g == r) {
+                    acc[i][2 * k][e] += t0[e];
+                    acc[i][2 * k + 1][e] += t1[e];
+                  }
+                }
+              }
+            }
           }
         }
       }
@@ -572,84 +631,75 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       ++n;
     }
 
-    // ---- end of the unit, or of this CTA's part of it
+    // ---- end of the unit, or of this CTA's part of it: merge the warps
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i) {
       float l = l_run[i];
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-      if (c == 0) s_sum[(8 * i + g) * 8 + warp] = l;
+      if (c == 0) s_ml[warp * UR + 8 * i + g] = make_float2(m_run[i], l);
     }
-    if constexpr (D == 64) {
-      // add the two token halves (through the probabilities' space)
-      sync_consumers();
-      float* half = reinterpret_cast<float*>(fix + L::kP);       // [UR][64]
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float* cell = half + (16 * i + 8 * (e >> 1) + g) * 64 + 16 * dchunk + nt * 8 + 2 * c + (e & 1);
-            if (warp >= 4) *cell = acc[i][nt][e];
-          }
-      sync_consumers();
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (warp < 4)
-              acc[i][nt][e] += half[(16 * i + 8 * (e >> 1) + g) * 64 + 16 * dchunk + nt * 8 + 2 * c + (e & 1)];
-    } else {
-      sync_consumers();
-    }
+    sync_consumers();
     const bool whole = ubase >= start && uend <= stop;
     const float scale_v = E4M3 ? __ldcg(sc + p.Hkv + h) : 1.0f;
-    // column of accumulator (nt, e): bf16 16 w + 8 nt + 2 c + e, E4M3 16 w + 4 c + 2 e + nt
     auto out_row = [&](int r) -> uint16_t* {
       const int row = r0 + r;
       return a.out + ((size_t)(rq.q0 + row / G) * p.Hq + h * G + row % G) * D;
     };
-    auto bf2 = [](float lo, float hi) {
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
-      return *reinterpret_cast<const uint32_t*>(&b2);
-    };
     const int part = 2 * blockIdx.x + (ubase < start ? 0 : 1);
+    auto row_max = [&](int r) {
+      float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w * UR + r].x);
+      return m;
+    };
+    // four rows at a time: every warp's O, scaled to the common maximum, into
+    // shared memory, then each thread adds them for two columns
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        const int r = 16 * i + 8 * hr + g;
-        if (r >= rows || (D == 64 && warp >= 4)) continue;
-        float l = 0.f;
+    for (int q4 = 0; q4 < UR / 4; ++q4) {
+      if (4 * q4 >= rows) break;
+      const int i = q4 / 4, hr = (q4 >> 1) & 1;          // the m tile, and which half of it
+      if ((g >> 2) == (q4 & 1)) {
+        const int r = 4 * q4 + (g & 3);
+        const float m = row_max(r), f = ex2_approx(m_run[2 * i + hr] - (m == -INFINITY ? 0.f : m));
+        float* o = s_o + (warp * 4 + (g & 3)) * D;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) l += s_sum[r * 8 + w];
-        float v0 = acc[i][0][2 * hr], v1 = acc[i][0][2 * hr + 1];
-        float v2 = acc[i][1][2 * hr], v3 = acc[i][1][2 * hr + 1];
-        if (whole) {
-          const float inv = l > 0.f || l != l ? scale_v / l : 0.f;
-          uint16_t* o = out_row(r) + 16 * dchunk;
+        for (int k = 0; k < D / 16; ++k) {
+          const float v0 = acc[i][2 * k][2 * hr] * f, v1 = acc[i][2 * k][2 * hr + 1] * f;
+          const float v2 = acc[i][2 * k + 1][2 * hr] * f, v3 = acc[i][2 * k + 1][2 * hr + 1] * f;
           if constexpr (E4M3) {
-            *reinterpret_cast<uint2*>(o + 4 * c) = make_uint2(bf2(v0 * inv, v2 * inv), bf2(v1 * inv, v3 * inv));
+            *reinterpret_cast<float4*>(o + 16 * k + 4 * c) = make_float4(v0, v2, v1, v3);
           } else {
-            *reinterpret_cast<uint32_t*>(o + 2 * c) = bf2(v0 * inv, v1 * inv);
-            *reinterpret_cast<uint32_t*>(o + 8 + 2 * c) = bf2(v2 * inv, v3 * inv);
+            *reinterpret_cast<float2*>(o + 16 * k + 2 * c) = make_float2(v0, v1);
+            *reinterpret_cast<float2*>(o + 16 * k + 8 + 2 * c) = make_float2(v2, v3);
           }
-        } else {
-          float* o = p.part_o + ((size_t)part * kPartRows + r) * D + 16 * dchunk;
-          if constexpr (E4M3) {
-            *reinterpret_cast<float4*>(o + 4 * c) = make_float4(v0, v2, v1, v3);
-          } else {
-            *reinterpret_cast<float2*>(o + 2 * c) = make_float2(v0, v1);
-            *reinterpret_cast<float2*>(o + 8 + 2 * c) = make_float2(v2, v3);
-          }
-          if (c == 0 && dchunk == 0)
-            *reinterpret_cast<float2*>(p.part_ml + ((size_t)part * kPartRows + r) * 2) =
-                make_float2(m_run[2 * i + hr], l);
         }
       }
+      sync_consumers();
+      for (int k = threadIdx.x; k < 4 * (D / 2); k += kConsumers) {
+        const int rr = k / (D / 2), d2 = k % (D / 2), r = 4 * q4 + rr;
+        if (r >= rows) break;
+        float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(s_o + (w * 4 + rr) * D + 2 * d2);
+          o.x += v.x;
+          o.y += v.y;
+        }
+        const float m = row_max(r), mu = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) l += s_ml[w * UR + r].y * ex2_approx(s_ml[w * UR + r].x - mu);
+        if (whole) {
+          const float inv = l > 0.f || l != l ? scale_v / l : 0.f;
+          *reinterpret_cast<uint32_t*>(out_row(r) + 2 * d2) = bf2(o.x * inv, o.y * inv);
+        } else {
+          *reinterpret_cast<float2*>(p.part_o + ((size_t)part * kPartRows + r) * D + 2 * d2) = o;
+          if (d2 == 0)
+            *reinterpret_cast<float2*>(p.part_ml + ((size_t)part * kPartRows + r) * 2) = make_float2(m, l);
+        }
+      }
+      sync_consumers();
     }
     if (!whole) {
       // CTAs whose ranges hold a tile of this unit: owner(t) is the last CTA
@@ -712,20 +762,17 @@ template <int D, bool E4M3>
 cudaError_t prepare_rows() {
   cudaError_t e = prepare_one<D, E4M3, 1>();
   if (e == cudaSuccess) e = prepare_one<D, E4M3, 2>();
-  if (e == cudaSuccess) e = prepare_one<D, E4M3, 4>();
   return e;
 }
 template <int D, bool E4M3, int MT>
 cudaError_t go(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s) {
-  return launch_pdl(k_paged_few<D, E4M3, MT>, dim3((unsigned)a.ctas), dim3(kFewThreads), FewLayout<D, E4M3, MT>::kBytes,
+  return launch_pdl(k_paged_few<D, E4M3, MT>, dim3((unsigned)a.ctas), dim3(FewLayout<D, E4M3, MT>::kThreads), FewLayout<D, E4M3, MT>::kBytes,
                     s, *tmK, *tmV, p, a);
 }
 template <int D, bool E4M3>
 cudaError_t go_rows(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a, int unit_rows,
                     cudaStream_t s) {
-  return unit_rows <= 16   ? go<D, E4M3, 1>(p, tmK, tmV, a, s)
-         : unit_rows <= 32 ? go<D, E4M3, 2>(p, tmK, tmV, a, s)
-                           : go<D, E4M3, 4>(p, tmK, tmV, a, s);
+  return unit_rows <= 16 ? go<D, E4M3, 1>(p, tmK, tmV, a, s) : go<D, E4M3, 2>(p, tmK, tmV, a, s);
 }
 
 }  // namespace

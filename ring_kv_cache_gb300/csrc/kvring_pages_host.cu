@@ -23,7 +23,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr unsigned long long kDefaultWaitNs = 1000000000ull;
-constexpr int kFewRows = 64;   // most query rows of a request for the kernel for few rows
+constexpr int kFewRows = 32;   // most query rows of a request for the kernel for few rows
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -359,9 +359,9 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   const int G = h->cfg.num_q_heads / h->cfg.num_kv_heads;
   const int64_t rows = (int64_t)h->max_new * G;
   const bool few = rows <= kFewRows || h->requests > 1, chunk = rows > kFewRows;
-  // in a batch with chunks, requests beyond one m = 16 row tile (two or four
-  // for many query heads per key/value head) go with the chunks
-  const int split_rows = G <= 16 ? 16 : (G <= 32 ? 32 : 64);
+  // in a batch with chunks, requests beyond one m = 16 row tile (two, with
+  // many query heads per key/value head) go with the chunks
+  const int split_rows = G <= 16 ? 16 : 32;
   CUtensorMap tmQ;
   if (chunk && !make_query_map(&tmQ, q, q_stride, n, h->cfg)) return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

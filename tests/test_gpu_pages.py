@@ -289,6 +289,47 @@ def test_queries_of_any_size(cache):
     close(out[2], want[2], 2.0 ** -7 * want[2].abs() + 1e-6)
 
 
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("d,hq,hkv,total,new,bad,window", [
+    (128, 4, 2, [300, 90], [5, 1], 297, 0), (64, 4, 4, [300, 90], [8, 1], 295, 0), (64, 12, 4, [400], [6], 197, 200),
+    (128, 4, 2, [300, 90], [200, 3], 250, 0), (64, 2, 1, [700], [300], 650, 0), (64, 2, 2, [900], [400], 350, 200),
+    (128, 5, 1, [400], [100], 390, 0)])
+def test_hidden_values_reach_no_row(d, hq, hkv, total, new, bad, window, cache, value):
+    """A key and a value of one token are not finite: the rows whose mask
+    hides it are as if it were not there, the others are not finite."""
+    if cache == "e4m3":
+        value = math.nan   # E4M3 has no infinities
+    p, s = filled(hq, hkv, d, 32, total, new, cache, seed=12)
+    page, off = int(p.tables[0, bad // 32]), bad % 32
+    want, tol = attention_64(p, s, window=window)
+    pos = torch.arange(total[0] - new[0], total[0], device="cuda")
+    sees = (pos >= bad) & ((pos < bad + window) if window else True)
+    assert bool(sees.any()) and not bool(sees.all())
+    c = p.v_cache(0)
+    for key in (False, True):
+        c = p.k_cache(0) if key else p.v_cache(0)
+        before = c[page, :, off].clone()
+        row = before.float()
+        row[:, 3] = value
+        c[page, :, off] = row.to(c.dtype)
+        out = p.attention(0, s["q"], window=window)
+        n = new[0]
+        close(out[:n][~sees], want[:n][~sees], tol[:n][~sees], "hidden")
+        close(out[n:], want[n:], tol[n:], "other requests")
+        if not key:
+            o = out[:n][sees]
+            assert not bool(torch.isfinite(o[..., 3]).any())
+            rest = [i for i in range(d) if i != 3]
+            close(o[..., rest], want[:n][sees][..., rest], tol[:n][sees][..., rest], "its other columns")
+            if value == math.inf:
+                assert bool((o[..., 3] == math.inf).all())
+        elif math.isnan(value):
+            assert bool(torch.isnan(out[:n][sees]).all())
+        c[page, :, off] = before
+    assert errors(p) == 0
+
+
 # --------------------------------------------------------------- together
 def plain_step(hist, qkv, cu, hq, hkv, d, pairing, wq, wk, cache, sk, sv):
     """One layer's step on host lists of (k, v) float64 per request."""
