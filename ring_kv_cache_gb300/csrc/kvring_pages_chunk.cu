@@ -38,6 +38,12 @@
 // f16 (K and V); over a bf16 cache they only touch tiles at the borders of
 // what a request may read, whose values at other places become zeros.
 //
+// A value that some rows of a unit see and others do not may be infinite or
+// NaN, and 0 x inf in the product would carry it into the rows that do not.
+// So the helpers, in tiles with a mask, put zeros in the place of such
+// values and mark the unit, and the rows that do see them add them to their
+// sums at the end (p inf = inf, p NaN = NaN for any probability).
+//
 // Queries over an E4M3 cache: f16 after scaling each row by a power of two
 // into [1, 2) at its largest value (bf16's 8 significant bits fit f16's 11).
 //
@@ -64,9 +70,9 @@ constexpr int kChunkSmem = 232448;
 template <int D, bool E4M3>
 struct ChunkLayout {
   // Over an E4M3 cache the helpers are a warpgroup of their own (warps
-  // 12-15, 11 idle), so that registers can move between warpgroups.
-  static constexpr int kWarpHelp = E4M3 ? 12 : 11;
-  static constexpr int kHelpers = E4M3 ? 4 : 1;                  // warps
+  // 12-15, those between idle), so that registers can move between warpgroups.
+  static constexpr int kWarpHelp = E4M3 ? 12 : (D == 128 ? 10 : 11);
+  static constexpr int kHelpers = E4M3 ? 4 : 12 - kWarpHelp;     // warps
   static constexpr int kThreads = 32 * (kWarpHelp + kHelpers);
   static constexpr int kAtom = kTile * 128;                      // 128 rows x 64 16-bit columns
   static constexpr int kAtoms = D / 64;
@@ -101,6 +107,8 @@ struct Unit {
   int part;        // workspace slot, if not
   int first, last; // the CTAs that share it
   int end;         // no unit follows
+  int table;       // the request's row of the block tables
+  int wild;        // a masked tile holds values that are not finite
 };
 
 struct ChunkMisc {
@@ -183,6 +191,27 @@ __device__ __forceinline__ void store_row32(uint16_t* dst, const float (&x)[32],
     for (int k = 0; k < 4; ++k)
       *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
   }
+}
+
+// Eight 16-bit values w = *at of a masked tile: zeros where no row may read, zeros in
+// the place of infinities and NaN (EXP: the exponent fields, ONE: their lowest
+// bits, so that the sum carries into bit 15 where a field is all ones).
+// Returns whether there were any of the latter.
+template <uint32_t EXP, uint32_t ONE>
+__device__ __forceinline__ uint32_t clean_values(uint4* at, uint4 w, bool inside) {
+  auto wild = [](uint32_t x) { return ((x & EXP) + ONE) & 0x80008000u; };
+  const uint32_t b = inside ? wild(w.x) | wild(w.y) | wild(w.z) | wild(w.w) : 0u;
+  if (!inside) {
+    *at = make_uint4(0u, 0u, 0u, 0u);
+  } else if (b) {
+    auto clean = [&](uint32_t& x) { x &= ~((wild(x) >> 15) * 0xFFFFu); };
+    clean(w.x);
+    clean(w.y);
+    clean(w.z);
+    clean(w.w);
+    *at = w;
+  }
+  return b;
 }
 
 template <int D, bool E4M3>
@@ -360,6 +389,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         u.tile0 = tile0;
         u.ntile = ntile;
         u.h = h;
+        u.table = end ? 0 : __ldcg(p.rows + b);
+        u.wild = 0;
         u.whole = ntile == nt;
         // the CTAs whose ranges hold a tile of this unit (the owner of place x
         // is the last CTA whose range starts at or before x)
@@ -454,12 +485,12 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       mbar_wait_bounded(bar(full[i % kRing]), (i / kRing) & 1, &no_abort, a.wait_ns);
     for (int i = nq - L::kQBufs < 0 ? 0 : nq - L::kQBufs; i < nq; ++i)
       mbar_wait_bounded(bar(misc->q_full[i % L::kQBufs]), (i / L::kQBufs) & 1, &no_abort, a.wait_ns);
-  } else if (warp == kWarpIssue || warp == kWarpIssue + 1) {
+  } else if (warp >= kWarpIssue && warp < kWarpIssue + L::kIssuers) {
     // ------------------------------------------------- MMA issuers
     // d = 64: a thread per group.  d = 128: one thread for both (two threads'
     // products interleave there, which cost 25 %), no commit between a
     // product and the next scores (each had cost 8 %).
-    if (lane == 0 && warp - kWarpIssue < L::kIssuers) {
+    if (lane == 0) {
       constexpr uint32_t idesc_qk = idesc_16(128, 128, false, !E4M3), idesc_pv = idesc_16(128, D, true, !E4M3);
       const uint64_t dq = smem_desc(sbase + L::kQ, 16, 1024, 2u), dk = smem_desc(sbase + L::kKV, 16, 1024, 2u);
       const uint64_t dv = smem_desc(sbase + L::kKV, (uint32_t)L::kAtom, 1024, 2u);
@@ -583,16 +614,6 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             w[i] = *reinterpret_cast<const uint4*>(src + swz_offset(k / CPR, k % CPR, D));
           }
           mbar_arrive(bar(misc->raw_empty[rs]));
-          if (j & 1) {   // values: what no row may read becomes zeros
-            const int t = (u.tile0 + (j >> 1)) * kTile;
-            if (t < u.vlo || t + kTile > u.vhi) {
-#pragma unroll
-              for (int i = 0; i < PER; ++i) {
-                const int tok = t + (ht + i * kHelpThreads) / CPR;
-                if (tok < u.vlo || tok >= u.vhi) w[i] = make_uint4(0u, 0u, 0u, 0u);
-              }
-            }
-          }
           wait(misc->empty[s], ((n / L::kSlots) & 1) ^ 1);
           uint8_t* dst = sm + L::kKV + s * L::kSlot;
 #pragma unroll
@@ -607,6 +628,20 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             *reinterpret_cast<uint4*>(atom + swz_offset(row, 2 * (c & 3) + 1, 128)) =
                 make_uint4(hv[4], hv[5], hv[6], hv[7]);
           }
+          if ((j & 1) && edge_tile(u, j >> 1)) {   // this thread's values again
+            uint32_t bad = 0;
+#pragma unroll 1
+            for (int k = 2 * ht; k < 2 * kTile * CPR; k += 2 * kHelpThreads) {
+              const int row = (k >> 1) / CPR, c = (k >> 1) % CPR, tok = (u.tile0 + (j >> 1)) * kTile + row;
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+{
+                uint4* at = reinterpret_cast<uint4*>(dst + (c >> 2) * L::kAtom + swz_offset(row, 2 * (c & 3) + e, 128));
+                bad |= clean_values<0x7C007C00u, 0x04000400u>(at, *at, tok >= u.vlo && tok < u.vhi);
+              }
+            }
+            if (bad) *const_cast<volatile int*>(&misc->u[uq].wild) = 1;
+          }
           fence_proxy_async_smem();
           mbar_arrive(bar(misc->ready[s]));
         }
@@ -618,10 +653,21 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           if ((j & 1) && edge_tile(u, j >> 1)) {
             uint8_t* v = sm + L::kKV + s * L::kSlot;
             const int t = (u.tile0 + (j >> 1)) * kTile;
-            for (int k = ht; k < kTile * L::kAtoms * 8; k += kHelpThreads) {
-              const int tok = t + ((k >> 3) & (kTile - 1));
-              if (tok < u.vlo || tok >= u.vhi) *reinterpret_cast<uint4*>(v + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t bad = 0;
+            constexpr int kBatch = 8;   // loads in flight
+#pragma unroll 1
+            for (int k0 = ht; k0 < kTile * L::kAtoms * 8; k0 += kBatch * kHelpThreads) {
+              uint4 w[kBatch];
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) w[i] = *reinterpret_cast<uint4*>(v + 16 * (k0 + i * kHelpThreads));
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i) {
+                const int k = k0 + i * kHelpThreads, tok = t + ((k >> 3) & (kTile - 1));
+                bad |= clean_values<0x7F807F80u, 0x00800080u>(reinterpret_cast<uint4*>(v + 16 * k), w[i],
+                                                              tok >= u.vlo && tok < u.vhi);
+              }
             }
+            if (bad) *const_cast<volatile int*>(&misc->u[uq].wild) = 1;
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -880,6 +926,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           if (row == 0) *ticket = 0;
           weigh();
         }
+        const bool is_wild = *const_cast<const volatile int*>(&u.wild);
         float4* o32 = reinterpret_cast<float4*>(p.part_o + ((size_t)u.part * kPartRows + g * kTile) * D) + row;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -887,6 +934,25 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           __syncwarp();
           tmem_ld32(tO + 32 * c, rr);
           tmem_wait_ld();
+          if (is_wild && live) {
+            // the values that are not finite among those this row sees
+            for (int j = 0; j < ntile; ++j) {
+              if (!edge_tile(u, j)) continue;
+              const int t = (u.tile0 + j) * kTile;
+              for (int k = lo > t ? lo : t; k < hi && k < t + kTile; ++k) {
+                const int page = __ldcg(p.tables + (size_t)u.table * p.W + (k >> p.logP));
+                if (page < 0 || page >= p.num_pages) continue;
+                const size_t at =
+                    (((((size_t)a.layer * p.num_pages + page) * p.Hkv + u.h) << p.logP) + (k & (p.P - 1))) * D + 32 * c;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const float x = E4M3 ? e4m3x2_to_f32x2(p.v[at + e]).x
+                                       : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.v)[at + e] << 16);
+                  if (!isfinite(x)) rr[e] = __float_as_uint(__uint_as_float(rr[e]) + x);
+                }
+              }
+            }
+          }
           if (!whole && !merge_now) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
