@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
+  int nfree = __ldcg(p.state + PST_FREE);
   unsigned long long carry = 0;
   for (int base = 0; base < B; base += kPlanThreads) {
     const int i = base + threadIdx.x;
@@ -123,7 +124,6 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   const unsigned long long tokens64 = carry & ((1ull << kTokBits) - 1);
   const int taken = (int)(carry >> kTokBits);
-  int nfree = __ldcg(p.state + PST_FREE);
   nfree = nfree < 0 ? 0 : (nfree > p.num_pages ? p.num_pages : nfree);
   if (threadIdx.x == 0) {
     s_cu[B] = (int32_t)(tokens64 & 0x7FFFFFFFull);

@@ -90,7 +90,8 @@ struct ChunkLayout {
   static constexpr int kKV = kQBufs * 2 * kQGroup;
   static constexpr int kRawAt = kKV + kSlots * kSlot;
   static constexpr int kMisc = kRawAt + kRaws * kRaw;
-  static constexpr int kBytes = 1024 + kMisc + 1024;
+  static constexpr int kMiscBytes = 1536;
+  static constexpr int kBytes = 1024 + kMisc + kMiscBytes;
   static_assert(kBytes <= kChunkSmem, "fits one CTA per SM");
 };
 
@@ -111,6 +112,28 @@ struct Unit {
   int wild;        // a masked tile holds values that are not finite
 };
 
+// The words of the step that describe a request, and what follows from them.
+struct ChunkWords {
+  int q0, end, klen, row;
+};
+__device__ __forceinline__ ChunkWords load_chunk_words(const PagesDev& p, int b) {
+  return ChunkWords{__ldcg(p.cu + b), __ldcg(p.cu + b + 1), __ldcg(p.klen + b), __ldcg(p.rows + b)};
+}
+struct ChunkReq {
+  int q0, nq, klen, pos0, nrt, row;
+};
+__device__ __forceinline__ ChunkReq make_chunk_req(const PagedAttn& a, const ChunkWords& w, int G, int tpu) {
+  ChunkReq r;
+  r.q0 = w.q0;
+  r.row = w.row;
+  r.klen = w.klen;
+  r.pos0 = r.klen - (w.end - r.q0);
+  r.nq = (w.end < a.T ? w.end : a.T) - r.q0;
+  const long long rows = (long long)(w.end - r.q0) * G;
+  if (r.nq < 0 || r.klen <= 0 || rows <= a.min_rows || rows > a.max_rows) r.nq = 0;
+  r.nrt = (r.nq + tpu - 1) / tpu;
+  return r;
+}
 struct ChunkMisc {
   uint64_t u_full[kUnitQueue], u_empty[kUnitQueue];
   uint64_t q_full[2], q_ready[2], q_empty[2];
@@ -123,27 +146,12 @@ struct ChunkMisc {
   unsigned long long ws[16];
   long long total, base;
   Unit u[kUnitQueue];
+  ChunkReq rq;   // the request the CTA starts in
   uint32_t tmem;
   int b0, rt0, parts, abort, last[2];
 };
-static_assert(sizeof(ChunkMisc) <= 1024, "misc block");
+static_assert(sizeof(ChunkMisc) <= ChunkLayout<128, false>::kMiscBytes, "misc block");
 
-struct ChunkReq {
-  int q0, nq, klen, pos0, nrt;
-};
-
-__device__ __forceinline__ ChunkReq load_chunk_req(const PagesDev& p, const PagedAttn& a, int b, int G, int tpu) {
-  ChunkReq r;
-  r.q0 = __ldcg(p.cu + b);
-  const int end = __ldcg(p.cu + b + 1);
-  r.klen = __ldcg(p.klen + b);
-  r.pos0 = r.klen - (end - r.q0);
-  r.nq = (end < a.T ? end : a.T) - r.q0;
-  if (r.nq < 0 || r.klen <= 0 || (end - r.q0) * (long long)G <= a.min_rows || (end - r.q0) * (long long)G > a.max_rows)
-    r.nq = 0;
-  r.nrt = (r.nq + tpu - 1) / tpu;
-  return r;
-}
 // The key tiles [t0, t0 + nt) of row tile rt.
 __device__ __forceinline__ int chunk_tiles(const PagedAttn& a, const ChunkReq& r, int rt, int tpu, int* t0) {
   const int i0 = rt * tpu, i1 = i0 + tpu < r.nq ? i0 + tpu : r.nq;
@@ -267,14 +275,17 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
   griddep_launch_dependents();
 
   // ------------------------------------------------- this CTA's range
+  // (the words of the first requests are asked for together with their count)
+  const ChunkWords first_words = load_chunk_words(p, (int)threadIdx.x < p.R ? threadIdx.x : 0);
   const int B = __ldcg(p.state + PST_REQUESTS);
   {
     const int per = (B + kThreads - 1) / kThreads;
     const int i0 = threadIdx.x * per, i1 = i0 + per < B ? i0 + per : B;
+    auto req_of = [&](int i) { return make_chunk_req(a, per == 1 ? first_words : load_chunk_words(p, i), G, tpu); };
     unsigned long long mine = 0;
     int t0;
     for (int i = i0; i < i1; ++i) {
-      const ChunkReq r = load_chunk_req(p, a, i, G, tpu);
+      const ChunkReq r = req_of(i);
       for (int rt = 0; rt < r.nrt; ++rt) mine += (unsigned)(kUnitCost + chunk_tiles(a, r, rt, tpu, &t0));
     }
     unsigned long long x = mine;
@@ -299,11 +310,12 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     if (mine && start >= before && start < before + mine) {   // exactly one thread, unless total is 0
       bool found = false;
       for (int i = i0; i < i1 && !found; ++i) {
-        const ChunkReq r = load_chunk_req(p, a, i, G, tpu);
+        const ChunkReq r = req_of(i);
         for (int rt = 0; rt < r.nrt; ++rt) {
           const unsigned long long n = (unsigned long long)(kUnitCost + chunk_tiles(a, r, rt, tpu, &t0)) * (unsigned)p.Hkv;
           if (start < before + n) {
             misc->b0 = i;
+            misc->rq = r;
             misc->rt0 = rt;
             misc->base = (long long)before;
             found = true;
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     constexpr int kRingAt = E4M3 ? L::kRawAt : L::kKV, kRingSize = E4M3 ? L::kRaw : L::kSlot;
     bool stopped = a.debug_stall;
     int b = misc->b0, rt = misc->rt0, t0;
-    ChunkReq rq = load_chunk_req(p, a, b, G, tpu);
+    ChunkReq rq = misc->rq;
     int nt = chunk_tiles(a, rq, rt, tpu, &t0);
     int h = (int)((start - misc->base) / (nt + kUnitCost));
     long long ubase = misc->base + (long long)h * (nt + kUnitCost), x = start;   // x: next place of the range
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         u.tile0 = tile0;
         u.ntile = ntile;
         u.h = h;
-        u.table = end ? 0 : __ldcg(p.rows + b);
+        u.table = rq.row;
         u.wild = 0;
         u.whole = ntile == nt;
         // the CTAs whose ranges hold a tile of this unit (the owner of place x
@@ -401,7 +413,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       }
       __syncwarp();
       if (end) break;
-      const int32_t* tab = p.tables + (size_t)__ldcg(p.rows + b) * p.W;
+      const int32_t* tab = p.tables + (size_t)rq.row * p.W;
       const int hi_u = a.causal ? rq.pos0 + i0 + ntok : rq.klen;   // what the unit's rows see
       int lo_u = a.window > 0 ? rq.pos0 + i0 + 1 - a.window : 0;
       lo_u = lo_u > 0 ? lo_u : 0;
@@ -472,7 +484,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           h = 0;
           if (++rt >= rq.nrt) {
             rt = 0;
-            do rq = load_chunk_req(p, a, ++b, G, tpu);
+            do rq = make_chunk_req(a, load_chunk_words(p, ++b), G, tpu);
             while (rq.nrt == 0);
           }
           nt = chunk_tiles(a, rq, rt, tpu, &t0);

@@ -70,12 +70,23 @@ struct FewLayout {
   static_assert(kSlots >= 4, "two tiles in flight");
 };
 
+// What a unit of a request needs to know.
+struct Req {
+  int q0, nq, klen;    // first token, tokens (that the tensors hold), length
+  int pos0;            // position of the first token
+  int nrows, nrt;      // query rows, row tiles
+  int lo, hi;          // tokens any row sees: [lo, hi)
+  int t0, nt;          // their tiles
+  int row;             // of the block tables
+};
+
 struct FewMisc {
   uint64_t full[16];
   uint64_t empty[16];
   unsigned long long ws[16];
   long long total;
   long long base;    // tiles before the request the CTA starts in
+  Req rq;            // that request
   int b0;
   int parts;         // CTAs that have a range
   int abort;
@@ -116,26 +127,25 @@ __device__ __forceinline__ void sync_consumers_n() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
-// What a unit of a request needs to know.
-struct Req {
-  int q0, nq, klen;    // first token, tokens (that the tensors hold), length
-  int pos0;            // position of the first token
-  int nrows, nrt;      // query rows, row tiles
-  int lo, hi;          // tokens any row sees: [lo, hi)
-  int t0, nt;          // their tiles
+// The words of the step that describe request b.
+struct ReqWords {
+  int q0, end, klen, row;
 };
+__device__ __forceinline__ ReqWords load_words(const PagesDev& p, int b) {
+  return ReqWords{__ldcg(p.cu + b), __ldcg(p.cu + b + 1), __ldcg(p.klen + b), __ldcg(p.rows + b)};
+}
 
 template <int UR>
-__device__ __forceinline__ Req load_req(const PagesDev& p, const PagedAttn& a, int b, int G) {
+__device__ __forceinline__ Req make_req(const PagedAttn& a, const ReqWords& w, int G) {
   Req r;
-  r.q0 = __ldcg(p.cu + b);
-  const int end = __ldcg(p.cu + b + 1);
-  r.klen = __ldcg(p.klen + b);
-  r.pos0 = r.klen - (end - r.q0);
-  r.nq = (end < a.T ? end : a.T) - r.q0;
+  r.q0 = w.q0;
+  r.row = w.row;
+  r.klen = w.klen;
+  r.pos0 = r.klen - (w.end - r.q0);
+  r.nq = (w.end < a.T ? w.end : a.T) - r.q0;
   if (r.nq < 0) r.nq = 0;
   r.nrows = r.nq * G;
-  const long long all = (long long)(end - r.q0) * G;
+  const long long all = (long long)(w.end - r.q0) * G;
   if (all <= a.min_rows || all > a.max_rows || r.klen <= 0) r.nrows = 0;
   r.nrt = (r.nrows + UR - 1) / UR;
   r.hi = r.klen;
@@ -181,14 +191,18 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
   griddep_launch_dependents();
 
   // ------------------------------------------------- this CTA's range
+  // Each thread sums the tiles (of one head) of its requests, then one block
+  // scan.  The words of the first requests are asked for together with the
+  // request count (the arrays are max_requests long).
+  const ReqWords ahead = load_words(p, (int)threadIdx.x < p.R ? threadIdx.x : 0);
   const int B = __ldcg(p.state + PST_REQUESTS);
   {
-    // tiles (of one head) of each thread's requests, then one block scan
     const int per = (B + kFewThreads - 1) / kFewThreads;
     const int i0 = threadIdx.x * per, i1 = i0 + per < B ? i0 + per : B;
+    auto req_of = [&](int i) { return make_req<UR>(a, per == 1 ? ahead : load_words(p, i), G); };
     unsigned long long mine = 0;
     for (int i = i0; i < i1; ++i) {
-      const Req r = load_req<UR>(p, a, i, G);
+      const Req r = req_of(i);
       mine += (unsigned long long)r.nrt * (unsigned)r.nt;
     }
     unsigned long long x = mine;
@@ -215,8 +229,8 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     if (mine && start >= before && start < before + mine) {   // exactly one thread, unless total is 0
       int i = i0;
       for (; i < i1; ++i) {
-        const Req r = load_req<UR>(p, a, i, G);
-        const unsigned long long n = (unsigned long long)r.nrt * (unsigned)r.nt * (unsigned)p.Hkv;
+        misc->rq = req_of(i);
+        const unsigned long long n = (unsigned long long)misc->rq.nrt * (unsigned)misc->rq.nt * (unsigned)p.Hkv;
         if (start < before + n) break;
         before += n;
       }
@@ -236,7 +250,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
 
   // The walk over units, the same in the producer and the consumers.
   int b = misc->b0;
-  Req rq = load_req<UR>(p, a, b, G);
+  Req rq = misc->rq;
   long long x = start;                       // next tile of the flattened space
   long long ubase;                           // first tile of the current unit
   int rt, h;
@@ -253,7 +267,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     h = 0;
     if (++rt < rq.nrt) return;
     rt = 0;
-    do rq = load_req<UR>(p, a, ++b, G);
+    do rq = make_req<UR>(a, load_words(p, ++b), G);
     while (rq.nt == 0);                      // (some request follows: x < stop)
   };
 
@@ -269,7 +283,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     bool stopped = a.debug_stall;            // a wait gave up (or test support: nothing is copied)
     while (x < stop && !stopped) {
       long long ue = ubase + rq.nt;
-      const int32_t* tab = p.tables + (size_t)__ldcg(p.rows + b) * p.W;
+      const int32_t* tab = p.tables + (size_t)rq.row * p.W;
       ue = ue < stop ? ue : stop;
       // one lane per page piece; the next tile's page id is read a tile ahead
       int tile = rq.t0 + (int)(x - ubase);
