@@ -57,23 +57,35 @@
 namespace kvr {
 namespace {
 
-constexpr int kWarpCopy = 8, kWarpIssue = 9;
 constexpr int kUnitQueue = 4;
 // A unit's start and end cost about as much as this many of its tiles (its
 // queries' way to the tensor cores, the last probabilities' and the results'
 // way out); ranges are cut by tiles plus this.
 constexpr int kUnitCost = 3;
+constexpr int kTileBits = 40;     // of the sums over requests: places in the low bits, units above
 constexpr float kRaise = 8.0f;    // log2 units
 constexpr float kShift = 7.0f;
 constexpr int kChunkSmem = 232448;
 
 template <int D, bool E4M3>
 struct ChunkLayout {
-  // Over an E4M3 cache the helpers are a warpgroup of their own (warps
-  // 12-15, those between idle), so that registers can move between warpgroups.
-  static constexpr int kWarpHelp = E4M3 ? 12 : (D == 128 ? 10 : 11);
-  static constexpr int kHelpers = E4M3 ? 4 : 12 - kWarpHelp;     // warps
+  // Streams: a row group's 128 rows, and at d = 64 half of each tile's tokens.
+  static constexpr int kHalves = D == 128 ? 1 : 2;               // token halves of a tile
+  static constexpr int kStreams = 2 * kHalves;
+  static constexpr int kCols = kTile / kHalves;                  // tokens of a stream's tile
+  static constexpr int kIssuers = kHalves;                       // MMA-issuing threads, two streams each
+  static constexpr int kSoftWarps = 4 * kStreams;
+  static constexpr int kSoftThreads = 32 * kSoftWarps;
+  static constexpr int kWarpCopy = kSoftWarps, kWarpIssue = kSoftWarps + 1;
+  // Over an E4M3 cache the helpers are a warpgroup of their own (with idle
+  // warps before them), so that registers can move between warpgroups.
+  static constexpr int kWarpHelp = E4M3 ? kSoftWarps + 4 : kWarpIssue + kIssuers;
+  static constexpr int kHelpers = E4M3 ? 4 : kSoftWarps + 4 - kWarpHelp;   // warps
   static constexpr int kThreads = 32 * (kWarpHelp + kHelpers);
+  // Registers per thread after the split (0: none): the sum over all threads
+  // stays that of the launch (128 x 512, 96 x 640, 80 x 768).
+  static constexpr int kRegsSoft = D == 128 ? (E4M3 ? 176 : 0) : (E4M3 ? 96 : 104);
+  static constexpr int kRegsRest = D == 128 ? (E4M3 ? 80 : 0) : (E4M3 ? 48 : 64);
   static constexpr int kAtom = kTile * 128;                      // 128 rows x 64 16-bit columns
   static constexpr int kAtoms = D / 64;
   static constexpr int kQGroup = kAtoms * kAtom;
@@ -82,16 +94,16 @@ struct ChunkLayout {
   static constexpr int kSlots = D == 128 ? (E4M3 ? 3 : 5) : (E4M3 ? 7 : 9);
   static constexpr int kRaws = E4M3 ? (D == 128 ? 4 : 5) : 0;
   static constexpr int kQBufs = D == 128 ? 1 : 2;                // units whose queries fit
-  static constexpr bool kOwnP = D == 64;                         // P has columns of its own
-  static constexpr int kIssuers = kOwnP ? 2 : 1;                 // MMA-issuing threads
-  static constexpr uint32_t kColO = 256, kColOStep = D == 128 ? 128 : 64;
-  static constexpr uint32_t kColP = kOwnP ? 384 : 0, kColPStep = kOwnP ? 64 : 128;
+  // TMEM columns of stream i: scores (the probabilities over them), sums
+  static constexpr uint32_t col_s(int i) { return 128 * i; }
+  static constexpr uint32_t col_o(int i) { return D == 128 ? 256 + 128 * i : 128 * i + 64; }
   static constexpr int kQ = 0;
   static constexpr int kKV = kQBufs * 2 * kQGroup;
   static constexpr int kRawAt = kKV + kSlots * kSlot;
   static constexpr int kMisc = kRawAt + kRaws * kRaw;
   static constexpr int kMiscBytes = 1536;
-  static constexpr int kBytes = 1024 + kMisc + kMiscBytes;
+  static constexpr int kMl = kMisc + kMiscBytes;                 // float2 [2][halves][128]: their maxima and sums
+  static constexpr int kBytes = 1024 + kMl + (kHalves > 1 ? 2 * kHalves * kTile * 8 : 0);
   static_assert(kBytes <= kChunkSmem, "fits one CTA per SM");
 };
 
@@ -137,13 +149,14 @@ __device__ __forceinline__ ChunkReq make_chunk_req(const PagedAttn& a, const Chu
 struct ChunkMisc {
   uint64_t u_full[kUnitQueue], u_empty[kUnitQueue];
   uint64_t q_full[2], q_ready[2], q_empty[2];
-  // s_free: the scores are in registers (kOwnP); pv: P_g V has finished
-  uint64_t s_full[2], s_free[2], p_full[2], pv[2], o_free[2];
+  // of a stream: scores there, probabilities there, its last product done
+  // (pv), its sums read
+  uint64_t s_full[4], p_full[4], pv[4], o_free[4];
   // ring slots: the copy landed (bf16 only), the helpers are done with it,
   // its MMAs have read it; and the E4M3 tiles before they are widened
   uint64_t full[11], ready[11], empty[11], raw_full[6], raw_empty[6];
   uint64_t done[2], grp[2];
-  unsigned long long ws[16];
+  unsigned long long ws[24];
   long long total, base;
   Unit u[kUnitQueue];
   ChunkReq rq;   // the request the CTA starts in
@@ -245,17 +258,18 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     prefetch_tensormap(&tmV);
     for (int i = 0; i < kUnitQueue; ++i) {
       mbar_init(bar(misc->u_full[i]), 1);
-      mbar_init(bar(misc->u_empty[i]), 8 + L::kIssuers + L::kHelpers);
+      mbar_init(bar(misc->u_empty[i]), L::kSoftWarps + L::kIssuers + L::kHelpers);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(bar(misc->q_full[g]), 1);
-      mbar_init(bar(misc->q_ready[g]), 256);
+      mbar_init(bar(misc->q_ready[g]), L::kSoftThreads);
       mbar_init(bar(misc->q_empty[g]), L::kIssuers);
-      mbar_init(bar(misc->s_full[g]), 1);
-      mbar_init(bar(misc->s_free[g]), 4);
-      mbar_init(bar(misc->p_full[g]), 4);
-      mbar_init(bar(misc->pv[g]), 1);
-      mbar_init(bar(misc->o_free[g]), 4);
+    }
+    for (int i = 0; i < L::kStreams; ++i) {
+      mbar_init(bar(misc->s_full[i]), 1);
+      mbar_init(bar(misc->p_full[i]), 4);
+      mbar_init(bar(misc->pv[i]), 1);
+      mbar_init(bar(misc->o_free[i]), 4 * L::kHalves);
     }
     for (int i = 0; i < L::kSlots; ++i) {
       mbar_init(bar(misc->full[i]), 1);
@@ -267,7 +281,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       mbar_init(bar(misc->raw_empty[i]), kHelpThreads);
     }
     for (int g = 0; g < 2; ++g) mbar_init(bar(misc->done[g]), 1);
-    for (int g = 0; g < 2; ++g) mbar_init(bar(misc->grp[g]), 128);
+    for (int g = 0; g < 2; ++g) mbar_init(bar(misc->grp[g]), kTile * L::kHalves);
     misc->abort = 0;
     mbar_fence_init();
   }
@@ -287,6 +301,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     for (int i = i0; i < i1; ++i) {
       const ChunkReq r = req_of(i);
       for (int rt = 0; rt < r.nrt; ++rt) mine += (unsigned)(kUnitCost + chunk_tiles(a, r, rt, tpu, &t0));
+      mine += (unsigned long long)r.nrt << kTileBits;
     }
     unsigned long long x = mine;
 #pragma unroll
@@ -301,10 +316,15 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       if (w < warp) before += misc->ws[w];
       total += misc->ws[w];
     }
-    total *= (unsigned)p.Hkv;
-    before = (before + x - mine) * (unsigned)p.Hkv;
-    mine *= (unsigned)p.Hkv;
+    constexpr unsigned long long kTiles = (1ull << kTileBits) - 1;
+    const unsigned long long units = (total >> kTileBits) * (unsigned)p.Hkv;
+    total = (total & kTiles) * (unsigned)p.Hkv;
+    before = ((before + x - mine) & kTiles) * (unsigned)p.Hkv;
+    mine = (mine & kTiles) * (unsigned)p.Hkv;
+    // a range per CTA; shorter than min_tiles only where that keeps as many
+    // ranges as there are units
     unsigned long long parts = total / (unsigned)a.min_tiles;
+    parts = parts > units ? parts : units;
     parts = parts < 1 ? 1 : (parts > gridDim.x ? gridDim.x : parts);
     const unsigned long long start = blockIdx.x < parts ? total * blockIdx.x / parts : total;
     if (mine && start >= before && start < before + mine) {   // exactly one thread, unless total is 0
@@ -334,7 +354,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
   const long long total = misc->total, parts = misc->parts;
   const long long start = total * blockIdx.x / parts, stop = total * (blockIdx.x + 1) / parts;
   if (blockIdx.x >= parts || start >= stop) return;
-  if (warp == kWarpIssue) {
+  if (warp == L::kWarpIssue) {
     tmem_alloc(smem_u32(&misc->tmem), 512);
     tmem_relinquish();
   }
@@ -351,11 +371,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     return t + kTile > seen || t < from;
   };
 
-  // Over an E4M3 cache 512 threads x 128 registers become 256 x 176 for the
-  // softmax and 256 x 80 for the rest (65,536 in all, before and after).
-  if (warp >= 8) {
-    if constexpr (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-  if (warp == kWarpCopy) {
+  if (warp >= L::kSoftWarps) {
+    if constexpr (L::kRegsRest) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsRest ? L::kRegsRest : 24));
+  if (warp == L::kWarpCopy) {
     // ------------------------------------------------------------ copies
     const int box_rows = p.P < kTile ? p.P : kTile, nbox = kTile / box_rows;
     constexpr int kBoxes = E4M3 ? 1 : L::kAtoms;
@@ -497,37 +515,44 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       mbar_wait_bounded(bar(full[i % kRing]), (i / kRing) & 1, &no_abort, a.wait_ns);
     for (int i = nq - L::kQBufs < 0 ? 0 : nq - L::kQBufs; i < nq; ++i)
       mbar_wait_bounded(bar(misc->q_full[i % L::kQBufs]), (i / L::kQBufs) & 1, &no_abort, a.wait_ns);
-  } else if (warp >= kWarpIssue && warp < kWarpIssue + L::kIssuers) {
+  } else if (warp >= L::kWarpIssue && warp < L::kWarpIssue + L::kIssuers) {
     // ------------------------------------------------- MMA issuers
-    // d = 64: a thread per group.  d = 128: one thread for both (two threads'
-    // products interleave there, which cost 25 %), no commit between a
-    // product and the next scores (each had cost 8 %).
+    // One thread issues for two streams: both row groups at d = 128 (with a
+    // thread for each, their products interleave, which cost 25 %), the two
+    // token halves of a group at d = 64.  Commits are few and none lies
+    // between a product and the next scores, where each cost 8 %.
     if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_16(128, 128, false, !E4M3), idesc_pv = idesc_16(128, D, true, !E4M3);
+      const int who = warp - L::kWarpIssue;
+      constexpr uint32_t idesc_qk = idesc_16(128, L::kCols, false, !E4M3), idesc_pv = idesc_16(128, D, true, !E4M3);
       const uint64_t dq = smem_desc(sbase + L::kQ, 16, 1024, 2u), dk = smem_desc(sbase + L::kKV, 16, 1024, 2u);
       const uint64_t dv = smem_desc(sbase + L::kKV, (uint32_t)L::kAtom, 1024, 2u);
       constexpr uint32_t kSlotStep = L::kSlot >> 4, kQStep = L::kQGroup >> 4, kAtomStep = L::kAtom >> 4;
+      constexpr uint32_t kHalfStep = L::kCols * 128 >> 4;   // a half's rows of a K or V tile
       const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32);
       const uint32_t k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
       int n = 0;   // slots so far
       auto slot_ready = [&](int i) { wait(misc->ready[i % L::kSlots], (i / L::kSlots) & 1); };
-      auto qk = [&](int g, int slot, uint32_t q_at) {
+      // i: 0 or 1 of this thread's streams
+      auto qk = [&](int i, int slot, uint32_t q_at) {
+        const int g = L::kHalves == 1 ? i : who;
+        const uint32_t k_at = k_lo + slot * kSlotStep + (L::kHalves == 1 ? 0 : i * kHalfStep);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ss(tmem + 128 * g, q_at + g * kQStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), q_hi,
-                     k_lo + slot * kSlotStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), k_hi, idesc_qk, kk != 0);
-        mma_commit(bar(misc->s_full[g]));
+          mma_f16_ss(tmem + L::col_s(2 * who + i), q_at + g * kQStep + (kk >> 2) * kAtomStep + 2 * (kk & 3), q_hi,
+                     k_at + (kk >> 2) * kAtomStep + 2 * (kk & 3), k_hi, idesc_qk, kk != 0);
+        mma_commit(bar(misc->s_full[2 * who + i]));
       };
-      auto pv = [&](int g, int slot, bool first) {
+      auto pv = [&](int i, int slot, bool first) {
+        const uint32_t v_at = v_lo + slot * kSlotStep + (L::kHalves == 1 ? 0 : i * kHalfStep);
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts_w(tmem + L::kColO + L::kColOStep * g, tmem + L::kColP + L::kColPStep * g + 8 * kk,
-                       v_lo + slot * kSlotStep + kk * 128, v_hi, idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < L::kCols / 16; ++kk)
+          mma_f16_ts_w(tmem + L::col_o(2 * who + i), tmem + L::col_s(2 * who + i) + 8 * kk, v_at + kk * 128, v_hi,
+                       idesc_pv, (!first || kk > 0) ? 1u : 0u);
       };
       auto free_slot = [&](int slot) { mma_commit(bar(misc->empty[slot])); };
-      int np[2] = {0, 0}, no[2] = {0, 0}, ns[2] = {0, 0};   // each group's P V, units, Q K so far
+      int np[2] = {0, 0}, no[2] = {0, 0};   // each stream's products and units so far
       for (int nu = 0;; ++nu) {
         const int uq = nu % kUnitQueue;
         wait(misc->u_full[uq], (nu / kUnitQueue) & 1);
@@ -536,55 +561,35 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         const int qb = nu % L::kQBufs;
         const uint32_t q_at = q_lo + 2 * qb * kQStep;
         wait(E4M3 ? misc->q_ready[qb] : misc->q_full[qb], (nu / L::kQBufs) & 1);
-        const int last = n + 2 * u.ntile - 1;
-        if constexpr (L::kOwnP) {
-          const int g = warp - kWarpIssue;
-          if (g == 1 && u.ntok <= TG) {
-            // no rows for this group: pass everything on as it comes
-            mbar_arrive(bar(misc->q_empty[qb]));
-            for (; n <= last; ++n) {
-              slot_ready(n);
-              mbar_arrive(bar(misc->empty[n % L::kSlots]));
-            }
-          } else {
-            auto scores = [&](int i) {   // of the tile in place i
-              slot_ready(i);
-              wait(misc->s_free[g], (ns[g]++ & 1) ^ 1);
-              qk(g, i % L::kSlots, q_at);
-              free_slot(i % L::kSlots);
-              if (i + 1 == last) mma_commit(bar(misc->q_empty[qb]));
-            };
-            scores(n);
-            for (int j = 0; j < u.ntile; ++j, n += 2) {
-              if (n + 2 < last) scores(n + 2);
-              slot_ready(n + 1);
-              wait(misc->p_full[g], np[g]++ & 1);
-              if (j == 0) wait(misc->o_free[g], (no[g]++ & 1) ^ 1);
-              pv(g, (n + 1) % L::kSlots, j == 0);
-              mma_commit(bar(misc->pv[g]));
-              free_slot((n + 1) % L::kSlots);
-            }
+        const bool second = u.ntok > TG;    // the second row group has rows
+        const int ns = L::kHalves == 1 ? (second ? 2 : 1) : (who == 0 || second ? 2 : 0);
+        if (ns == 0) {
+          // no rows for this group: pass everything on as it comes
+          mbar_arrive(bar(misc->q_empty[qb]));
+          for (const int stop_n = n + 2 * u.ntile; n < stop_n; ++n) {
+            slot_ready(n);
+            mbar_arrive(bar(misc->empty[n % L::kSlots]));
           }
         } else {
-          const int ng = u.ntok > TG ? 2 : 1;
           slot_ready(n);
-          for (int g = 0; g < ng; ++g) qk(g, n % L::kSlots, q_at);
+          for (int i = 0; i < ns; ++i) qk(i, n % L::kSlots, q_at);
           free_slot(n % L::kSlots);
           if (u.ntile == 1) mma_commit(bar(misc->q_empty[qb]));
           for (int j = 0; j < u.ntile; ++j, n += 2) {
             const bool more = j + 1 < u.ntile;
-            for (int g = 0; g < ng; ++g) {
-              if (g == 0) slot_ready(n + 1);
-              wait(misc->p_full[g], np[g]++ & 1);
-              if (j == 0) wait(misc->o_free[g], (no[g]++ & 1) ^ 1);
-              pv(g, (n + 1) % L::kSlots, j == 0);
+            for (int i = 0; i < ns; ++i) {
+              const int st = 2 * who + i;
+              if (i == 0) slot_ready(n + 1);
+              wait(misc->p_full[st], np[i]++ & 1);
+              if (j == 0) wait(misc->o_free[st], (no[i]++ & 1) ^ 1);
+              pv(i, (n + 1) % L::kSlots, j == 0);
               // (the next scores' commit tells the softmax of this product
               // too, except behind the last tile)
               if (!more) {
-                mma_commit(bar(misc->pv[g]));
+                mma_commit(bar(misc->pv[st]));
               } else {
-                if (g == 0) slot_ready(n + 2);
-                qk(g, (n + 2) % L::kSlots, q_at);
+                if (i == 0) slot_ready(n + 2);
+                qk(i, (n + 2) % L::kSlots, q_at);
               }
             }
             free_slot((n + 1) % L::kSlots);
@@ -595,7 +600,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         mbar_arrive(bar(misc->u_empty[uq]));
       }
       // every MMA issued above has finished before TMEM is freed
-      uint64_t& done = misc->done[warp - kWarpIssue];
+      uint64_t& done = misc->done[who];
       mma_commit(bar(done));
       volatile int no_abort = 0;
       mbar_wait_bounded(bar(done), 0, &no_abort, a.wait_ns);
@@ -691,13 +696,13 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     }
   }
   } else {
-    if constexpr (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if constexpr (L::kRegsSoft) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegsSoft ? L::kRegsSoft : 24));
     // ------------------------------------------------------------ softmax
-    const int g = warp >> 2, row = threadIdx.x & (kTile - 1);
+    const int st = warp >> 2, g = st / L::kHalves, half = st % L::kHalves, row = threadIdx.x & (kTile - 1);
     const int ri = row / G, head = row % G;            // the row's token in its group, its query head
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = trow + 128 * g, tO = trow + L::kColO + L::kColOStep * g;
-    const uint32_t tP = trow + L::kColP + L::kColPStep * g;
+    const uint32_t tS = trow + L::col_s(st), tO = trow + L::col_o(st);
+    const bool speaks = half == 0 && row == 0;         // one thread of the group
     const float* sc = p.scales + (size_t)a.layer * 4 * p.Hkv;
     int syncs = 0;
     auto sync_group = [&]() {
@@ -719,23 +724,29 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       if constexpr (E4M3) {
         const int qb = nu % L::kQBufs;
         wait(misc->q_full[qb], (nu / L::kQBufs) & 1);
+        // this row's queries, in place: D / 8 chunks of 16 bytes
+        uint8_t* qg = sm + L::kQ + (2 * qb + g) * L::kQGroup;
+        auto chunk_at = [&](int c) {
+          return reinterpret_cast<uint4*>(qg + (c >> 3) * L::kAtom + swz_offset(row, c & 7, 128));
+        };
+        uint32_t em = 0;
         if (live) {
-          // this row's queries, in place: 8 D/64 chunks of 16 bytes
-          uint8_t* qg = sm + L::kQ + (2 * qb + g) * L::kQGroup;
-          uint32_t em = 0;
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(qg + (c >> 3) * L::kAtom + swz_offset(row, c & 7, 128));
+            const uint4 w = *chunk_at(c);
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) em = max(em, max((ww[e] >> 7) & 0xFFu, (ww[e] >> 23) & 0xFFu));
           }
-          const bool plain = em == 0 || em >= 254;   // zeros, infinities, NaN: a factor of 1
+        }
+        if (L::kHalves > 1) sync_group();              // (both halves' threads have read the row)
+        if (live) {
+          const bool plain = em == 0 || em >= 254;     // zeros, infinities, NaN: a factor of 1
           const float down = plain ? 1.0f : __uint_as_float((254u - em) << 23);
           f_row *= __ldcg(sc + u.h) * (plain ? 1.0f : __uint_as_float(em << 23));
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(qg + (c >> 3) * L::kAtom + swz_offset(row, c & 7, 128));
+          for (int i = 0; i < D / 8 / L::kHalves; ++i) {
+            uint4* at = chunk_at(half * (D / 8 / L::kHalves) + i);
             const uint4 w = *at;
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
             uint32_t o[4];
@@ -786,51 +797,34 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             for (int i = 0; i < w; ++i) e[i] = __fadd2_rn(e[i], e[i + w]);
           lsum = __fadd2_rn(lsum, e[0]);
         };
-        auto scores_read = [&]() {
-          if constexpr (L::kOwnP) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(misc->s_free[g]));
-          }
-        };
-        // O_g and P_g are touched once P V of the previous tile is complete;
-        // where S_g follows it, S(j) complete says so
-        auto previous_done = [&](int j) {
-          if (L::kOwnP && j > 0) {
-            wait(misc->pv[g], (nt_done - 1) & 1);
-            __syncwarp();
-            tc_fence_after();
-          }
-        };
         for (int j = 0; j < ntile; ++j, ++nt_done) {
-          wait(misc->s_full[g], nt_done & 1);
+          wait(misc->s_full[st], nt_done & 1);
           __syncwarp();
           tc_fence_after();
-          const int t = (u.tile0 + j) * kTile;
-          const bool masked = t + kTile > all_hi || t < all_lo;
-          uint32_t sr[128];
+          const int t = (u.tile0 + j) * kTile + half * L::kCols;
+          const bool masked = t + L::kCols > all_hi || t < all_lo;
+          uint32_t sr[L::kCols];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
+          for (int c = 0; c < L::kCols / 32; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
           tmem_wait_ld();
-          scores_read();
           if (masked) {
             const int vh = hi - t, vl = lo - t;
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
+            for (int c = 0; c < L::kCols; ++c)
               if (c >= vh || c < vl) sr[c] = __float_as_uint(-INFINITY);
           }
           float mx[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
 #pragma unroll
-          for (int i = 1; i < 8; ++i)
+          for (int i = 1; i < L::kCols / 16; ++i)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               mx[k] = fmax3(mx[k], __uint_as_float(sr[16 * i + 2 * k]), __uint_as_float(sr[16 * i + 2 * k + 1]));
           const float tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
           const bool need = tmax > m_run + kRaise || (m_run == -INFINITY && tmax > m_run);
           const float m_new = need ? tmax : m_run;
-          previous_done(j);
+          // S(j) complete means that P V(j - 1), issued before it, is, too
           if (j > 0 && __any_sync(0xFFFFFFFFu, need)) {
             const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
 #pragma unroll 1
@@ -853,24 +847,41 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           const float moff = kShift - (m_run == -INFINITY ? 0.f : m_run);   // nothing seen yet: 2^-inf = 0
           float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < L::kCols / 32; ++c) {
             uint32_t pw[16];
             probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
-            tmem_st16(tP + 16 * c, pw);
+            tmem_st16(tS + 16 * c, pw);
           }
           ell += lsum.x + lsum.y;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(misc->p_full[g]));
+          if (lane == 0) mbar_arrive(bar(misc->p_full[st]));
         }
         // ------------------------------------------------------- epilogue
-        wait(misc->pv[g], (L::kOwnP ? nt_done - 1 : nu_done) & 1);
+        // Both halves' sums count from here on: w_half their weights, m_run
+        // and ell those of the row.  A half's threads write half the columns.
+        float w_half[2] = {1.0f, 1.0f};
+        if constexpr (L::kHalves > 1) {
+          float2* ml = reinterpret_cast<float2*>(sm + L::kMl) + g * 2 * kTile + row;
+          ml[half * kTile] = make_float2(m_run, ell);
+          sync_group();
+          const float2 a0 = ml[0], a1 = ml[kTile];
+          m_run = fmaxf(a0.x, a1.x);
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+          w_half[0] = ex2_approx(a0.x - mu);
+          w_half[1] = ex2_approx(a1.x - mu);
+          ell = a0.y * w_half[0] + a1.y * w_half[1];
+        }
+#pragma unroll
+        for (int i = 0; i < L::kHalves; ++i) wait(misc->pv[g * L::kHalves + i], nu_done & 1);
         ++nu_done;
         __syncwarp();
         tc_fence_after();
+        constexpr int kC = D / 32 / L::kHalves;        // 32-column groups of this thread
+        const int c_first = half * kC;
         const float scale_v = E4M3 ? __ldcg(sc + p.Hkv + u.h) : 1.0f;
-        const float inv = ell > 0.f || ell != ell ? scale_v / ell : 0.f;
+        const float inv = ell > 0.f || ell != ell ? scale_v / ell : 0.f;   // (of the row, both halves)
         const bool whole = u.whole;
         const int first = u.first, last = u.last;
         uint16_t* o16 = a.out + ((size_t)(u.q_tok + tok) * p.Hq + u.h * G + head) * D;
@@ -884,7 +895,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         // all from the workspace.
         bool merge_now = false;
         if (!whole) {
-          if (row == 0) misc->last[g] = ld_acquire_gpu(ticket) == last - first;
+          if (speaks) misc->last[g] = ld_acquire_gpu(ticket) == last - first;
           sync_group();
           merge_now = misc->last[g];
         }
@@ -935,17 +946,27 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         };
         if (merge_now) {
           __threadfence();
-          if (row == 0) *ticket = 0;
+          if (speaks) *ticket = 0;
           weigh();
         }
         const bool is_wild = *const_cast<const volatile int*>(&u.wild);
         float4* o32 = reinterpret_cast<float4*>(p.part_o + ((size_t)u.part * kPartRows + g * kTile) * D) + row;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = c_first; c < c_first + kC; ++c) {
           uint32_t rr[32];
           __syncwarp();
-          tmem_ld32(tO + 32 * c, rr);
-          tmem_wait_ld();
+          if constexpr (L::kHalves == 1) {
+            tmem_ld32(tO + 32 * c, rr);
+            tmem_wait_ld();
+          } else {
+            uint32_t r1[32];
+            tmem_ld32(trow + L::col_o(2 * g) + 32 * c, rr);
+            tmem_ld32(trow + L::col_o(2 * g + 1) + 32 * c, r1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              rr[k] = __float_as_uint(__uint_as_float(rr[k]) * w_half[0] + __uint_as_float(r1[k]) * w_half[1]);
+          }
           if (is_wild && live) {
             // the values that are not finite among those this row sees
             for (int j = 0; j < ntile; ++j) {
@@ -981,13 +1002,16 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(misc->o_free[g]));
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < L::kHalves; ++i) mbar_arrive(bar(misc->o_free[g * L::kHalves + i]));
+        }
         if (!whole && !merge_now) {
-          *reinterpret_cast<float2*>(p.part_ml + ((size_t)u.part * kPartRows + g * kTile + row) * 2) =
+          if (half == 0) *reinterpret_cast<float2*>(p.part_ml + ((size_t)u.part * kPartRows + g * kTile + row) * 2) =
               make_float2(m_run, ell);
           __threadfence();
           sync_group();
-          if (row == 0) {
+          if (speaks) {
             misc->last[g] = atomicAdd(ticket, 1) == last - first;
             if (misc->last[g]) *ticket = 0;
           }
@@ -997,7 +1021,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             weigh();
             const uint32_t none[32] = {};
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) merge_columns(c, none);
+            for (int c = c_first; c < c_first + kC; ++c) merge_columns(c, none);
           }
         }
       }
@@ -1008,13 +1032,22 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpIssue) tmem_dealloc(tmem, 512);
+  if (warp == L::kWarpIssue) tmem_dealloc(tmem, 512);
   if (threadIdx.x == 0 && *abort)
     atomicOr(reinterpret_cast<unsigned*>(p.state + PST_ERROR), KVRING_PAGES_ERR_TIMEOUT);
 }
 
 template <int D, bool E4M3>
 cudaError_t prepare_one() {
+  using L = ChunkLayout<D, E4M3>;
+  // the register split must fit what a block is launched with, or the warps
+  // that ask for more would wait for ever
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, k_paged_chunk<D, E4M3>);
+  if (e != cudaSuccess) return e;
+  if (L::kRegsSoft && at.numRegs * L::kThreads <
+                          L::kRegsSoft * L::kSoftThreads + L::kRegsRest * (L::kThreads - L::kSoftThreads))
+    return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(k_paged_chunk<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               ChunkLayout<D, E4M3>::kBytes);
 }

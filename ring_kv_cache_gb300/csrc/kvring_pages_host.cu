@@ -370,7 +370,7 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
     if (chunk) {
       a.min_rows = few ? split_rows : 0;
       a.max_rows = INT32_MAX;
-      a.min_tiles = 4;
+      a.min_tiles = 8;
       e = kvr::launch_paged_chunk(h->dev, &tmQ, &h->tmK, &h->tmV, a, s);
     }
     if (few && e == cudaSuccess) {
