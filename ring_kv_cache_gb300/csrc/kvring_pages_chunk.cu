@@ -771,10 +771,13 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         // (a row that is none keeps a factor of 0 and never asks for anything)
         float m_run = live ? -INFINITY : 0.f, ell = 0.f;
         if (!live) f_row = 0.f;
+        // (nothing seen yet: 2^-inf = 0)
+        float factor = f_row, moff = kShift;
+        bool huge = false;
         // 32 scores to probabilities, as pairs of the 16-bit type; their sum
         // is added to lsum
-        auto probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, float moff, float2& lsum) {
-          const float2 fr2 = make_float2(f_row, f_row), mo2 = make_float2(moff, moff);
+        auto probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, float factor, float moff, float2& lsum) {
+          const float2 fr2 = make_float2(factor, factor), mo2 = make_float2(moff, moff);
           float2 e[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -824,32 +827,46 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           const float tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
           const bool need = tmax > m_run + kRaise || (m_run == -INFINITY && tmax > m_run);
           const float m_new = need ? tmax : m_run;
-          // S(j) complete means that P V(j - 1), issued before it, is, too
-          if (j > 0 && __any_sync(0xFFFFFFFFu, need)) {
-            const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
+          if (__any_sync(0xFFFFFFFFu, need)) {
+            // S(j) complete means that P V(j - 1), issued before it, is, too
+            if (j > 0) {
+              const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t rr[16];
-              tmem_ld_n<16>(tO + 16 * c, rr);
-              tmem_wait_ld();
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t rr[16];
+                tmem_ld_n<16>(tO + 16 * c, rr);
+                tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float2 y = __fmul2_rn(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])),
-                                            make_float2(alpha, alpha));
-                rr[i] = __float_as_uint(y.x);
-                rr[i + 1] = __float_as_uint(y.y);
+                for (int i = 0; i < 16; i += 2) {
+                  const float2 y = __fmul2_rn(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])),
+                                              make_float2(alpha, alpha));
+                  rr[i] = __float_as_uint(y.x);
+                  rr[i + 1] = __float_as_uint(y.y);
+                }
+                tmem_st16(tO + 16 * c, rr);
               }
-              tmem_st16(tO + 16 * c, rr);
+              ell *= alpha;
             }
-            ell *= alpha;
+            m_run = m_new;
+            moff = kShift - (m_run == -INFINITY ? 0.f : m_run);
+            factor = f_row;
+            huge = __any_sync(0xFFFFFFFFu, fabsf(moff) > 0x1p20f);
           }
-          m_run = m_new;
-          const float moff = kShift - (m_run == -INFINITY ? 0.f : m_run);   // nothing seen yet: 2^-inf = 0
+          // Scores so large that factor x score, not rounded in the fused
+          // multiply-add, may lie well above its rounding, the maximum:
+          // rounded first, then the largest gives exactly 0.
+          if (huge) {
+            const float mu = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+            for (int c = 0; c < L::kCols; ++c) sr[c] = __float_as_uint(__fmul_rn(__uint_as_float(sr[c]), f_row) - mu);
+            factor = 1.0f;
+            moff = kShift;
+          }
           float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < L::kCols / 32; ++c) {
             uint32_t pw[16];
-            probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
+            probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, factor, moff, lsum);
             tmem_st16(tS + 16 * c, pw);
           }
           ell += lsum.x + lsum.y;

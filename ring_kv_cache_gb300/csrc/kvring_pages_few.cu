@@ -329,9 +329,16 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
   // A wait that gives up raises the abort flag; from then on nobody waits
   // and the rest of the range runs through on whatever the slots hold, so
   // every barrier is still met and every ticket still drawn.
-  auto wait_full = [&](int s, int n) {
-    if (!mbar_try_wait(full(s), (n / L::kSlots) & 1) && !*abort)
-      mbar_wait_bounded(full(s), (n / L::kSlots) & 1, abort, a.wait_ns);
+  int s = 0;                                            // the next slot, and its barrier's phase
+  uint32_t phase = 0;
+  auto wait_full = [&]() {
+    if (!mbar_try_wait(full(s), phase) && !*abort) mbar_wait_bounded(full(s), phase, abort, a.wait_ns);
+  };
+  auto next_slot = [&]() {
+    if (++s == L::kSlots) {
+      s = 0;
+      phase ^= 1u;
+    }
   };
   const int g = lane >> 2, c = lane & 3;
   float* s_o = reinterpret_cast<float*>(fix + L::kO);
@@ -357,7 +364,6 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b2);
   };
-  int n = 0;
   while (x < stop) {
     const long long uend = ubase + rq.nt;
     const long long ue = uend < stop ? uend : stop;
@@ -444,13 +450,13 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     for (int tile = rq.t0 + (int)(x - ubase); x < ue; ++x, ++tile, group += group < kGroups ? kWarps - kGroups : -kGroups) {
       const int tok0 = tile * kTile + group * 16;        // this warp's tokens
       // ---- scores
-      int s = n % L::kSlots;
-      wait_full(s, n);
+      wait_full();
       if (kWarps > kGroups && group >= kGroups) {
         // another's tile: only waited for, so that this warp stays within a
         // phase of every slot's barrier
-        wait_full((n + 1) % L::kSlots, n + 1);
-        n += 2;
+        next_slot();
+        wait_full();
+        next_slot();
         continue;
       }
       float sc_[MT][2][4];
@@ -487,7 +493,8 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
 #pragma unroll
         for (int k2 = 0; k2 < D / 32; ++k2) {
           uint32_t kb[4];
-          ldsm4(kb, sK + swz_offset(tok, 2 * k2 + (lane >> 4), D));
+          ldsm4(kb, D == 128 ? (sK + tok * 128 + ((tok & 7) << 4)) ^ ((2 * k2 + (lane >> 4)) << 4)
+                             : sK + swz_offset(tok, 2 * k2 + (lane >> 4), D));
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t b[4];
@@ -499,7 +506,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
-      ++n;
+      next_slot();
       // ---- probabilities, in the layout of the next product's operand
       const bool masked = tok0 < all_lo || tok0 + 16 > all_hi;
       uint32_t pa[MT][4];
@@ -512,22 +519,24 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
             continue;
           }
           const float f = fac[2 * i + hr];
-          int lo = 0, hi = INT32_MAX;
           if (masked) {
             const int4 ri = s_row[16 * i + 8 * hr + g];
-            lo = ri.x;
-            hi = ri.y;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int tok = tok0 + nt * 8 + 2 * c + e;
+                if (tok < ri.x || tok >= ri.y) sc_[i][nt][2 * hr + e] = -INFINITY;
+              }
           }
-          float mx = -INFINITY;
+          // (rounded before the maximum is taken away, so that the largest
+          // gives exactly 0 whatever its size)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& v = sc_[i][nt][2 * hr + e];
-              const int tok = tok0 + nt * 8 + 2 * c + e;
-              v = tok >= lo && tok < hi ? v * f : -INFINITY;
-              mx = fmaxf(mx, v);
-            }
+          for (int nt = 0; nt < 2; ++nt) {
+            sc_[i][nt][2 * hr] *= f;
+            sc_[i][nt][2 * hr + 1] *= f;
+          }
+          float mx = fmaxf(fmax3(sc_[i][0][2 * hr], sc_[i][0][2 * hr + 1], sc_[i][1][2 * hr]), sc_[i][1][2 * hr + 1]);
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
           float& mr = m_run[2 * i + hr];
@@ -553,8 +562,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
         }
       }
       // ---- values
-      s = n % L::kSlots;
-      wait_full(s, n);
+      wait_full();
       const uint32_t sV = sbase + s * L::kSlot;
       // 16 columns (two column tiles) of the warp's 16 tokens; columns of an
       // E4M3 cache as 16 ch + 2 n + (0, 1) for column n of the two tiles
@@ -565,7 +573,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
           ldsm4t(vb, sV + (ch >> 3) * (kTile * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
         } else {
           uint32_t vr[2];
-          ldsm2t(vr, sV + swz_offset(tok, ch2, D));
+          ldsm2t(vr, D == 128 ? (sV + tok * 128 + ((tok & 7) << 4)) ^ (ch2 << 4) : sV + swz_offset(tok, ch2, D));
           // (token, column) 00 01 10 11 in the bytes of vr: token pairs per column
 #pragma unroll
           for (int e = 0; e < 2; ++e) e4m3x4_to_f16x4(__byte_perm(vr[e], 0u, 0x3120), vb[e], vb[2 + e]);
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
-      ++n;
+      next_slot();
     }
 
     // ---- end of the unit, or of this CTA's part of it: merge the warps

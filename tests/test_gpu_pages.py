@@ -271,10 +271,12 @@ def test_tensors_shorter_than_the_plan():
         close(out, want[:n], tol[:n], n)
 
 
+@pytest.mark.parametrize("new", [5, 90])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("cache", ["e4m3", "bf16"])
-def test_queries_of_any_size(cache):
+def test_queries_of_any_size(cache, d, new):
     """Tiny, zero and huge query rows: the 8-bit cache's queries change type."""
-    p, s = filled(2, 1, 64, 16, [100], [5], cache, seed=7)
+    p, s = filled(2, 1, d, 16, [300], [new], cache, seed=7)
     q = s["q"].clone()
     q[0] = 0.0
     q[1] *= 2.0 ** -100
@@ -282,7 +284,7 @@ def test_queries_of_any_size(cache):
     q[3, 0, 0] = math.nan
     out = p.attention(0, q)
     want, tol = attention_64(p, s, q=q)
-    ok = [0, 1, 4]
+    ok = [0, 1, 4] + list(range(5, new))
     close(out[ok], want[ok], tol[ok])
     assert bool(torch.isnan(out[3, 0]).all()) and bool(torch.isfinite(out[3, 1]).all())
     # row 2 is one-hot on its largest score
