@@ -518,6 +518,12 @@ def make_pages_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_req
                              int(rope_pairing), 0, float(rope_base))
 
 
+def _i32(x) -> int:
+    """An int argument, kept in range where ctypes would wrap it."""
+    x = int(x)
+    return x if -(1 << 31) <= x < 1 << 31 else (-1 if x < 0 else (1 << 31) - 1)
+
+
 def kvring_pages_get_layout(cfg: KvringPagesConfig) -> KvringPagesLayout:
     lay = KvringPagesLayout()
     _check(lib().kvring_pages_get_layout(ctypes.byref(cfg), ctypes.byref(lay)), "kvring_pages_get_layout")
@@ -649,7 +655,7 @@ class KvPages:
             if not isinstance(t, torch.Tensor) or t.device != self.device or t.dtype != torch.float32 \
                     or tuple(t.shape) != (self.Hkv,) or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 tensor [{self.Hkv}] on {self.device}")
-        self._call(_LIB.kvring_pages_set_scales, "kvring_pages_set_scales", stream, int(layer), scale_k.data_ptr(),
+        self._call(_LIB.kvring_pages_set_scales, "kvring_pages_set_scales", stream, _i32(layer), scale_k.data_ptr(),
                    scale_v.data_ptr())
 
     def plan(self, new_tokens, num_tokens: int, rows=None, max_new: int | None = None, stream=None) -> KvStep:
@@ -660,8 +666,9 @@ class KvPages:
         n = self._int_arg(new_tokens, "new_tokens").numel()
         if rows is not None:
             self._int_arg(rows, "rows", (n,))
+        num_tokens = _i32(num_tokens)
         self._call(_LIB.kvring_pages_plan, "kvring_pages_plan", stream, _ptr(rows), new_tokens.data_ptr(), n, num_tokens,
-                   num_tokens if max_new is None else max_new)
+                   num_tokens if max_new is None else _i32(max_new))
         step = self._steps.get((n, num_tokens))
         if step is None:
             if len(self._steps) >= 256:
@@ -716,8 +723,8 @@ class KvPages:
                                   or t.device != self.device or t.shape != (self.d,) or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{self.d}] on {self.device}")
         q_out = self._result(q_out, n, "q_out")
-        self._call(_LIB.kvring_pages_write, "kvring_pages_write", stream, layer, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                   qs, ks, vs, _ptr(q_norm), _ptr(k_norm), eps, q_out.data_ptr(), n)
+        self._call(_LIB.kvring_pages_write, "kvring_pages_write", stream, _i32(layer), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                   qs, ks, vs, _ptr(q_norm), _ptr(k_norm), float(eps), q_out.data_ptr(), n)
         return q_out
 
     def attention(self, layer: int, q, out=None, causal: bool = True, window: int = 0, scale: float = 0.0,
@@ -729,8 +736,8 @@ class KvPages:
         were (undefined in a new tensor)."""
         n, qs = self._heads(q, self.Hq, "q")
         out = self._result(out, n, "out")
-        self._call(_LIB.kvring_pages_attention, "kvring_pages_attention", stream, layer, q.data_ptr(), qs, out.data_ptr(),
-                   n, 1 if causal else 0, window, scale)
+        self._call(_LIB.kvring_pages_attention, "kvring_pages_attention", stream, _i32(layer), q.data_ptr(), qs, out.data_ptr(),
+                   n, 1 if causal else 0, _i32(window), float(scale))
         return out
 
     def set_wait(self, limit_ns: int = 1_000_000_000, stall: bool = False) -> None:

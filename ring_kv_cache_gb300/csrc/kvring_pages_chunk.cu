@@ -4,10 +4,9 @@
 //   out[r] = sum_j softmax_j(s_rj) V[j],  s_rj = scale q[r] . K[j]
 // in one pass over the keys with a running maximum per row, raised only when
 // a tile's maximum exceeds it by more than 8 (log2 units): then and only then
-// is the accumulator rescaled.  Probabilities carry 2^7 relative to that
-// maximum, so that the largest is 2^15 (inside f16) and small ones stay
-// normal numbers; they are rounded once to the 16-bit type of the values'
-// operand, the normaliser sums them unrounded in fp32.
+// is the accumulator rescaled.  Probabilities are rounded once, to the 16-bit
+// type of the values' operand (f16 over an E4M3 cache, else bf16), and the
+// normaliser sums them unrounded in fp32.
 //
 // Bound by the tensor cores: 4 rows keys d operations against
 // 2 keys d cached values per 256 rows.  A unit is 256 query rows of one
@@ -64,7 +63,11 @@ constexpr int kUnitQueue = 4;
 constexpr int kUnitCost = 3;
 constexpr int kTileBits = 40;     // of the sums over requests: places in the low bits, units above
 constexpr float kRaise = 8.0f;    // log2 units
-constexpr float kShift = 7.0f;
+// Probabilities carry 2^kShift relative to the running maximum: with f16 the
+// largest is then 2^15 and small ones stay normal numbers; bf16 needs no shift,
+// and values near the end of its range no further factor.
+template <bool E4M3>
+constexpr float kShift = E4M3 ? 7.0f : 0.0f;
 constexpr int kChunkSmem = 232448;
 
 template <int D, bool E4M3>
@@ -743,7 +746,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         if (live) {
           const bool plain = em == 0 || em >= 254;     // zeros, infinities, NaN: a factor of 1
           const float down = plain ? 1.0f : __uint_as_float((254u - em) << 23);
-          f_row *= __ldcg(sc + u.h) * (plain ? 1.0f : __uint_as_float(em << 23));
+          // (at least 1e-30: a factor that underflows would make NaN of what is
+          // masked, and such scores are all alike anyway)
+          f_row = fmaxf(f_row * __ldcg(sc + u.h) * (plain ? 1.0f : __uint_as_float(em << 23)), 1e-30f);
 #pragma unroll
           for (int i = 0; i < D / 8 / L::kHalves; ++i) {
             uint4* at = chunk_at(half * (D / 8 / L::kHalves) + i);
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         float m_run = live ? -INFINITY : 0.f, ell = 0.f;
         if (!live) f_row = 0.f;
         // (nothing seen yet: 2^-inf = 0)
-        float factor = f_row, moff = kShift;
+        float factor = f_row, moff = kShift<E4M3>;
         bool huge = false;
         // 32 scores to probabilities, as pairs of the 16-bit type; their sum
         // is added to lsum
@@ -848,7 +853,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
               ell *= alpha;
             }
             m_run = m_new;
-            moff = kShift - (m_run == -INFINITY ? 0.f : m_run);
+            moff = kShift<E4M3> - (m_run == -INFINITY ? 0.f : m_run);
             factor = f_row;
             huge = __any_sync(0xFFFFFFFFu, fabsf(moff) > 0x1p20f);
           }
@@ -860,7 +865,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < L::kCols; ++c) sr[c] = __float_as_uint(__fmul_rn(__uint_as_float(sr[c]), f_row) - mu);
             factor = 1.0f;
-            moff = kShift;
+            moff = kShift<E4M3>;
           }
           float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll

@@ -391,7 +391,9 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
         // (and stay what they are), and so does a row of zeros
         const bool plain = em == 0 || em >= 254;
         const float down = plain ? 1.0f : __uint_as_float((254u - em) << 23);
-        fac *= scale_k * (plain ? 1.0f : __uint_as_float(em << 23));
+        // (at least 1e-30: a factor that underflows would make NaN of what is
+        // masked, and such scores are all alike anyway)
+        fac = fmaxf(fac * scale_k * (plain ? 1.0f : __uint_as_float(em << 23)), 1e-30f);
         uint32_t hq[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)

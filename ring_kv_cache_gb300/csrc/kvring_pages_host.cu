@@ -349,6 +349,9 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   a.causal = causal;
   a.window = window;
   a.sm_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.0f / sqrtf((float)h->cfg.head_dim));
+  // (a product that overflows, or underflows to 0, is no factor for a mask)
+  if (!std::isfinite(a.sm_log2)) return KVRING_ERR_INVALID_ARG;
+  if (a.sm_log2 < 1e-30f) a.sm_log2 = 1e-30f;
   a.ctas = h->sm_count;
   a.wait_ns = h->wait_ns;
   a.debug_stall = h->debug_stall;

@@ -332,6 +332,123 @@ def test_hidden_values_reach_no_row(d, hq, hkv, total, new, bad, window, cache, 
     assert errors(p) == 0
 
 
+@pytest.mark.parametrize("new", [1, 60])
+def test_large_values_and_tiny_scales(new):
+    """bf16 values near the end of their range, and scales that leave no score."""
+    p, s = filled(4, 2, 128, 64, [300], [new], "bf16", seed=13)
+    p.v_cache(0).mul_(2.0 ** 114)
+    want, tol = attention_64(p, s)
+    out = p.attention(0, s["q"])
+    close(out, want, tol)
+    p.v_cache(0).mul_(2.0 ** -114)
+    for cache in ("bf16", "e4m3"):
+        p, s = filled(4, 2, 128, 64, [300], [new], cache, seed=13)
+        for scale in (1e-44, 1e-30):
+            out = p.attention(0, s["q"], scale=scale)
+            want, tol = attention_64(p, s, scale=scale)
+            close(out, want, tol)
+    with pytest.raises(kv.KvRingError):
+        p.attention(0, s["q"], scale=3e38)
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_a_cache_beyond_32_bit_offsets(cache):
+    """Pages whose bytes lie beyond 2^32 of the pool, in a later layer."""
+    hq, hkv, d, page, num = 8, 8, 128, 64, 24000 if cache == "bf16" else 40000
+    dt = torch.float8_e4m3fn if cache == "e4m3" else torch.bfloat16
+    p = kv.KvPages(hq, hkv, d, page_size=page, num_pages=num, max_requests=2, max_request_tokens=6 * page,
+                   max_tokens=200, layers=2, cache_dtype=dt)
+    assert p.k_cache(1)[num - 9].data_ptr() - p.k_cache(0).data_ptr() > 2 ** 32
+    ids = torch.full((2, 6), -1, dtype=torch.int32, device="cuda")
+    ids[0, :3] = torch.tensor([num - 1, 0, num - 2], dtype=torch.int32)
+    ids[1, :2] = torch.tensor([num - 5, num - 9], dtype=torch.int32)
+    p.restore(i32([150, 100]), ids, i32([1, num - 3, num - 4, num - 6]))
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for c in (p.k_cache(1), p.v_cache(1)):
+        for i in (num - 1, 0, num - 2, num - 5, num - 9):
+            c[i] = torch.randn(c.shape[1:], generator=g, device="cuda").to(dt)
+    s = dict(layer=1)
+    if cache == "e4m3":
+        s.update(sk=torch.ones(hkv, device="cuda"), sv=torch.ones(hkv, device="cuda"))
+    for new in ([1, 1], [120, 70]):
+        n = sum(new)
+        p.plan(i32(new), n, max_new=max(new))
+        qkv = torch.randn((n, 3 * hq, d), generator=g, device="cuda").to(torch.bfloat16)
+        q, k, v = qkv.split([hq, hkv, hkv], dim=1)
+        q_out = p.write(1, q, k, v)
+        out = p.attention(1, q_out)
+        s.update(total=[150 + new[0], 100 + new[1]], new=new, before=[150, 100])
+        want, tol = attention_64(p, s, q=q_out)
+        close(out, want, tol)
+        # the values written are those read back
+        sl = p._slots[:n].long()
+        raw = p.v_cache(1).view(torch.uint8)[sl // page, :, sl % page] if cache == "e4m3" else \
+            p.v_cache(1)[sl // page, :, sl % page]
+        got = raw.view(dt).float()
+        close(got, v.double(), (2.0 ** -4 * v.double().abs() + 2.0 ** -10) if cache == "e4m3" else 0 * v.double(), "v")
+    assert errors(p) == 0
+
+
+def test_two_caches_on_two_streams_at_once():
+    """Objects of their own are independent: chunks on one stream, single
+    tokens on another, and a ring's projection feeding the pages."""
+    a, sa = filled(4, 2, 128, 64, [3000, 700], [500, 200], "bf16", seed=20)
+    b, sb = filled(8, 8, 64, 16, [5000, 80, 900], [1, 1, 1], "e4m3", seed=21)
+    wa, ta = attention_64(a, sa)
+    wb, tb = attention_64(b, sb)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [(torch.zeros_like(sa["q"]), torch.zeros_like(sb["q"])) for _ in range(6)]
+    torch.cuda.synchronize()
+    for oa, ob in outs:
+        a.attention(0, sa["q"], out=oa, stream=s1)
+        b.attention(0, sb["q"], out=ob, stream=s2)
+    torch.cuda.synchronize()
+    for oa, ob in outs:
+        close(oa, wa, ta, "a")
+        close(ob, wb, tb, "b")
+
+
+def test_the_rings_projection_feeds_the_pages():
+    """Queries, keys and values from kvring_project_write, read by the write
+    right behind it, and the pages' output read by a ring's write."""
+    H, d, n, dm = 2, 64, 12, 128
+    ring = kv.KvRing(H, d, 48, n, 256)
+    p = kv.KvPages(H, H, d, page_size=16, num_pages=20, max_requests=1, max_request_tokens=300, max_tokens=n,
+                   cache_dtype=torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = (0.1 * torch.randn((3 * H * d, dm), generator=g, device="cuda")).to(torch.bfloat16)
+    xs = [torch.randn((n, dm), generator=g, device="cuda").to(torch.bfloat16) for _ in range(8)]
+    ones = torch.ones((n, H, d), dtype=torch.bfloat16, device="cuda")
+    ring.calibrate(ones, ones)
+    torch.cuda.synchronize()
+    got, kept = [], []
+    for x in xs:
+        q, kv_out = ring.project_write(x, w, write=False, store_kv=True)
+        p.plan(i32([n]), n)
+        q_out = p.write(0, q, kv_out[0], kv_out[1])
+        out = p.attention(0, q_out)
+        p.commit()
+        ring.write(out, out)   # reads the pages' output
+        got.append(out)
+        kept.append((q, kv_out))
+    e = ring.export()
+    torch.cuda.synchronize()
+    total = n * len(xs)
+    s = dict(total=[total], new=[n], before=[total - n], layer=0)
+    p.plan(i32([0]), n)
+    for i, (q, kv_out) in enumerate(kept):
+        pos = torch.arange(i * n, (i + 1) * n, device="cuda")
+        q_want = norm_rope_64(q, None, pos, "adjacent")[0].to(torch.bfloat16)
+        s.update(total=[(i + 1) * n])
+        want, tol = attention_64(p, s, q=q_want)
+        # (a rotated query may have been rounded the other way)
+        close(got[i], want, tol + 2.0 ** -6 * want.abs().amax(), i)
+    last = torch.cat(got[-4:]).float()          # the ring's 48 slots: the last four outputs
+    codes = e["v"].view(torch.float8_e4m3fn).float() * e["scales"][H:2 * H, None, None]
+    order = torch.argsort(e["slot_pos"])
+    close(codes[:, order].transpose(0, 1), last.clamp(-1, 1).double(), 2.0 ** -4 * last.abs() + 2.0 ** -10, "ring")
+
+
 # --------------------------------------------------------------- together
 def plain_step(hist, qkv, cu, hq, hkv, d, pairing, wq, wk, cache, sk, sv):
     """One layer's step on host lists of (k, v) float64 per request."""
@@ -495,6 +612,10 @@ def test_refusals_of_the_binding():
             p.plan(*args)
     with pytest.raises(kv.KvRingError):
         p.plan(i32([1]), 4, max_new=0)
+    with pytest.raises(kv.KvRingError):
+        p.plan(i32([1]), 2 ** 32 + 4)   # does not wrap to 4
+    with pytest.raises(kv.KvRingError):
+        p.attention(2 ** 32, q)
     with pytest.raises(ValueError):
         p.restore(i32([1, 2]), p.tables, i32([0]))
     assert errors(p) == 0
