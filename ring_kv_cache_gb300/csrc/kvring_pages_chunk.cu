@@ -51,6 +51,8 @@
 // leaves at its next unit, copies and MMAs in flight are drained, TMEM is
 // freed and KVRING_PAGES_ERR_TIMEOUT is set.  Tickets that were then not
 // drawn are cleared by the next plan.
+#include <type_traits>
+
 #include "kvring_pages.cuh"
 
 namespace kvr {
@@ -777,12 +779,14 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         float m_run = live ? -INFINITY : 0.f, ell = 0.f;
         if (!live) f_row = 0.f;
         // (nothing seen yet: 2^-inf = 0)
-        float factor = f_row, moff = kShift<E4M3>;
-        bool huge = false;
+        float moff = kShift<E4M3>;
+        // (over an E4M3 cache a score is at most 2 x 448 x 128 < 2^17, so the
+        // factor tells)
+        bool huge = E4M3 && __any_sync(0xFFFFFFFFu, f_row > 8.0f);
         // 32 scores to probabilities, as pairs of the 16-bit type; their sum
         // is added to lsum
-        auto probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, float factor, float moff, float2& lsum) {
-          const float2 fr2 = make_float2(factor, factor), mo2 = make_float2(moff, moff);
+        auto probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, float moff, float2& lsum) {
+          const float2 fr2 = make_float2(f_row, f_row), mo2 = make_float2(moff, moff);
           float2 e[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -805,7 +809,21 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             for (int i = 0; i < w; ++i) e[i] = __fadd2_rn(e[i], e[i + w]);
           lsum = __fadd2_rn(lsum, e[0]);
         };
-        for (int j = 0; j < ntile; ++j, ++nt_done) {
+        // Scores so large that factor x score, not rounded in the fused
+        // multiply-add, may lie well above its rounding, the maximum: the
+        // differences of the rounded ones (for the largest exactly 0) go in
+        // the scores' place, over the factor.  From the first such tile on
+        // the unit's tiles take the loop below that always does this.
+        auto differences = [&](uint32_t (&sr)[L::kCols]) {
+          const float mu = m_run == -INFINITY ? 0.f : m_run, over = 1.0f / f_row;
+#pragma unroll
+          for (int c = 0; c < L::kCols; ++c)
+            sr[c] = __float_as_uint((__fmul_rn(__uint_as_float(sr[c]), f_row) - mu) * over);
+          moff = kShift<E4M3>;
+        };
+        int j = 0;
+        auto tile = [&](auto slow_tag) {
+          constexpr bool slow = decltype(slow_tag)::value;
           wait(misc->s_full[st], nt_done & 1);
           __syncwarp();
           tc_fence_after();
@@ -854,24 +872,17 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             }
             m_run = m_new;
             moff = kShift<E4M3> - (m_run == -INFINITY ? 0.f : m_run);
-            factor = f_row;
-            huge = __any_sync(0xFFFFFFFFu, fabsf(moff) > 0x1p20f);
+            if constexpr (!slow && !E4M3) {
+              huge = __any_sync(0xFFFFFFFFu, fabsf(moff) > 0x1p20f);
+              if (huge) differences(sr);
+            }
           }
-          // Scores so large that factor x score, not rounded in the fused
-          // multiply-add, may lie well above its rounding, the maximum:
-          // rounded first, then the largest gives exactly 0.
-          if (huge) {
-            const float mu = m_run == -INFINITY ? 0.f : m_run;
-#pragma unroll
-            for (int c = 0; c < L::kCols; ++c) sr[c] = __float_as_uint(__fmul_rn(__uint_as_float(sr[c]), f_row) - mu);
-            factor = 1.0f;
-            moff = kShift<E4M3>;
-          }
+          if constexpr (slow) differences(sr);
           float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < L::kCols / 32; ++c) {
             uint32_t pw[16];
-            probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, factor, moff, lsum);
+            probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
             tmem_st16(tS + 16 * c, pw);
           }
           ell += lsum.x + lsum.y;
@@ -879,7 +890,10 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(misc->p_full[st]));
-        }
+          ++nt_done;
+        };
+        for (; j < ntile && !huge; ++j) tile(std::false_type{});
+        for (; j < ntile; ++j) tile(std::true_type{});
         // ------------------------------------------------------- epilogue
         // Both halves' sums count from here on: w_half their weights, m_run
         // and ell those of the row.  A half's threads write half the columns.
