@@ -60,6 +60,8 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
 // words at most, in one pass with one block scan of tokens and pages packed
 // in 64 bits), so no block waits for another and the plan is one launch; a
 // block then writes its share of the token maps and of the table entries.
+// Bound by latency: 4.3 us for 48 requests and as many tokens, 6.4 us for 1,000
+// requests with 65,536 tokens (0.6 MB).
 // Tokens take 34 bits (4,096 requests x 2^20 tokens), pages 30.
 constexpr int kTokBits = 34;
 
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       p.klen[i] = bad ? s_len[i] : s_len[i] + s_cu[i + 1] - s_cu[i];
     }
     // (only an attention whose waits gave up leaves tickets behind)
-    for (int i = threadIdx.x; i < 2 * kPagedMaxCtas; i += kPlanThreads) p.tickets[i] = 0;
+    for (int i = threadIdx.x; i < 3 * kPagedMaxCtas; i += kPlanThreads) p.tickets[i] = 0;
     if (threadIdx.x == 0) {
       p.cu[B] = tokens;
       p.state[PST_PLANNED] = 1;
@@ -334,9 +336,11 @@ __global__ void k_pages_table(float* table, const Thetas th, int half, size_t n)
 // warp and head row).  A block takes the tokens of one warp (2 or 4) and its
 // eight warps walk the heads; loads of a batch of heads go out together,
 // those of the first batch and of the first key and value before anything
-// else is known.
+// else is known.  Measured (GB300): 16,384 tokens, 32/8 heads x 128, bf16 cache,
+// 411 MB: 73.5 us, 5.6 TB/s (82 % of the copy rate; issue slots 54 % busy); 757
+// tokens of 40 heads into an E4M3 cache, 39 MB: 8.8 us; nine tokens: 1.9 us.
 constexpr int kWriteWarps = 8;
-constexpr int kWriteBatch = 2;
+constexpr int kWriteBatch = 2;   // (with four resident blocks; 3: 77 us, 4 with three blocks: 85 us)
 
 template <int D, bool E4M3, bool HALVES>
 __global__ void __launch_bounds__(kWriteWarps * 32, 4)

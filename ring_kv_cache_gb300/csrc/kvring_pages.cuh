@@ -18,7 +18,13 @@ enum : int {
 
 constexpr int kMaxRows = 4096;       // rows of the block tables
 constexpr int kPagedMaxCtas = 160;   // CTAs of an attention launch (workspace slots: two each)
-constexpr int kPartRows = 256;       // query rows of a workspace slot
+constexpr int kPartRows = 256;       // query rows of a workspace slot of the chunk kernel
+// Query rows of a unit of the kernel for few rows, one m = 16 tile, and the most
+// a request may have for it.  Beyond, the chunk kernel takes the request:
+// requests of 16 to 32 rows take 173 us so, and took 324 us with two m = 16 tiles
+// per warp (64 requests of up to 8,192 tokens, 32/8 heads x 128, bf16; E4M3 178
+// and 346); requests of 8 to 16 rows 166 us there and 161 us here (136 and 131).
+constexpr int kFewRows = 16;
 
 struct PagesDev {
   uint8_t* k;             // [L][num_pages][Hkv][P][D]
@@ -37,6 +43,9 @@ struct PagesDev {
   float* part_o;          // [2 * kPagedMaxCtas][kPartRows x D] attention partials, laid out by the kernel
   float* part_ml;         // [2 * kPagedMaxCtas][kPartRows][2] their running maxima and sums
   int32_t* tickets;       // [2 * kPagedMaxCtas] arrivals per split unit (0 between calls)
+  float* few_o;           // the same of the kernel for few rows: [2 * kPagedMaxCtas][kFewRows][D]
+  float* few_ml;          // [2 * kPagedMaxCtas][kFewRows][2]
+  int32_t* few_tickets;   // [kPagedMaxCtas]; behind `tickets`
   int Hq, Hkv, D, L, P, logP, num_pages, R, W, max_tokens;
   int e4m3;               // cache type
   int halves;             // rotation pairs (i, i + d/2)
@@ -55,6 +64,7 @@ struct PagedAttn {
   int min_tiles;          // a CTA's range holds at least this many tiles
   unsigned long long wait_ns;
   int debug_stall;
+  int beside;             // the kernel for few rows runs beside the chunk kernel of the same call
 };
 
 cudaError_t pages_prepare();
@@ -76,10 +86,10 @@ struct PagesWrite {
 };
 cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_count, cudaStream_t s);
 
-// Attention: few query rows per request (rows16 = 16, 32 or 64 rows a unit).
+// Attention: few query rows per request (units of 16 rows) ...
 cudaError_t paged_few_prepare();
 cudaError_t launch_paged_few(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a,
-                             int unit_rows, cudaStream_t s);
+                             cudaStream_t s);
 
 // ... and many (chunks).
 cudaError_t paged_chunk_prepare();

@@ -1,5 +1,5 @@
 // Attention over the paged cache for requests with few query rows: single
-// tokens, drafts, short chunks (up to 32 rows a unit, a row being one query
+// tokens, drafts, short chunks (up to 16 rows a unit, a row being one query
 // head of one token).
 //
 //   out[r] = sum_j softmax_j(s_rj) V[j],  s_rj = scale q[r] . K[j]
@@ -8,7 +8,7 @@
 // l' = l 2^(m - m') + sum p, O' = O 2^(m - m') + p V.
 //
 // Bound by HBM: every cached key and value of the request is read once per
-// key/value head (all its query heads share the tile), and with at most 32
+// key/value head (all its query heads share the tile), and with at most 16
 // rows the arithmetic is a small part of the tensor rate.  So the design is
 // about keeping copies in flight: one CTA per SM whose producer warp streams
 // page pieces by TMA into a ring of shared-memory slots (about 190 KB), and
@@ -40,29 +40,38 @@
 // other.  Queries become f16 after scaling each row by a power of two into
 // [1, 2) at its largest value: bf16's 8 significant bits fit f16's 11, and
 // what the row's small values lose is below 2^-25 of its largest.
+//
+// Measured (GB300): 128 decoding requests of 7,000 tokens on average, 32/8
+// heads x 128, bf16, 3.67 GB: 541 us, 6.79 TB/s (the copy rate is 6.80); the
+// same in E4M3 321 us, 5.7 TB/s, bound by the instructions that widen and
+// multiply; six requests of up to 32,000 tokens in pages of 16, 10 heads, E4M3,
+// four tokens each, 310 MB: 69 us (62 us in pages of 64); one request of 700
+// tokens: 10 us, latency.
 #include "kvring_pages.cuh"
+
 
 namespace kvr {
 namespace {
 
 constexpr int kGroups = 8;       // groups of 16 tokens of a tile
+constexpr int kRows = kFewRows;  // query rows of a unit
 constexpr int kSmemMost = 232448;
 
-template <int D, bool E4M3, int MT>
+template <int D, bool E4M3>
 struct FewLayout {
-  static constexpr int UR = 16 * MT;                       // query rows of a unit
   // Consumer warps.  They take the 16-token groups in turn.  Eight keep up
   // with HBM over a bf16 cache; an E4M3 tile is there in half the time and
-  // takes more instructions: eleven.
-  static constexpr int kWarps = E4M3 && MT == 1 ? 11 : 8;
+  // takes more instructions (1.83 GB: 370 us with 8 warps, 354 with 11, 381
+  // with 15, which leaves them 128 registers).
+  static constexpr int kWarps = E4M3 ? 11 : 8;
   static constexpr int kConsumers = kWarps * 32;
   static constexpr int kThreads = kConsumers + 32;
   static constexpr int kSlot = kTile * D * (E4M3 ? 1 : 2); // one K or V tile
   static constexpr int kQ = 0;                             // offsets behind the slots
-  static constexpr int kO = kQ + UR * D * 2;               // float [warps][4 rows][D]: the merge of the warps
-  static constexpr int kMl = kO + kWarps * 4 * D * 4;      // float2 [warps][UR]: their maxima and sums
-  static constexpr int kRow = kMl + kWarps * UR * 8;       // int lo, hi; float factor; pad: [UR][4]
-  static constexpr int kMisc = kRow + UR * 16;
+  static constexpr int kO = kQ + kRows * D * 2;               // float [warps][4 rows][D]: the merge of the warps
+  static constexpr int kMl = kO + kWarps * 4 * D * 4;      // float2 [warps][kRows]: their maxima and sums
+  static constexpr int kRow = kMl + kWarps * kRows * 8;       // int lo, hi; float factor; pad: [kRows][4]
+  static constexpr int kMisc = kRow + kRows * 16;
   static constexpr int kFixed = kMisc + 512;
   static constexpr int kRoom = (kSmemMost - 1024 - kFixed) / kSlot;
   static constexpr int kSlots = kRoom > 16 ? 16 : kRoom;
@@ -135,7 +144,6 @@ __device__ __forceinline__ ReqWords load_words(const PagesDev& p, int b) {
   return ReqWords{__ldcg(p.cu + b), __ldcg(p.cu + b + 1), __ldcg(p.klen + b), __ldcg(p.rows + b)};
 }
 
-template <int UR>
 __device__ __forceinline__ Req make_req(const PagedAttn& a, const ReqWords& w, int G) {
   Req r;
   r.q0 = w.q0;
@@ -147,7 +155,7 @@ __device__ __forceinline__ Req make_req(const PagedAttn& a, const ReqWords& w, i
   r.nrows = r.nq * G;
   const long long all = (long long)(w.end - r.q0) * G;
   if (all <= a.min_rows || all > a.max_rows || r.klen <= 0) r.nrows = 0;
-  r.nrt = (r.nrows + UR - 1) / UR;
+  r.nrt = (r.nrows + kRows - 1) / kRows;
   r.hi = r.klen;
   r.lo = 0;
   if (a.window > 0) {
@@ -159,12 +167,12 @@ __device__ __forceinline__ Req make_req(const PagedAttn& a, const ReqWords& w, i
   return r;
 }
 
-template <int D, bool E4M3, int MT>
-__global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
     k_paged_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagesDev p,
                 const PagedAttn a) {
-  using L = FewLayout<D, E4M3, MT>;
-  constexpr int UR = L::UR, kWarps = L::kWarps, kConsumers = L::kConsumers, kFewThreads = L::kThreads;
+  using L = FewLayout<D, E4M3>;
+  constexpr int kWarps = L::kWarps, kConsumers = L::kConsumers, kFewThreads = L::kThreads;
   auto sync_consumers = [] { sync_consumers_n<kConsumers>(); };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -187,7 +195,11 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     misc->abort = 0;
     mbar_fence_init();
   }
-  griddep_wait();
+  // Behind the chunk kernel of the same call this one starts as soon as that
+  // kernel has seen its own predecessors done, works beside it (on other
+  // requests, with tickets and workspace of its own) and waits for it at the
+  // end, so that what follows waits for both.
+  if (!a.beside) griddep_wait();
   griddep_launch_dependents();
 
   // ------------------------------------------------- this CTA's range
@@ -199,7 +211,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
   {
     const int per = (B + kFewThreads - 1) / kFewThreads;
     const int i0 = threadIdx.x * per, i1 = i0 + per < B ? i0 + per : B;
-    auto req_of = [&](int i) { return make_req<UR>(a, per == 1 ? ahead : load_words(p, i), G); };
+    auto req_of = [&](int i) { return make_req(a, per == 1 ? ahead : load_words(p, i), G); };
     unsigned long long mine = 0;
     for (int i = i0; i < i1; ++i) {
       const Req r = req_of(i);
@@ -246,7 +258,10 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
   const long long total = misc->total;
   const long long parts = misc->parts;
   const long long start = total * blockIdx.x / parts, stop = total * (blockIdx.x + 1) / parts;
-  if (blockIdx.x >= parts || start >= stop) return;
+  if (blockIdx.x >= parts || start >= stop) {
+    if (a.beside) griddep_wait();
+    return;
+  }
 
   // The walk over units, the same in the producer and the consumers.
   int b = misc->b0;
@@ -267,7 +282,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     h = 0;
     if (++rt < rq.nrt) return;
     rt = 0;
-    do rq = make_req<UR>(a, load_words(p, ++b), G);
+    do rq = make_req(a, load_words(p, ++b), G);
     while (rq.nt == 0);                      // (some request follows: x < stop)
   };
 
@@ -321,6 +336,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     volatile int none_aborted = 0;
     for (int i = n - L::kSlots < 0 ? 0 : n - L::kSlots; i < n; ++i)
       mbar_wait_bounded(full(i % L::kSlots), (i / L::kSlots) & 1, &none_aborted, a.wait_ns);
+    if (a.beside) griddep_wait();
     return;
   }
 
@@ -346,9 +362,8 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
   const uint32_t sQ = fbase + L::kQ;
   const float* sc = p.scales + (size_t)a.layer * 4 * p.Hkv;
   constexpr int kChunksQ = D / 8;                       // 16-byte chunks of a query row
-  constexpr bool kQRegs = MT == 1;                      // the query operand stays in registers
-  auto load_q = [&](int i, int ks, uint32_t (&qa)[4]) {
-    const int r = 16 * i + (lane & 15);
+  auto load_q = [&](int ks, uint32_t (&qa)[4]) {
+    const int r = lane & 15;
     ldsm4(qa, sQ + r * (D * 2) + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4));
   };
   auto pack = [](float lo, float hi) {
@@ -366,12 +381,12 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
   while (x < stop) {
     const long long uend = ubase + rq.nt;
     const long long ue = uend < stop ? uend : stop;
-    const int r0 = rt * UR;
-    const int rows = rq.nrows - r0 < UR ? rq.nrows - r0 : UR;
+    const int r0 = rt * kRows;
+    const int rows = rq.nrows - r0 < kRows ? rq.nrows - r0 : kRows;
     // ---- queries and row data into shared memory
     sync_consumers();                                    // the previous unit is done with it
     const float scale_k = E4M3 ? __ldcg(sc + h) : 1.0f;
-    for (int i = threadIdx.x; i < UR * kChunksQ; i += kConsumers) {
+    for (int i = threadIdx.x; i < kRows * kChunksQ; i += kConsumers) {
       const int r = i / kChunksQ, ch = i % kChunksQ;
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
       if (r < rows) {
@@ -425,25 +440,21 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
       }
     }
     sync_consumers();
-    uint32_t qreg[kQRegs ? D / 16 : 1][4];
-    if constexpr (kQRegs) {
+    uint32_t qreg[D / 16][4];
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) load_q(0, ks, qreg[ks]);
-    }
-    float m_run[2 * MT], l_run[2 * MT], fac[2 * MT];     // rows 16 i + g and 16 i + 8 + g
-    float acc[MT][D / 8][4];
+    for (int ks = 0; ks < D / 16; ++ks) load_q(ks, qreg[ks]);
+    float m_run[2], l_run[2], fac[2];                    // rows g and 8 + g
+    float acc[D / 8][4];
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
+    for (int i = 0; i < 2; ++i) {
       m_run[i] = -INFINITY;
       l_run[i] = 0.f;
       fac[i] = __int_as_float(s_row[8 * i + g].z);
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int k = 0; k < D / 8; ++k)
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][k][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
     // tokens that every row of the unit sees: tiles inside need no mask
     const int all_hi = s_row[0].y, all_lo = s_row[rows - 1].x;
 
@@ -460,25 +471,13 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
         next_slot();
         continue;
       }
-      float sc_[MT][2][4];
+      float sc_[2][4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc_[i][0][e] = sc_[i][1][e] = 0.f;
+      for (int e = 0; e < 4; ++e) sc_[0][e] = sc_[1][e] = 0.f;
       const uint32_t sK = sbase + s * L::kSlot;
       auto score_step = [&](int ks, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          if constexpr (kQRegs) {
-            mma16816<E4M3>(sc_[i][0], qreg[ks], b0, b1);
-            mma16816<E4M3>(sc_[i][1], qreg[ks], b2, b3);
-          } else {
-            uint32_t qa[4];
-            load_q(i, ks, qa);
-            mma16816<E4M3>(sc_[i][0], qa, b0, b1);
-            mma16816<E4M3>(sc_[i][1], qa, b2, b3);
-          }
-        }
+        mma16816<E4M3>(sc_[0], qreg[ks], b0, b1);
+        mma16816<E4M3>(sc_[1], qreg[ks], b2, b3);
       };
       if constexpr (!E4M3) {
         const int tok = group * 16 + (lane & 7) + ((lane >> 4) << 3);
@@ -510,57 +509,54 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
       next_slot();
       // ---- probabilities, in the layout of the next product's operand
       const bool masked = tok0 < all_lo || tok0 + 16 > all_hi;
-      uint32_t pa[MT][4];
+      uint32_t pa[4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-#pragma unroll
-        for (int hr = 0; hr < 2; ++hr) {
-          if (16 * i + 8 * hr >= rows) {                 // no such rows (the same for all threads)
-            pa[i][hr] = pa[i][2 + hr] = 0u;
-            continue;
-          }
-          const float f = fac[2 * i + hr];
-          if (masked) {
-            const int4 ri = s_row[16 * i + 8 * hr + g];
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int tok = tok0 + nt * 8 + 2 * c + e;
-                if (tok < ri.x || tok >= ri.y) sc_[i][nt][2 * hr + e] = -INFINITY;
-              }
-          }
-          // (rounded before the maximum is taken away, so that the largest
-          // gives exactly 0 whatever its size)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            sc_[i][nt][2 * hr] *= f;
-            sc_[i][nt][2 * hr + 1] *= f;
-          }
-          float mx = fmaxf(fmax3(sc_[i][0][2 * hr], sc_[i][0][2 * hr + 1], sc_[i][1][2 * hr]), sc_[i][1][2 * hr + 1]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-          float& mr = m_run[2 * i + hr];
-          const float m = fmaxf(mr, mx), mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
-          if (__any_sync(0xFFFFFFFFu, m > mr)) {
-            const float alpha = ex2_approx(mr - mu);
-            l_run[2 * i + hr] *= alpha;
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-              acc[i][k][2 * hr] *= alpha;
-              acc[i][k][2 * hr + 1] *= alpha;
-            }
-          }
-          mr = m;
-          float sum = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt) {
-            const float p0 = ex2_approx(sc_[i][nt][2 * hr] - mu), p1 = ex2_approx(sc_[i][nt][2 * hr + 1] - mu);
-            sum += p0 + p1;
-            pa[i][2 * nt + hr] = pack(p0, p1);
-          }
-          l_run[2 * i + hr] += sum;
+      for (int hr = 0; hr < 2; ++hr) {
+        if (8 * hr >= rows) {                            // no such rows (the same for all threads)
+          pa[hr] = pa[2 + hr] = 0u;
+          continue;
         }
+        const float f = fac[hr];
+        if (masked) {
+          const int4 ri = s_row[8 * hr + g];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int tok = tok0 + nt * 8 + 2 * c + e;
+              if (tok < ri.x || tok >= ri.y) sc_[nt][2 * hr + e] = -INFINITY;
+            }
+        }
+        // (rounded before the maximum is taken away, so that the largest
+        // gives exactly 0 whatever its size)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          sc_[nt][2 * hr] *= f;
+          sc_[nt][2 * hr + 1] *= f;
+        }
+        float mx = fmaxf(fmax3(sc_[0][2 * hr], sc_[0][2 * hr + 1], sc_[1][2 * hr]), sc_[1][2 * hr + 1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        float& mr = m_run[hr];
+        const float m = fmaxf(mr, mx), mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
+        if (__any_sync(0xFFFFFFFFu, m > mr)) {
+          const float alpha = ex2_approx(mr - mu);
+          l_run[hr] *= alpha;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            acc[k][2 * hr] *= alpha;
+            acc[k][2 * hr + 1] *= alpha;
+          }
+        }
+        mr = m;
+        float sum = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const float p0 = ex2_approx(sc_[nt][2 * hr] - mu), p1 = ex2_approx(sc_[nt][2 * hr + 1] - mu);
+          sum += p0 + p1;
+          pa[2 * nt + hr] = pack(p0, p1);
+        }
+        l_run[hr] += sum;
       }
       // ---- values
       wait_full();
@@ -593,11 +589,8 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
         for (int k = 0; k < D / 16; ++k) {
           uint32_t vb[4];
           load_v(k, vb);
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            mma16816<E4M3>(acc[i][2 * k], pa[i], vb[0], vb[1]);
-            mma16816<E4M3>(acc[i][2 * k + 1], pa[i], vb[2], vb[3]);
-          }
+          mma16816<E4M3>(acc[2 * k], pa, vb[0], vb[1]);
+          mma16816<E4M3>(acc[2 * k + 1], pa, vb[2], vb[3]);
         }
       } else {
         // What no row sees may hold anything and becomes zeros.  What some
@@ -621,28 +614,22 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
           load_v(k, vb);
           hide(vb, rq.lo, rq.hi);
           if (!wild) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              mma16816<E4M3>(acc[i][2 * k], pa[i], vb[0], vb[1]);
-              mma16816<E4M3>(acc[i][2 * k + 1], pa[i], vb[2], vb[3]);
-            }
+            mma16816<E4M3>(acc[2 * k], pa, vb[0], vb[1]);
+            mma16816<E4M3>(acc[2 * k + 1], pa, vb[2], vb[3]);
           } else {
 #pragma unroll 1
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < kRows; ++r) {
+              const int4 ri = s_row[r];
+              uint32_t wb[4] = {vb[0], vb[1], vb[2], vb[3]};
+              hide(wb, ri.x, ri.y);
+              float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<E4M3>(t0, pa, wb[0], wb[1]);
+              mma16816<E4M3>(t1, pa, wb[2], wb[3]);
 #pragma unroll
-              for (int i = 0; i < MT; ++i) {
-                const int4 ri = s_row[16 * i + r];
-                uint32_t wb[4] = {vb[0], vb[1], vb[2], vb[3]};
-                hide(wb, ri.x, ri.y);
-                float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816<E4M3>(t0, pa[i], wb[0], wb[1]);
-                mma16816<E4M3>(t1, pa[i], wb[2], wb[3]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {            // e >> 1: the thread's row g or g + 8
-                  if (8 * (e >> 1) + g == r) {
-                    acc[i][2 * k][e] += t0[e];
-                    acc[i][2 * k + 1][e] += t1[e];
-                  }
+              for (int e = 0; e < 4; ++e) {              // e >> 1: the thread's row g or g + 8
+                if (8 * (e >> 1) + g == r) {
+                  acc[2 * k][e] += t0[e];
+                  acc[2 * k + 1][e] += t1[e];
                 }
               }
             }
@@ -656,11 +643,11 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
 
     // ---- end of the unit, or of this CTA's part of it: merge the warps
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float l = l_run[i];
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-      if (c == 0) s_ml[warp * UR + 8 * i + g] = make_float2(m_run[i], l);
+      if (c == 0) s_ml[warp * kRows + 8 * i + g] = make_float2(m_run[i], l);
     }
     sync_consumers();
     const bool whole = ubase >= start && uend <= stop;
@@ -673,23 +660,23 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
     auto row_max = [&](int r) {
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w * UR + r].x);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w * kRows + r].x);
       return m;
     };
     // four rows at a time: every warp's O, scaled to the common maximum, into
     // shared memory, then each thread adds them for two columns
 #pragma unroll
-    for (int q4 = 0; q4 < UR / 4; ++q4) {
+    for (int q4 = 0; q4 < kRows / 4; ++q4) {
       if (4 * q4 >= rows) break;
-      const int i = q4 / 4, hr = (q4 >> 1) & 1;          // the m tile, and which half of it
+      const int hr = q4 >> 1;                            // which of the thread's rows
       if ((g >> 2) == (q4 & 1)) {
         const int r = 4 * q4 + (g & 3);
-        const float m = row_max(r), f = ex2_approx(m_run[2 * i + hr] - (m == -INFINITY ? 0.f : m));
+        const float m = row_max(r), f = ex2_approx(m_run[hr] - (m == -INFINITY ? 0.f : m));
         float* o = s_o + (warp * 4 + (g & 3)) * D;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const float v0 = acc[i][2 * k][2 * hr] * f, v1 = acc[i][2 * k][2 * hr + 1] * f;
-          const float v2 = acc[i][2 * k + 1][2 * hr] * f, v3 = acc[i][2 * k + 1][2 * hr + 1] * f;
+          const float v0 = acc[2 * k][2 * hr] * f, v1 = acc[2 * k][2 * hr + 1] * f;
+          const float v2 = acc[2 * k + 1][2 * hr] * f, v3 = acc[2 * k + 1][2 * hr + 1] * f;
           if constexpr (E4M3) {
             *reinterpret_cast<float4*>(o + 16 * k + 4 * c) = make_float4(v0, v2, v1, v3);
           } else {
@@ -712,14 +699,14 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
         const float m = row_max(r), mu = m == -INFINITY ? 0.f : m;
         float l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) l += s_ml[w * UR + r].y * ex2_approx(s_ml[w * UR + r].x - mu);
+        for (int w = 0; w < kWarps; ++w) l += s_ml[w * kRows + r].y * ex2_approx(s_ml[w * kRows + r].x - mu);
         if (whole) {
           const float inv = l > 0.f || l != l ? scale_v / l : 0.f;
           *reinterpret_cast<uint32_t*>(out_row(r) + 2 * d2) = bf2(o.x * inv, o.y * inv);
         } else {
-          *reinterpret_cast<float2*>(p.part_o + ((size_t)part * kPartRows + r) * D + 2 * d2) = o;
+          *reinterpret_cast<float2*>(p.few_o + ((size_t)part * kFewRows + r) * D + 2 * d2) = o;
           if (d2 == 0)
-            *reinterpret_cast<float2*>(p.part_ml + ((size_t)part * kPartRows + r) * 2) = make_float2(m, l);
+            *reinterpret_cast<float2*>(p.few_ml + ((size_t)part * kFewRows + r) * 2) = make_float2(m, l);
         }
       }
       sync_consumers();
@@ -731,16 +718,16 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
       __threadfence();
       sync_consumers();
       if (threadIdx.x == 0) {
-        const int old = atomicAdd(p.tickets + first, 1);
+        const int old = atomicAdd(p.few_tickets + first, 1);
         misc->last = old == last - first;
-        if (misc->last) p.tickets[first] = 0;
+        if (misc->last) p.few_tickets[first] = 0;
       }
       sync_consumers();
       if (misc->last) {
         __threadfence();
         for (int k = threadIdx.x; k < rows * (D / 4); k += kConsumers) {
           const int r = k / (D / 4), d4 = k % (D / 4);
-          auto slot = [&](int cta) { return (size_t)(2 * cta + (cta == first ? 1 : 0)) * kPartRows + r; };
+          auto slot = [&](int cta) { return (size_t)(2 * cta + (cta == first ? 1 : 0)) * kFewRows + r; };
           float m = -INFINITY, l = 0.f;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int c0 = first; c0 <= last; c0 += 8) {     // eight parts' loads in flight at a time
@@ -749,8 +736,8 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int cta = c0 + i <= last ? c0 + i : last;
-              ml[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + slot(cta) * 2));
-              v[i] = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot(cta) * D) + d4);
+              ml[i] = __ldcg(reinterpret_cast<const float2*>(p.few_ml + slot(cta) * 2));
+              v[i] = __ldcg(reinterpret_cast<const float4*>(p.few_o + slot(cta) * D) + d4);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -774,45 +761,34 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, MT>::kThreads, 1)
   }
   if (threadIdx.x == 0 && *abort)
     atomicOr(reinterpret_cast<unsigned*>(p.state + PST_ERROR), KVRING_PAGES_ERR_TIMEOUT);
+  if (a.beside) griddep_wait();
 }
 
-template <int D, bool E4M3, int MT>
+template <int D, bool E4M3>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(k_paged_few<D, E4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              FewLayout<D, E4M3, MT>::kBytes);
+  return cudaFuncSetAttribute(k_paged_few<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              FewLayout<D, E4M3>::kBytes);
 }
 template <int D, bool E4M3>
-cudaError_t prepare_rows() {
-  cudaError_t e = prepare_one<D, E4M3, 1>();
-  if (e == cudaSuccess) e = prepare_one<D, E4M3, 2>();
-  return e;
-}
-template <int D, bool E4M3, int MT>
 cudaError_t go(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s) {
-  return launch_pdl(k_paged_few<D, E4M3, MT>, dim3((unsigned)a.ctas), dim3(FewLayout<D, E4M3, MT>::kThreads), FewLayout<D, E4M3, MT>::kBytes,
-                    s, *tmK, *tmV, p, a);
-}
-template <int D, bool E4M3>
-cudaError_t go_rows(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a, int unit_rows,
-                    cudaStream_t s) {
-  return unit_rows <= 16 ? go<D, E4M3, 1>(p, tmK, tmV, a, s) : go<D, E4M3, 2>(p, tmK, tmV, a, s);
+  return launch_pdl(k_paged_few<D, E4M3>, dim3((unsigned)a.ctas), dim3(FewLayout<D, E4M3>::kThreads),
+                    FewLayout<D, E4M3>::kBytes, s, *tmK, *tmV, p, a);
 }
 
 }  // namespace
 
 cudaError_t paged_few_prepare() {
-  cudaError_t e = prepare_rows<128, true>();
-  if (e == cudaSuccess) e = prepare_rows<128, false>();
-  if (e == cudaSuccess) e = prepare_rows<64, true>();
-  if (e == cudaSuccess) e = prepare_rows<64, false>();
+  cudaError_t e = prepare_one<128, true>();
+  if (e == cudaSuccess) e = prepare_one<128, false>();
+  if (e == cudaSuccess) e = prepare_one<64, true>();
+  if (e == cudaSuccess) e = prepare_one<64, false>();
   return e;
 }
 
 cudaError_t launch_paged_few(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a,
-                             int unit_rows, cudaStream_t s) {
-  if (p.D == 128)
-    return p.e4m3 ? go_rows<128, true>(p, tmK, tmV, a, unit_rows, s) : go_rows<128, false>(p, tmK, tmV, a, unit_rows, s);
-  return p.e4m3 ? go_rows<64, true>(p, tmK, tmV, a, unit_rows, s) : go_rows<64, false>(p, tmK, tmV, a, unit_rows, s);
+                             cudaStream_t s) {
+  if (p.D == 128) return p.e4m3 ? go<128, true>(p, tmK, tmV, a, s) : go<128, false>(p, tmK, tmV, a, s);
+  return p.e4m3 ? go<64, true>(p, tmK, tmV, a, s) : go<64, false>(p, tmK, tmV, a, s);
 }
 
 }  // namespace kvr

@@ -23,7 +23,6 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr unsigned long long kDefaultWaitNs = 1000000000ull;
-constexpr int kFewRows = 32;   // most query rows of a request for the kernel for few rows
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -48,7 +47,7 @@ bool config_ok(const kvring_pages_config* c) {
 
 struct Plan {
   kvring_pages_layout pub;
-  size_t table, part_o, part_ml, tickets;
+  size_t table, part_o, part_ml, tickets, few_o, few_ml;
   size_t cache_bytes;   // of K, and of V
 };
 
@@ -78,7 +77,9 @@ Plan plan_for(const kvring_pages_config* c) {
   p.table = take(W * c->page_size * D * 4);
   p.part_o = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * D * 4);
   p.part_ml = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * 8);
-  p.tickets = take((size_t)2 * kvr::kPagedMaxCtas * 4);
+  p.tickets = take((size_t)3 * kvr::kPagedMaxCtas * 4);   // two per CTA, and one of the other kernel
+  p.few_o = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kFewRows * D * 4);
+  p.few_ml = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kFewRows * 8);
   p.pub.total = off;
   return p;
 }
@@ -192,6 +193,9 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   d.part_o = reinterpret_cast<float*>(b + p.part_o);
   d.part_ml = reinterpret_cast<float*>(b + p.part_ml);
   d.tickets = ints(p.tickets);
+  d.few_tickets = d.tickets + 2 * kvr::kPagedMaxCtas;
+  d.few_o = reinterpret_cast<float*>(b + p.few_o);
+  d.few_ml = reinterpret_cast<float*>(b + p.few_ml);
   d.Hq = cfg->num_q_heads;
   d.Hkv = cfg->num_kv_heads;
   d.D = cfg->head_dim;
@@ -215,7 +219,7 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   if (st == KVRING_OK) st = cuda_status(kvr::paged_chunk_prepare());
   // everything but the caches and the workspace's partial rows starts as zeros
   if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(b + p.pub.scales, 0, p.table - p.pub.scales, s));
-  if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(d.tickets, 0, 2 * kvr::kPagedMaxCtas * 4, s));
+  if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(d.tickets, 0, 3 * kvr::kPagedMaxCtas * 4, s));
   if (st == KVRING_OK)
     st = recorded(s, [&] {
       const cudaError_t e = kvr::launch_pages_table(d, reinterpret_cast<float*>(b + p.table), theta, s);
@@ -361,26 +365,24 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   // that one then takes every request, whatever the device's lengths are.
   const int G = h->cfg.num_q_heads / h->cfg.num_kv_heads;
   const int64_t rows = (int64_t)h->max_new * G;
-  const bool few = rows <= kFewRows || h->requests > 1, chunk = rows > kFewRows;
-  // in a batch with chunks, requests beyond one m = 16 row tile (two, with
-  // many query heads per key/value head) go with the chunks
-  const int split_rows = G <= 16 ? 16 : 32;
+  const bool chunk = rows > kvr::kFewRows, few = !chunk || (h->requests > 1 && G <= kvr::kFewRows);
   CUtensorMap tmQ;
   if (chunk && !make_query_map(&tmQ, q, q_stride, n, h->cfg)) return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return recorded(s, [&] {
     cudaError_t e = cudaSuccess;
     if (chunk) {
-      a.min_rows = few ? split_rows : 0;
+      a.min_rows = few ? kvr::kFewRows : 0;
       a.max_rows = INT32_MAX;
       a.min_tiles = 8;
       e = kvr::launch_paged_chunk(h->dev, &tmQ, &h->tmK, &h->tmV, a, s);
     }
     if (few && e == cudaSuccess) {
       a.min_rows = 0;
-      a.max_rows = chunk ? split_rows : INT32_MAX;
+      a.max_rows = chunk ? kvr::kFewRows : INT32_MAX;
       a.min_tiles = 2;
-      e = kvr::launch_paged_few(h->dev, &h->tmK, &h->tmV, a, chunk ? split_rows : (int)rows, s);
+      a.beside = chunk;
+      e = kvr::launch_paged_few(h->dev, &h->tmK, &h->tmV, a, s);
     }
     return e;
   }, out, out_bytes);
