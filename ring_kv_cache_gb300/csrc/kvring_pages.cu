@@ -334,16 +334,19 @@ __global__ void k_pages_table(float* table, const Thetas th, int half, size_t n)
 // queries and once for the keys and kept for all heads: with the weights
 // applied separately the kernel was bound by issuing instructions (153 per
 // warp and head row).  A block takes the tokens of one warp (2 or 4) and its
-// eight warps walk the heads; loads of a batch of heads go out together,
+// four warps walk the heads; loads of a batch of heads go out together,
 // those of the first batch and of the first key and value before anything
 // else is known.  Measured (GB300): 16,384 tokens, 32/8 heads x 128, bf16 cache,
-// 411 MB: 73.5 us, 5.6 TB/s (82 % of the copy rate; issue slots 54 % busy); 757
-// tokens of 40 heads into an E4M3 cache, 39 MB: 8.8 us; nine tokens: 1.9 us.
-constexpr int kWriteWarps = 8;
-constexpr int kWriteBatch = 2;   // (with four resident blocks; 3: 77 us, 4 with three blocks: 85 us)
+// 411 MB: 65.2 us, 6.3 TB/s (93 % of the copy rate); 757 tokens of 40 heads into
+// an E4M3 cache, 39 MB: 8.5 us; nine tokens: 1.9 us.
+// Blocks of four warps with batches of four, eight on an SM: eight warps with
+// batches of two take 73.5 us (a finished warp's place stays empty until the
+// block's last is done), two warps with batches of four 66.8 us.
+constexpr int kWriteWarps = 4;
+constexpr int kWriteBatch = 4;
 
 template <int D, bool E4M3, bool HALVES>
-__global__ void __launch_bounds__(kWriteWarps * 32, 4)
+__global__ void __launch_bounds__(kWriteWarps * 32, 8)
     k_pages_write(const PagesDev p, const PagesWrite w) {
   constexpr int LPR = D / 8, TPW = 32 / LPR;
   const int lane = threadIdx.x & 31, c = lane % LPR;
@@ -551,9 +554,9 @@ cudaError_t launch_pages_release(const PagesDev& p, const int32_t* rows, int B, 
 cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_count, cudaStream_t s) {
   const int tpw = 32 / (p.D / 8), blocks = (w.T + tpw - 1) / tpw;
   const int htot = p.Hq + 2 * p.Hkv, most = (htot + kWriteWarps - 1) / kWriteWarps;
-  // few tokens: split the heads over blocks too, until every SM has the four
+  // few tokens: split the heads over blocks too, until every SM has the eight
   // blocks that it holds
-  int split = (4 * sm_count + blocks - 1) / blocks;
+  int split = (8 * sm_count + blocks - 1) / blocks;
   split = split < 1 ? 1 : (split > most ? most : split);
   const dim3 grid((unsigned)blocks, (unsigned)split), block(kWriteWarps * 32);
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, s, p, w); };
