@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_release(const PagesDev p
     const int n = s_off[b + 1] - s_off[b];
     int32_t* row = p.tables + (size_t)s_row[b] * p.W;
     for (int w = threadIdx.x & 31; w < n; w += 32) {
-      p.free_pages[nfree + s_off[b] + w] = row[w];
+      p.free_pages[nfree + s_off[b] + w] = __ldcg(row + w);
       row[w] = -1;
     }
     if ((threadIdx.x & 31) == 0) p.lens[s_row[b]] = 0;
@@ -302,10 +302,11 @@ __global__ void k_pages_scales(const PagesDev p, int layer, const float* sk, con
   griddep_launch_dependents();
   float* dst = p.scales + (size_t)layer * 4 * p.Hkv;
   for (int h = threadIdx.x; h < p.Hkv; h += blockDim.x) {
-    dst[h] = sk[h];
-    dst[p.Hkv + h] = sv[h];
-    dst[2 * p.Hkv + h] = 1.0f / sk[h];
-    dst[3 * p.Hkv + h] = 1.0f / sv[h];
+    const float k = __ldcg(sk + h), v = __ldcg(sv + h);   // (past L1, as everywhere: see the write)
+    dst[h] = k;
+    dst[p.Hkv + h] = v;
+    dst[2 * p.Hkv + h] = 1.0f / k;
+    dst[3 * p.Hkv + h] = 1.0f / v;
   }
 }
 
