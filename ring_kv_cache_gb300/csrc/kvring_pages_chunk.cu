@@ -845,8 +845,14 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           if (masked) {
             const int vh = hi - t, vl = lo - t;
 #pragma unroll
-            for (int c = 0; c < L::kCols; ++c)
-              if (c >= vh || c < vl) sr[c] = __float_as_uint(-INFINITY);
+            for (int w = 0; w < L::kCols / 32; ++w) {
+              const int h = vh - 32 * w, l = vl - 32 * w;
+              uint32_t seen = h >= 32 ? 0xFFFFFFFFu : (h <= 0 ? 0u : (1u << h) - 1);
+              if (l > 0) seen &= l >= 32 ? 0u : ~0u << l;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(seen >> c & 1u)) sr[32 * w + c] = __float_as_uint(-INFINITY);
+            }
           }
           float mx[8];
 #pragma unroll
