@@ -379,6 +379,16 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// True in one thread of a converged warp, always the same.  Behind a branch on
+// this (not on the lane) the compiler knows that one thread runs: operands that
+// tcgen05 and TMA instructions take from uniform registers stay there, where
+// behind a branch on the lane each instruction moves its own over first (an MMA
+// took 50 cycles to issue so, and takes 6).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 // Arrive on an mbarrier once every previously issued tcgen05 op of this
 // thread has completed.
 __device__ __forceinline__ void mma_commit(uint32_t mbar) {

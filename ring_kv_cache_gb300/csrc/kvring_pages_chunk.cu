@@ -52,13 +52,10 @@
 // drawn are cleared by the next plan.
 //
 // Measured (GB300): 4,096 queries behind 12,288 cached tokens, causal, 32/8
-// heads x 128, bf16: 632 us, 1,520 TFLOP/s (81 % of the library product's
-// 1,884), over an E4M3 cache 671 us; 757 queries over 5,788 E4M3 tokens, 40
-// heads, all seen: 90 us (1,000 TFLOP/s; 120 units on 152 SMs, so nearly all
-// are split); 11 chunks of up to 900 tokens, window 1,500, 20/4 heads x 64:
-// 93 us.  ncu on 1,024 queries over 8,192 tokens: tensor pipe 53 % of the active
-// cycles, ALU 25 %, exponentials 27 %, issue 34 %: what is left is the chain of
-// scores, probabilities and product of each row group.
+// heads x 128, bf16: 612 us, 1,570 TFLOP/s (83 % of the library product's
+// 1,884); 757 queries over 5,788 E4M3 tokens, 40 heads, all seen: 85 us (1,050
+// TFLOP/s; 120 units on 152 SMs, so nearly all are split); 11 chunks of up to
+// 900 tokens, window 1,500, 20/4 heads x 64: 87 us.
 #include <type_traits>
 
 #include "kvring_pages.cuh"
@@ -535,7 +532,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     // thread for each, their products interleave, which cost 25 %), the two
     // token halves of a group at d = 64.  Commits are few and none lies
     // between a product and the next scores, where each cost 8 %.
-    if (lane == 0) {
+    if (elect_one()) {
       const int who = warp - L::kWarpIssue;
       constexpr uint32_t idesc_qk = idesc_16(128, L::kCols, false, !E4M3), idesc_pv = idesc_16(128, D, true, !E4M3);
       const uint64_t dq = smem_desc(sbase + L::kQ, 16, 1024, 2u), dk = smem_desc(sbase + L::kKV, 16, 1024, 2u);
