@@ -300,11 +300,14 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
       long long ue = ubase + rq.nt;
       const int32_t* tab = p.tables + (size_t)rq.row * p.W;
       ue = ue < stop ? ue : stop;
-      // A lane per page piece (8 at most), kind and 64-column half, so that a
-      // tile's copies go out in one go: with small pages it is their issue
-      // that takes the time (16 copies of 2 KB one kind after the other held
-      // a 16-token-page cache to 4.3 TB/s).  The next tile's page id is read a
-      // tile ahead.
+      // A lane per page piece (8 at most), kind and 64-column half reads its
+      // page id, a tile ahead, and waits for its slot.  With small pages it is
+      // the copies' issue that takes the time (16 of 2 KB, one kind after the
+      // other from 8 lanes, held a 16-token-page E4M3 cache to 4.3 TB/s).  Where
+      // a piece is one copy the elected thread issues them all: lanes move
+      // their operands to uniform registers in turn (128 decoding requests, E4M3
+      // in 16-token pages: 346 -> 331 us; d = 64 in bf16: 296 -> 293 us).  Where
+      // it is two, the lanes do (d = 128 in bf16: 543 us, 548 from one thread).
       const int box = lane & 7, kv = (lane >> 3) & 1, hf = lane >> 4;
       int tile = rq.t0 + (int)(x - ubase);
       auto page_of = [&](int t) -> int {
@@ -323,11 +326,31 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         const int mine = n + kv, s = mine % L::kSlots;
         stopped = !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(empty(s), ((mine / L::kSlots) & 1) ^ 1, abort, a.wait_ns));
         if (stopped) break;
-        if (box == 0 && hf == 0) mbar_arrive_expect_tx(full(s), (uint32_t)__popc(there) * kHalves * box_bytes);
-        __syncwarp();
-        if (page != -2)
-          tma_load_3d(sbase + s * L::kSlot + hf * (kTile * 128) + box * box_bytes, kv ? &tmV : &tmK, hf * 64, row0, c2,
-                      full(s));
+        if constexpr (kHalves == 1) {
+          int c2s[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c2s[i] = __shfl_sync(0xFFFFFFFFu, c2, i);
+          const int row_0 = __shfl_sync(0xFFFFFFFFu, row0, 0);   // (of the others 0: whole pages)
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int sk = (n + k) % L::kSlots;
+              mbar_arrive_expect_tx(full(sk), (uint32_t)__popc(there) * box_bytes);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (there >> i & 1)
+                  tma_load_3d(sbase + sk * L::kSlot + i * box_bytes, k ? &tmV : &tmK, 0, i == 0 ? row_0 : 0, c2s[i],
+                              full(sk));
+            }
+          }
+          __syncwarp();
+        } else {
+          if (box == 0 && hf == 0) mbar_arrive_expect_tx(full(s), (uint32_t)__popc(there) * kHalves * box_bytes);
+          __syncwarp();
+          if (page != -2)
+            tma_load_3d(sbase + s * L::kSlot + hf * (kTile * 128) + box * box_bytes, kv ? &tmV : &tmK, hf * 64, row0, c2,
+                        full(s));
+        }
         page = ahead;
       }
       if (x < stop && !stopped) next_unit();
