@@ -53,7 +53,7 @@
 //
 // Measured (GB300): 4,096 queries behind 12,288 cached tokens, causal, 32/8
 // heads x 128, bf16: 612 us, 1,570 TFLOP/s (83 % of the library product's
-// 1,884); 757 queries over 5,788 E4M3 tokens, 40 heads, all seen: 85 us (1,050
+// 1,884); 757 queries over 5,788 E4M3 tokens, 40 heads, all seen: 84 us (1,070
 // TFLOP/s; 120 units on 152 SMs, so nearly all are split); 11 chunks of up to
 // 900 tokens, window 1,500, 20/4 heads x 64: 87 us.
 #include <type_traits>
@@ -166,6 +166,7 @@ struct ChunkMisc {
   // ring slots: the copy landed (bf16 only), the helpers are done with it,
   // its MMAs have read it; and the E4M3 tiles before they are widened
   uint64_t full[11], ready[11], empty[11], raw_full[6], raw_empty[6];
+  uint64_t p_half[4];   // the first half of the probabilities there
   uint64_t done[2], grp[2];
   unsigned long long ws[24];
   long long total, base;
@@ -251,6 +252,11 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PagesDev p, const PagedAttn a) {
   using L = ChunkLayout<D, E4M3>;
+  // Probabilities handed over in two parts, so that the first half's product
+  // runs beside the second half's exponentials: over an E4M3 cache a gain (757
+  // queries over 5,788 tokens, 40 heads: 86.4 -> 83.8 us), over a bf16 one, whose
+  // scores wait for no helper, a loss (4,096 behind 12,288: 611 -> 630 us).
+  constexpr bool kTwo = D == 128 && E4M3;
   constexpr int kThreads = L::kThreads, kHelpThreads = 32 * L::kHelpers;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -279,6 +285,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     for (int i = 0; i < L::kStreams; ++i) {
       mbar_init(bar(misc->s_full[i]), 1);
       mbar_init(bar(misc->p_full[i]), 4);
+      mbar_init(bar(misc->p_half[i]), 4);
       mbar_init(bar(misc->pv[i]), 1);
       mbar_init(bar(misc->o_free[i]), 4 * L::kHalves);
     }
@@ -554,11 +561,11 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
                      k_at + (kk >> 2) * kAtomStep + 2 * (kk & 3), k_hi, idesc_qk, kk != 0);
         mma_commit(bar(misc->s_full[2 * who + i]));
       };
-      auto pv = [&](int i, int slot, bool first) {
+      auto pv = [&](int i, int slot, bool first, int k0, int k1) {
         const uint32_t v_at = v_lo + slot * kSlotStep + (L::kHalves == 1 ? 0 : i * kHalfStep);
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < L::kCols / 16; ++kk)
+        for (int kk = k0; kk < k1; ++kk)
           mma_f16_ts_w(tmem + L::col_o(2 * who + i), tmem + L::col_s(2 * who + i) + 8 * kk, v_at + kk * 128, v_hi,
                        idesc_pv, (!first || kk > 0) ? 1u : 0u);
       };
@@ -591,9 +598,17 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             for (int i = 0; i < ns; ++i) {
               const int st = 2 * who + i;
               if (i == 0) slot_ready(n + 1);
-              wait(misc->p_full[st], np[i]++ & 1);
-              if (j == 0) wait(misc->o_free[st], (no[i]++ & 1) ^ 1);
-              pv(i, (n + 1) % L::kSlots, j == 0);
+              if constexpr (kTwo) {
+                wait(misc->p_half[st], np[i] & 1);
+                if (j == 0) wait(misc->o_free[st], (no[i]++ & 1) ^ 1);
+                pv(i, (n + 1) % L::kSlots, j == 0, 0, L::kCols / 32);
+                wait(misc->p_full[st], np[i]++ & 1);
+                pv(i, (n + 1) % L::kSlots, false, L::kCols / 32, L::kCols / 16);
+              } else {
+                wait(misc->p_full[st], np[i]++ & 1);
+                if (j == 0) wait(misc->o_free[st], (no[i]++ & 1) ^ 1);
+                pv(i, (n + 1) % L::kSlots, j == 0, 0, L::kCols / 16);
+              }
               // (the next scores' commit tells the softmax of this product
               // too, except behind the last tile)
               if (!more) {
@@ -896,6 +911,14 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             uint32_t pw[16];
             probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
             tmem_st16(tS + 16 * c, pw);
+            if constexpr (kTwo) {
+              if (c + 1 == L::kCols / 64) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(misc->p_half[st]));
+              }
+            }
           }
           ell += lsum.x + lsum.y;
           tmem_wait_st();
