@@ -22,8 +22,11 @@
 // this one.  At d = 128: S_0, S_1, O_0, O_1, 128 columns each.  At d = 64 the
 // products are half as long and there is room for four streams of 128 columns,
 // each row group's tiles cut into two halves of 64 tokens with softmax warps and
-// sums of their own, added at the unit's end (windowed chunks 99 -> 92 us), and
-// for two units' queries in shared memory.
+// sums of their own, added at the unit's end, and for two units' queries in
+// shared memory.  (With whole tiles in two streams, probabilities in columns of
+// their own and each tile's scores computed while the tile before is turned into
+// probabilities, 2,048 queries over 32,768 tokens take 555 us instead of 470: eight
+// softmax warps are too few to keep the exponentials busy.)
 //
 // The (request, row tile, head, key tile) space is flattened and cut into
 // one contiguous range per CTA, as in the kernel for few rows; units cut by a
@@ -52,10 +55,14 @@
 // drawn are cleared by the next plan.
 //
 // Measured (GB300): 4,096 queries behind 12,288 cached tokens, causal, 32/8
-// heads x 128, bf16: 612 us, 1,570 TFLOP/s (83 % of the library product's
-// 1,884); 757 queries over 5,788 E4M3 tokens, 40 heads, all seen: 84 us (1,070
-// TFLOP/s; 120 units on 152 SMs, so nearly all are split); 11 chunks of up to
-// 900 tokens, window 1,500, 20/4 heads x 64: 87 us.
+// heads x 128, bf16: 600 to 620 us, 1,550 to 1,600 TFLOP/s (82 to 85 % of the
+// library product's 1,884, 92 to 95 % of what that keeps up for seconds); 757
+// queries over 5,788 E4M3 tokens, 40 heads, all seen: 84 us (1,070 TFLOP/s; 120
+// units on 152 SMs, so nearly all are split); 11 chunks of up to 900 tokens,
+// window 1,500, 20/4 heads x 64: 80 to 87 us.  At d = 128 a tile takes what a
+// group's chain does (softmax 1,550 cycles, then its two products behind the
+// other group's, 1,230), at d = 64 the issue of the softmax warps (59 % of the
+// slots; exponentials 44 %, ALU 42 %, tensor pipe 43 %).
 #include <type_traits>
 
 #include "kvring_pages.cuh"
@@ -536,9 +543,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
   } else if (warp >= L::kWarpIssue && warp < L::kWarpIssue + L::kIssuers) {
     // ------------------------------------------------- MMA issuers
     // One thread issues for two streams: both row groups at d = 128 (with a
-    // thread for each, their products interleave, which cost 25 %), the two
-    // token halves of a group at d = 64.  Commits are few and none lies
-    // between a product and the next scores, where each cost 8 %.
+    // thread for each, their products interleave: 612 -> 655 us), the two token
+    // halves of a group at d = 64.  Commits are few and none lies between a
+    // product and the next scores.
     if (elect_one()) {
       const int who = warp - L::kWarpIssue;
       constexpr uint32_t idesc_qk = idesc_16(128, L::kCols, false, !E4M3), idesc_pv = idesc_16(128, D, true, !E4M3);
