@@ -75,7 +75,7 @@ constexpr int kUnitQueue = 4;
 // A unit's start and end cost about as much as this many of its tiles (its
 // queries' way to the tensor cores, the last probabilities' and the results'
 // way out); ranges are cut by tiles plus this.
-constexpr int kUnitCost = 3;      // (8,192 causal queries: 676, 533, 401, 411 us with 0, 1, 3, 6)
+constexpr int kUnitCost = 3;      // (8,192 causal queries: 404, 372, 372, 380 us with 2, 3, 4, 6)
 constexpr int kTileBits = 40;     // of the sums over requests: places in the low bits, units above
 constexpr float kRaise = 8.0f;    // log2 units
 // Probabilities carry 2^kShift relative to the running maximum: with f16 the

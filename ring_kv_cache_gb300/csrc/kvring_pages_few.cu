@@ -45,7 +45,7 @@
 // heads x 128, bf16, 3.67 GB: 541 us, 6.79 TB/s (the copy rate is 6.80); the
 // same in E4M3 321 us, 5.7 TB/s, bound by the instructions that widen and
 // multiply; six requests of up to 32,000 tokens in pages of 16, 10 heads, E4M3,
-// four tokens each, 310 MB: 69 us (62 us in pages of 64); one request of 700
+// four tokens each, 310 MB: 65 us (61 us in pages of 64); one request of 700
 // tokens: 10 us, latency.
 #include "kvring_pages.cuh"
 
