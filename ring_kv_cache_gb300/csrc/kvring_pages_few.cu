@@ -56,6 +56,10 @@ namespace {
 constexpr int kGroups = 8;       // groups of 16 tokens of a tile
 constexpr int kRows = kFewRows;  // query rows of a unit
 constexpr int kSmemMost = 232448;
+// A running maximum is raised when a score exceeds it by more than this (log2
+// units; a probability is then at most 2^8, well within f16), so that sums are
+// rescaled about once per unit and not in every other step.
+constexpr float kFewRaise = 8.0f;
 
 template <int D, bool E4M3>
 struct FewLayout {
@@ -561,8 +565,9 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
         float& mr = m_run[hr];
-        const float m = fmaxf(mr, mx), mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
-        if (__any_sync(0xFFFFFFFFu, m > mr)) {
+        const bool need = mx > mr + kFewRaise || (mr == -INFINITY && mx > mr);
+        const float m = need ? mx : mr, mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
+        if (__any_sync(0xFFFFFFFFu, need)) {
           const float alpha = ex2_approx(mr - mu);
           l_run[hr] *= alpha;
 #pragma unroll
