@@ -684,8 +684,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             for (int k = 2 * ht; k < 2 * kTile * CPR; k += 2 * kHelpThreads) {
               const int row = (k >> 1) / CPR, c = (k >> 1) % CPR, tok = (u.tile0 + (j >> 1)) * kTile + row;
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-{
+              for (int e = 0; e < 2; ++e) {
                 uint4* at = reinterpret_cast<uint4*>(dst + (c >> 2) * L::kAtom + swz_offset(row, 2 * (c & 3) + e, 128));
                 bad |= clean_values<0x7C007C00u, 0x04000400u>(at, *at, tok >= u.vlo && tok < u.vhi);
               }

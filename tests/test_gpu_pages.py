@@ -291,6 +291,30 @@ def test_queries_of_any_size(cache, d, new):
     close(out[2], want[2], 2.0 ** -7 * want[2].abs() + 1e-6)
 
 
+@pytest.mark.parametrize("rise", [0.03, 0.4, 3.0])
+@pytest.mark.parametrize("d,new", [(128, 1), (128, 70), (64, 3), (64, 200)])
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_scores_that_keep_rising(cache, d, new, rise):
+    """Scores that grow by `rise` (log2 units) a token: running maxima that
+    are raised never, now and then or by every tile."""
+    total = 900
+    p, s = filled(2, 2, d, 32, [total], [new], cache, seed=14)
+    c = p.k_cache(0)
+    up = torch.arange(total, device="cuda") * (440.0 / total)
+    pages, off = p.tables[0, torch.arange(total, device="cuda") // 32].long(), torch.arange(total, device="cuda") % 32
+    x = c.float()
+    x[..., 0] = 0.0
+    x[pages, :, off, 0] = up[:, None].expand(total, 2)
+    c.copy_(x.to(c.dtype))
+    q = 0.05 * s["q"].float()
+    scale = s["sk"] if cache == "e4m3" else torch.ones(2, device="cuda")
+    q[..., 0] = rise * total / 440.0 / (scale * math.log2(math.e) / math.sqrt(d))
+    q = q.to(torch.bfloat16)
+    want, tol = attention_64(p, s, q=q)
+    close(p.attention(0, q), want, tol)
+    assert errors(p) == 0
+
+
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
 @pytest.mark.parametrize("cache", ["e4m3", "bf16"])
 @pytest.mark.parametrize("d,hq,hkv,total,new,bad,window", [
