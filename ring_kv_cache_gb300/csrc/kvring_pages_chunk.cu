@@ -663,7 +663,6 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             const int k = ht + i * kHelpThreads;
             w[i] = *reinterpret_cast<const uint4*>(src + swz_offset(k / CPR, k % CPR, D));
           }
-          mbar_arrive(bar(misc->raw_empty[rs]));
           wait(misc->empty[s], ((n / L::kSlots) & 1) ^ 1);
           uint8_t* dst = sm + L::kKV + s * L::kSlot;
 #pragma unroll
@@ -691,8 +690,12 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             }
             if (bad) *const_cast<volatile int*>(&misc->u[uq].wild) = 1;
           }
+          // (the E4M3 tile goes back only now: every value read from it is in
+          // use, and the fence stands between the reads and the next copy, which
+          // is of the other proxy)
           fence_proxy_async_smem();
           mbar_arrive(bar(misc->ready[s]));
+          mbar_arrive(bar(misc->raw_empty[rs]));
         }
       } else {
         // every landed tile passes through the helpers, nearly always untouched

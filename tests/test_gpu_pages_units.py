@@ -1,0 +1,49 @@
+"""Attention over the paged cache with so many units that every CTA has
+several whole ones: both row groups in use, last units that end inside a
+group, units cut by range borders, and the same bits from call to call."""
+import random
+
+import pytest
+import torch
+
+from _pagescheck import attention_64, close, errors, filled
+
+pytestmark = pytest.mark.gpu
+
+SMS = 160   # CTAs of an attention launch, at most
+
+
+def lengths(requests, tokens, heads_kv, per_unit, seed):
+    """New tokens and totals of `requests` requests of up to `tokens` tokens,
+    all of more than 16 query rows, with at least three units per CTA."""
+    r = random.Random(seed)
+    new = [r.randint(max(17, 2 * tokens // 3), tokens) for _ in range(requests - 1)] + [tokens]
+    units = sum(-(-n // per_unit) for n in new) * heads_kv
+    assert units >= 3 * SMS, units
+    assert any(n % per_unit % (per_unit // 2) for n in new)   # a last unit ends inside a group
+    return [n + r.choice([0, 1, 127, r.randint(0, 400)]) for n in new], new
+
+
+# (query heads, key/value heads, requests, most new tokens): Hq / Hkv of 1, 3, 4, 5, 7 and 8
+UNITS = [(40, 40, 10, 400), (60, 60, 1, 2200), (36, 12, 9, 500), (64, 16, 3, 900), (40, 8, 8, 500), (56, 8, 7, 400),
+         (64, 8, 4, 700), (32, 8, 10, 600)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,cache", [(128, "e4m3"), (64, "e4m3"), (128, "bf16")])
+@pytest.mark.parametrize("case", range(len(UNITS)))
+def test_many_whole_units_per_cta(case, d, cache, causal):
+    hq, hkv, requests, tokens = UNITS[case]
+    seed = 100 * case + d + causal
+    total, new = lengths(requests, tokens, hkv, 2 * (128 // (hq // hkv)), seed)
+    page = random.Random(seed).choice([16, 32, 64, 128, 256])
+    p, s = filled(hq, hkv, d, page, total, new, cache, seed=seed)
+    out = torch.full_like(s["q"], 9.0)
+    p.attention(0, s["q"], out=out, causal=causal)
+    want, tol = attention_64(p, s, causal=causal)
+    close(out, want, tol)
+    for i in range(20):
+        again = p.attention(0, s["q"], causal=causal)
+        differ = (again != out).any(-1).nonzero().tolist()
+        assert not differ, ("call", i, differ[:8], len(differ))
+    assert errors(p) == 0
