@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
     prefetch_tensormap(&tmV);
     for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), kGroups);
+      mbar_init(empty(s), kWarps);   // every consumer warp, those without a group of the tile too
     }
     misc->abort = 0;
     mbar_fence_init();
@@ -491,10 +491,15 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
       // ---- scores
       wait_full();
       if (kWarps > kGroups && group >= kGroups) {
-        // another's tile: only waited for, so that this warp stays within a
-        // phase of every slot's barrier
+        // another's tile: waited for and given back like an own one, so that
+        // no slot is filled again before every warp has seen it full (its
+        // barrier then never is two phases ahead of a waiting warp)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(s));
         next_slot();
         wait_full();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(s));
         next_slot();
         continue;
       }

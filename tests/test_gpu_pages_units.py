@@ -47,3 +47,26 @@ def test_many_whole_units_per_cta(case, d, cache, causal):
         differ = (again != out).any(-1).nonzero().tolist()
         assert not differ, ("call", i, differ[:8], len(differ))
     assert errors(p) == 0
+
+
+def same_bits(p, s, out, calls, **kw):
+    for i in range(calls):
+        again = p.attention(0, s["q"], **kw)
+        differ = (again != out).any(-1).nonzero().tolist()
+        assert not differ, ("call", i, differ[:8], len(differ))
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d,page,requests,most,new", [
+    (32, 8, 128, 64, 60, 4000, 1), (10, 10, 128, 16, 6, 12000, 4), (16, 2, 64, 32, 50, 3000, 2), (7, 1, 64, 16, 128, 2500, 2),
+    (8, 8, 64, 256, 30, 5000, 16)])
+def test_few_rows_over_many_tiles(hq, hkv, d, page, requests, most, new, cache):
+    """Hundreds of tiles per CTA, so that its warps have the room to drift apart."""
+    r = random.Random(requests)
+    total = [r.randint(most // 8, most) for _ in range(requests)]
+    p, s = filled(hq, hkv, d, page, total, [new] * requests, cache, seed=requests)
+    out = p.attention(0, s["q"])
+    want, tol = attention_64(p, s)
+    close(out, want, tol)
+    same_bits(p, s, out, 50)
+    assert errors(p) == 0
