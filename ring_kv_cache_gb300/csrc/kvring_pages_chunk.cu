@@ -120,8 +120,8 @@ struct ChunkLayout {
   static constexpr int kRawAt = kKV + kSlots * kSlot;
   static constexpr int kMisc = kRawAt + kRaws * kRaw;
   static constexpr int kMiscBytes = 1536;
-  static constexpr int kMl = kMisc + kMiscBytes;                 // float2 [2][halves][128]: their maxima and sums
-  static constexpr int kBytes = 1024 + kMl + (kHalves > 1 ? 2 * kHalves * kTile * 8 : 0);
+  static constexpr int kMl = kMisc + kMiscBytes;                 // float2 [2][2][halves][128]: their maxima and sums, by unit parity
+  static constexpr int kBytes = 1024 + kMl + (kHalves > 1 ? 4 * kHalves * kTile * 8 : 0);
   static_assert(kBytes <= kChunkSmem, "fits one CTA per SM");
 };
 
@@ -943,7 +943,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         // and ell those of the row.  A half's threads write half the columns.
         float w_half[2] = {1.0f, 1.0f};
         if constexpr (L::kHalves > 1) {
-          float2* ml = reinterpret_cast<float2*>(sm + L::kMl) + g * 2 * kTile + row;
+          // (two places in turn: a half may be through the next unit's tiles
+          // before the other has read this one's, but not through its exchange)
+          float2* ml = reinterpret_cast<float2*>(sm + L::kMl) + (2 * (nu_done & 1) + g) * 2 * kTile + row;
           ml[half * kTile] = make_float2(m_run, ell);
           sync_group();
           const float2 a0 = ml[0], a1 = ml[kTile];

@@ -24,13 +24,20 @@ def lengths(requests, tokens, heads_kv, per_unit, seed):
     return [n + r.choice([0, 1, 127, r.randint(0, 400)]) for n in new], new
 
 
+def same_bits(p, s, out, calls, **kw):
+    for i in range(calls):
+        again = p.attention(0, s["q"], **kw)
+        differ = (again != out).any(-1).nonzero().tolist()
+        assert not differ, ("call", i, differ[:8], len(differ))
+
+
 # (query heads, key/value heads, requests, most new tokens): Hq / Hkv of 1, 3, 4, 5, 7 and 8
 UNITS = [(40, 40, 10, 400), (60, 60, 1, 2200), (36, 12, 9, 500), (64, 16, 3, 900), (40, 8, 8, 500), (56, 8, 7, 400),
          (64, 8, 4, 700), (32, 8, 10, 600)]
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("d,cache", [(128, "e4m3"), (64, "e4m3"), (128, "bf16")])
+@pytest.mark.parametrize("d,cache", [(128, "e4m3"), (64, "e4m3"), (128, "bf16"), (64, "bf16")])
 @pytest.mark.parametrize("case", range(len(UNITS)))
 def test_many_whole_units_per_cta(case, d, cache, causal):
     hq, hkv, requests, tokens = UNITS[case]
@@ -42,18 +49,8 @@ def test_many_whole_units_per_cta(case, d, cache, causal):
     p.attention(0, s["q"], out=out, causal=causal)
     want, tol = attention_64(p, s, causal=causal)
     close(out, want, tol)
-    for i in range(20):
-        again = p.attention(0, s["q"], causal=causal)
-        differ = (again != out).any(-1).nonzero().tolist()
-        assert not differ, ("call", i, differ[:8], len(differ))
+    same_bits(p, s, out, 20, causal=causal)
     assert errors(p) == 0
-
-
-def same_bits(p, s, out, calls, **kw):
-    for i in range(calls):
-        again = p.attention(0, s["q"], **kw)
-        differ = (again != out).any(-1).nonzero().tolist()
-        assert not differ, ("call", i, differ[:8], len(differ))
 
 
 @pytest.mark.parametrize("cache", ["e4m3", "bf16"])
@@ -69,4 +66,42 @@ def test_few_rows_over_many_tiles(hq, hkv, d, page, requests, most, new, cache):
     want, tol = attention_64(p, s)
     close(out, want, tol)
     same_bits(p, s, out, 50)
+    assert errors(p) == 0
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("d,window", [(64, 0), (64, 60), (128, 60)])
+@pytest.mark.parametrize("hq,hkv,requests", [(8, 8, 120), (12, 4, 150), (16, 2, 200)])
+def test_units_of_one_tile(hq, hkv, requests, d, window, cache):
+    """A unit's end and the next one's only tile follow at once."""
+    r = random.Random(requests)
+    new = [r.randint(17, 40) for _ in range(requests)]
+    total = [n + r.randint(0, 80) for n in new]
+    p, s = filled(hq, hkv, d, 16, total, new, cache, seed=d)
+    out = p.attention(0, s["q"], window=window)
+    want, tol = attention_64(p, s, window=window)
+    close(out, want, tol)
+    same_bits(p, s, out, 50, window=window)
+    assert errors(p) == 0
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("hq,hkv,d,page,singles,chunks", [
+    (32, 8, 128, 64, 100, [900, 70]), (10, 10, 128, 16, 16, [757]), (20, 4, 64, 32, 128, [600, 33]), (7, 1, 64, 128, 60, [1500, 1])])
+def test_single_tokens_and_chunks_in_one_step(hq, hkv, d, page, singles, chunks, cache):
+    """Both kernels in one call, over a serving step's batch."""
+    r = random.Random(singles)
+    new = [1] * singles + chunks
+    r.shuffle(new)
+    total = [n + r.randint(0, 2500) for n in new]
+    p, s = filled(hq, hkv, d, page, total, new, cache, seed=singles, pad=3)
+    out = torch.full_like(s["q"], 9.0)
+    p.attention(0, s["q"], out=out)
+    n = sum(new)
+    want, tol = attention_64(p, s)
+    close(out[:n], want[:n], tol[:n])
+    for i in range(30):
+        again = torch.full_like(out, 9.0)
+        p.attention(0, s["q"], out=again)
+        assert torch.equal(again, out), i   # rows past the plan's among them
     assert errors(p) == 0
