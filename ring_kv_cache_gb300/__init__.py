@@ -524,6 +524,16 @@ def _i32(x) -> int:
     return x if -(1 << 31) <= x < 1 << 31 else (-1 if x < 0 else (1 << 31) - 1)
 
 
+def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
+    """A new tensor that ``stream`` (None: the current one) may write: memory
+    of that stream's own, which no work on another may still be using, and
+    which goes back to it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def kvring_pages_get_layout(cfg: KvringPagesConfig) -> KvringPagesLayout:
     lay = KvringPagesLayout()
     _check(lib().kvring_pages_get_layout(ctypes.byref(cfg), ctypes.byref(lay)), "kvring_pages_get_layout")
@@ -556,8 +566,9 @@ class KvPages:
     All of it runs on the device and can be captured in a CUDA graph.  Calls
     on one object must be ordered (one stream, or events); graphs that use
     one share its plan and workspace.  Every call runs with the object's
-    device current and takes tensors on it.  Its buffer is freed with the
-    object: keep it alive until the work enqueued on it has completed.
+    device current and takes tensors on it.  A tensor that a call with
+    ``stream`` makes belongs to that stream.  The object's buffer is freed with
+    it: keep it alive until the work enqueued on it has completed.
     """
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, num_pages: int, max_requests: int,
@@ -587,7 +598,7 @@ class KvPages:
             raise ValueError("invalid paged-cache config") from None
         self.nbytes = int(self.layout.total)
         with torch.cuda.device(self.device):
-            self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+            self.buf = _empty_on(stream, (self.nbytes,), torch.uint8, self.device)
             self.handle = kvring_pages_create(self.cfg, self.buf, stream)
         lay = self.layout
         self.lengths = self._ints(lay.lengths, self.R)
@@ -700,9 +711,9 @@ class KvPages:
             raise ValueError(f"{name}: the heads of a token must be contiguous, and tokens must not overlap")
         return n, st if n > 1 else row
 
-    def _result(self, x, n: int, name: str):
+    def _result(self, x, n: int, name: str, stream):
         if x is None:
-            return torch.empty((n, self.Hq, self.d), dtype=torch.bfloat16, device=self.device)
+            return _empty_on(stream, (n, self.Hq, self.d), torch.bfloat16, self.device)
         if self._heads(x, self.Hq, name) != (n, self.Hq * self.d):
             raise ValueError(f"{name} must be contiguous, [{n}, {self.Hq}, {self.d}]")
         return x
@@ -722,7 +733,7 @@ class KvPages:
             if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16
                                   or t.device != self.device or t.shape != (self.d,) or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{self.d}] on {self.device}")
-        q_out = self._result(q_out, n, "q_out")
+        q_out = self._result(q_out, n, "q_out", stream)
         self._call(_LIB.kvring_pages_write, "kvring_pages_write", stream, _i32(layer), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                    qs, ks, vs, _ptr(q_norm), _ptr(k_norm), float(eps), q_out.data_ptr(), n)
         return q_out
@@ -735,7 +746,7 @@ class KvPages:
         1/sqrt(d).  Rows of ``out`` past the plan's tokens are left as they
         were (undefined in a new tensor)."""
         n, qs = self._heads(q, self.Hq, "q")
-        out = self._result(out, n, "out")
+        out = self._result(out, n, "out", stream)
         self._call(_LIB.kvring_pages_attention, "kvring_pages_attention", stream, _i32(layer), q.data_ptr(), qs, out.data_ptr(),
                    n, 1 if causal else 0, _i32(window), float(scale))
         return out

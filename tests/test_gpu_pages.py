@@ -643,3 +643,55 @@ def test_refusals_of_the_binding():
     with pytest.raises(ValueError):
         p.restore(i32([1, 2]), p.tables, i32([0]))
     assert errors(p) == 0
+
+
+# ------------------------------------------------------------ other streams
+def busy(stream):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(40_000_000)   # some 20 ms
+
+
+def test_results_made_on_another_stream():
+    """Neither earlier work of the current stream, in memory that was freed
+    there, nor later work of it, in the result's once it is dropped, meets a
+    call on a stream of its own."""
+    p, s = filled(4, 2, 64, 32, [400, 300], [1, 200], "bf16", seed=9)
+    k = torch.ones((201, 2, 64), dtype=torch.bfloat16, device="cuda")
+    want, tol = attention_64(p, s)
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    before_k, before_v = p.k_cache(0).clone(), p.v_cache(0).clone()
+    q_want = p.write(0, s["q"], k, k)
+    p.k_cache(0).copy_(before_k)
+    p.v_cache(0).copy_(before_v)
+    torch.cuda.synchronize()
+    for call, result in ((lambda: p.attention(0, s["q"], stream=side), None),
+                         (lambda: p.write(0, s["q"], k, k, stream=side), q_want)):
+        olds = [torch.empty_like(s["q"]) for _ in range(4)]
+        busy(here)
+        for x in olds:
+            x.fill_(7.0)      # still to come when the call below runs
+        del olds, x
+        out = call()
+        torch.cuda.synchronize()
+        close(out, want, tol) if result is None else close(out, result.double(), 0.0)
+        busy(side)
+        out = call()
+        del out
+        later = [torch.full_like(s["q"], 7.0) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(bool((x == 7.0).all()) for x in later)
+
+
+def test_a_cache_made_on_another_stream():
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    make = lambda **kw: kv.KvPages(2, 1, 64, 16, 40, 6, 200, 64, **kw)  # noqa: E731
+    old = make().buf
+    n = old.numel()
+    torch.cuda.synchronize()
+    busy(here)
+    old.fill_(7)
+    del old
+    p = make(stream=side)
+    torch.cuda.synchronize()
+    assert p.nbytes == n and p.free_pages.tolist() == list(range(39, -1, -1))
+    assert p.lengths.tolist() == [0] * 6 and errors(p) == 0
