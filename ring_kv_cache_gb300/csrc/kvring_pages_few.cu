@@ -57,9 +57,15 @@ constexpr int kGroups = 8;       // groups of 16 tokens of a tile
 constexpr int kRows = kFewRows;  // query rows of a unit
 constexpr int kSmemMost = 232448;
 // A running maximum is raised when a score exceeds it by more than this (log2
-// units; a probability is then at most 2^8, well within f16), so that sums are
-// rescaled about once per unit and not in every other step.
+// units), so that sums are rescaled about once per unit and not in every other
+// step.
 constexpr float kFewRaise = 8.0f;
+// Probabilities carry 2^kFewShift relative to the running maximum, as the chunk
+// kernel's do: in f16 the largest is then 2^15 and those down to 2^-21 of the
+// maximum stay normal numbers.  What a row keeps, and what its parts are merged
+// by, is the offset that scores are taken relative to: the maximum less the shift.
+template <bool E4M3>
+constexpr float kFewShift = E4M3 ? 7.0f : 0.0f;
 
 template <int D, bool E4M3>
 struct FewLayout {
@@ -73,7 +79,7 @@ struct FewLayout {
   static constexpr int kSlot = kTile * D * (E4M3 ? 1 : 2); // one K or V tile
   static constexpr int kQ = 0;                             // offsets behind the slots
   static constexpr int kO = kQ + kRows * D * 2;               // float [warps][4 rows][D]: the merge of the warps
-  static constexpr int kMl = kO + kWarps * 4 * D * 4;      // float2 [warps][kRows]: their maxima and sums
+  static constexpr int kMl = kO + kWarps * 4 * D * 4;      // float2 [warps][kRows]: their offsets and sums
   static constexpr int kRow = kMl + kWarps * kRows * 8;       // int lo, hi; float factor; pad: [kRows][4]
   static constexpr int kMisc = kRow + kRows * 16;
   static constexpr int kFixed = kMisc + 512;
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
     uint32_t qreg[D / 16][4];
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) load_q(ks, qreg[ks]);
-    float m_run[2], l_run[2], fac[2];                    // rows g and 8 + g
+    float m_run[2], l_run[2], fac[2];                    // offsets, sums, factors of rows g and 8 + g
     float acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -570,8 +576,10 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
         float& mr = m_run[hr];
-        const bool need = mx > mr + kFewRaise || (mr == -INFINITY && mx > mr);
-        const float m = need ? mx : mr, mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
+        // (a difference, so that it holds for scores whose steps are coarser than
+        // the shift too; at the start, where mr is -inf, for anything but -inf)
+        const bool need = mx - mr > kFewRaise + kFewShift<E4M3>;
+        const float m = need ? mx - kFewShift<E4M3> : mr, mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
         if (__any_sync(0xFFFFFFFFu, need)) {
           const float alpha = ex2_approx(mr - mu);
           l_run[hr] *= alpha;

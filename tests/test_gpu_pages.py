@@ -695,3 +695,29 @@ def test_a_cache_made_on_another_stream():
     torch.cuda.synchronize()
     assert p.nbytes == n and p.free_pages.tolist() == list(range(39, -1, -1))
     assert p.lengths.tolist() == [0] * 6 and errors(p) == 0
+
+
+# -------------------------------------------------------- ranges of numbers
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_far_below_the_largest_over_e4m3(d, new):
+    """Values that only tokens of weight 2^-23.5 of the largest have, beside
+    it in the same tile: their probabilities keep their bits in f16."""
+    p, s = filled(2, 1, d, 16, [300], [new], "e4m3", seed=2, garbage=False)
+    k, v, q = torch.zeros_like(p.k_cache(0), dtype=torch.float32), torch.zeros_like(p.v_cache(0), dtype=torch.float32), s["q"]
+    ids = p.tables[0].long()
+    k[ids[200 // 16], 0, 200 % 16, 0] = 448.0
+    for j in range(192, 208):
+        v[ids[j // 16], 0, j % 16] = 0.0 if j == 200 else 448.0
+    p.k_cache(0).copy_(k.to(torch.float8_e4m3fn))
+    p.v_cache(0).copy_(v.to(torch.float8_e4m3fn))
+    s["sk"].fill_(23.5 * math.log(2.0) * math.sqrt(d) / 448.0)
+    s["sv"].fill_(1.0)
+    p.set_scales(0, s["sk"], s["sv"])
+    q.zero_()
+    q[..., 0] = 1.0
+    want, _ = attention_64(p, s)
+    # a probability of 2^-16.5 behind the shift of 2^7 in steps of 2^-24, the
+    # result to bf16, and 2^-12 for fp32 scores of 23.5 and their exponentials
+    close(p.attention(0, q), want, (2.0 ** -8.5 + 2.0 ** -8 + 2.0 ** -12) * want)
+    assert errors(p) == 0
