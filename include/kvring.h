@@ -471,7 +471,8 @@ kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const voi
  * out: bf16 [num_tokens][Hq][d], q with a token stride (elements, a multiple
  * of 8), out contiguous and not overlapping q; rows past the plan's tokens stay as
  * they were.  Scores, softmax statistics and sums are fp32; probabilities
- * are rounded once, to bf16 (f16 over an E4M3 cache).  Cached tokens that
+ * are rounded once, to bf16 (f16 over an E4M3 cache).  Finite cached values
+ * of any size give finite results at any length.  Cached tokens that
  * a query's mask hides do not affect it, whatever they hold. */
 kvring_status kvring_pages_attention(kvring_pages_t* pages, int32_t layer, const void* q, int64_t q_stride, void* out,
                                      int32_t num_tokens, int32_t causal, int32_t window, float scale, void* stream);

@@ -26,6 +26,18 @@ constexpr int kPartRows = 256;       // query rows of a workspace slot of the ch
 // and 346); requests of 8 to 16 rows 166 us there and 161 us here (136 and 131).
 constexpr int kFewRows = 16;
 
+// Both attention kernels raise a row's running maximum only when a score exceeds
+// it by more than kRaise (log2 units), so that sums are rescaled about once per
+// unit and not in every other tile, and probabilities carry 2^kShift relative to
+// it.  Over an E4M3 cache they become f16: the largest is then 2^15, and those down to
+// 2^-21 of the maximum stay normal numbers.  Over a bf16 cache the probabilities,
+// which become bf16, are at most 2^-24, so that the sums of 2^24 tokens' weighted
+// values stay finite as long as the values are; what a row weighs with less than 2^-94 of
+// its maximum counts as 0.
+constexpr float kRaise = 8.0f;
+template <bool E4M3>
+constexpr float kShift = E4M3 ? 7.0f : -32.0f;
+
 struct PagesDev {
   uint8_t* k;             // [L][num_pages][Hkv][P][D]
   uint8_t* v;

@@ -77,12 +77,6 @@ constexpr int kUnitQueue = 4;
 // way out); ranges are cut by tiles plus this.
 constexpr int kUnitCost = 3;      // (8,192 causal queries: 404, 372, 372, 380 us with 2, 3, 4, 6)
 constexpr int kTileBits = 40;     // of the sums over requests: places in the low bits, units above
-constexpr float kRaise = 8.0f;    // log2 units
-// Probabilities carry 2^kShift relative to the running maximum: with f16 the
-// largest is then 2^15 and small ones stay normal numbers; bf16 needs no shift,
-// and values near the end of its range no further factor.
-template <bool E4M3>
-constexpr float kShift = E4M3 ? 7.0f : 0.0f;
 constexpr int kChunkSmem = 232448;
 
 template <int D, bool E4M3>

@@ -56,16 +56,6 @@ namespace {
 constexpr int kGroups = 8;       // groups of 16 tokens of a tile
 constexpr int kRows = kFewRows;  // query rows of a unit
 constexpr int kSmemMost = 232448;
-// A running maximum is raised when a score exceeds it by more than this (log2
-// units), so that sums are rescaled about once per unit and not in every other
-// step.
-constexpr float kFewRaise = 8.0f;
-// Probabilities carry 2^kFewShift relative to the running maximum, as the chunk
-// kernel's do: in f16 the largest is then 2^15 and those down to 2^-21 of the
-// maximum stay normal numbers.  What a row keeps, and what its parts are merged
-// by, is the offset that scores are taken relative to: the maximum less the shift.
-template <bool E4M3>
-constexpr float kFewShift = E4M3 ? 7.0f : 0.0f;
 
 template <int D, bool E4M3>
 struct FewLayout {
@@ -576,10 +566,12 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
         float& mr = m_run[hr];
-        // (a difference, so that it holds for scores whose steps are coarser than
-        // the shift too; at the start, where mr is -inf, for anything but -inf)
-        const bool need = mx - mr > kFewRaise + kFewShift<E4M3>;
-        const float m = need ? mx - kFewShift<E4M3> : mr, mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
+        // What a row keeps, and what its parts are merged by, is the offset that
+        // scores are taken relative to: the maximum less the shift.  (Compared as
+        // a difference, so that it holds for scores whose steps are coarser than
+        // the shift too; at the start, where mr is -inf, for anything but -inf.)
+        const bool need = mx - mr > kRaise + kShift<E4M3>;
+        const float m = need ? mx - kShift<E4M3> : mr, mu = m == -INFINITY ? 0.f : m;   // nothing seen yet: p = 2^-inf = 0
         if (__any_sync(0xFFFFFFFFu, need)) {
           const float alpha = ex2_approx(mr - mu);
           l_run[hr] *= alpha;

@@ -721,3 +721,30 @@ def test_weights_far_below_the_largest_over_e4m3(d, new):
     # result to bf16, and 2^-12 for fp32 scores of 23.5 and their exponentials
     close(p.attention(0, q), want, (2.0 ** -8.5 + 2.0 ** -8 + 2.0 ** -12) * want)
     assert errors(p) == 0
+
+
+@pytest.mark.parametrize("rise", [0.0, 7.9])
+@pytest.mark.parametrize("d,total,new", [(128, 300, 1), (128, 6000, 60), (64, 5000, 3), (64, 700, 300), (128, 20000, 1)])
+def test_values_at_the_end_of_bf16(d, total, new, rise):
+    """Values up to 3.3e38 under scores that rise by less than what raises a
+    running maximum: sums over thousands of tokens that stay finite."""
+    p, s = filled(2, 2, d, 32, [total], [new], "bf16", seed=15, garbage=False)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    p.v_cache(0).copy_((1.0e38 + 2.3e38 * torch.rand(p.v_cache(0).shape, generator=g, device="cuda")).to(torch.bfloat16))
+    c, j = p.k_cache(0), torch.arange(total, device="cuda")
+    x = c.float()
+    x[..., 0] = 0.0
+    x[p.tables[0, j // 32].long(), :, j % 32, 0] = (j * (1.0 / total))[:, None].expand(total, 2)
+    c.copy_(x.to(torch.bfloat16))
+    q = 0.05 * s["q"].float()
+    q[..., 0] = rise * math.log(2.0) * math.sqrt(d)
+    q = q.to(torch.bfloat16)
+    want, tol = attention_64(p, s, q=q)
+    out = p.attention(0, q)
+    assert bool(torch.isfinite(out).all())
+    close(out, want, tol)
+    # and small ones keep theirs
+    p.v_cache(0).mul_(2.0 ** -190)
+    want, tol = attention_64(p, s, q=q)
+    close(p.attention(0, q).double() * 2.0 ** 100, want * 2.0 ** 100, (tol - 1e-30) * 2.0 ** 100)
+    assert errors(p) == 0
