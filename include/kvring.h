@@ -432,7 +432,9 @@ kvring_status kvring_pages_set_scales(kvring_pages_t* pages, int32_t layer, cons
  * Lengths and the free list change only with kvring_pages_commit: a plan
  * that is not committed is dropped by the next one and costs nothing.
  * A plan that cannot be made (rows, tokens, length or pages: see the error
- * bits) sets its error bit and plans no token for any request. */
+ * bits) sets its error bit and plans no token for any request.  A page id
+ * outside the pool does not stop a plan: it sets KVRING_PAGES_ERR_TABLE, its
+ * tokens get slot -1 and are not written, and attention reads zeros there. */
 kvring_status kvring_pages_plan(kvring_pages_t* pages, const int32_t* rows, const int32_t* new_tokens,
                                 int32_t num_requests, int32_t num_tokens, int32_t max_new, void* stream);
 
@@ -443,7 +445,8 @@ kvring_status kvring_pages_commit(kvring_pages_t* pages, void* stream);
  * order of `rows` (device int32), each request's first page first) and
  * their lengths to 0.  Rows that are already empty are allowed; a row out
  * of range or given twice sets KVRING_PAGES_ERR_ROW and nothing is
- * released.  Drops a plan that awaits its commit, and empties the step. */
+ * released.  A table entry that is no page of the pool sets
+ * KVRING_PAGES_ERR_TABLE and does not go back; the other pages do.  Drops a plan that awaits its commit, and empties the step. */
 kvring_status kvring_pages_release(kvring_pages_t* pages, const int32_t* rows, int32_t num_requests, void* stream);
 
 /* Keys, values and queries of the planned tokens, for one layer:

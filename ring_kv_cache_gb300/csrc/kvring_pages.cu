@@ -224,41 +224,60 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_commit(const PagesDev p)
   }
 }
 
+// Ends requests.  A page id that the pool does not have is reported and not put
+// back: on the stack it would go to the next request.
 __global__ void __launch_bounds__(kPlanThreads) k_pages_release(const PagesDev p, const int32_t* rows, int B) {
   extern __shared__ int32_t sm_plan[];
   __shared__ unsigned long long ws[33];
   __shared__ unsigned s_err;
   int32_t* s_row = sm_plan;
-  int32_t* s_off = s_row + B;   // [B + 1]
-  unsigned* s_seen = reinterpret_cast<unsigned*>(s_off + B + 1);
+  int32_t* s_n = s_row + B;     // [B] pages of each row
+  int32_t* s_off = s_n + B;     // [B] those that go back, then the sums before
+  unsigned* s_seen = reinterpret_cast<unsigned*>(s_off + B);
   for (int i = threadIdx.x; i < (p.R + 31) / 32; i += kPlanThreads) s_seen[i] = 0u;
   if (threadIdx.x == 0) s_err = 0u;
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
+  for (int i = threadIdx.x; i < B; i += kPlanThreads) {
+    const int row = __ldcg(rows + i);
+    int n = 0;
+    if (row < 0 || row >= p.R || (atomicOr(s_seen + (row >> 5), 1u << (row & 31)) & (1u << (row & 31)))) {
+      atomicOr(&s_err, KVRING_PAGES_ERR_ROW);
+    } else {
+      const int len = __ldcg(p.lens + row);
+      if (len < 0 || (long long)len > (long long)p.W * p.P) atomicOr(&s_err, KVRING_PAGES_ERR_LENGTH);
+      else n = (len + p.P - 1) >> p.logP;
+    }
+    s_row[i] = row;
+    s_n[i] = n;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  auto page_ok = [&](int id) { return id >= 0 && id < p.num_pages; };
+  // one warp per request, a lane per table entry
+  unsigned foreign = 0;
+  for (int b = threadIdx.x >> 5; b < B; b += kPlanThreads / 32) {
+    const int n = s_n[b];
+    int back = 0;
+    for (int w = lane; w - lane < n; w += 32) {
+      const bool ok = w < n && page_ok(__ldcg(p.tables + (size_t)s_row[b] * p.W + w));
+      if (w < n && !ok) foreign = KVRING_PAGES_ERR_TABLE;
+      back += __popc(__ballot_sync(0xFFFFFFFFu, ok));
+    }
+    if (lane == 0) s_off[b] = back;
+  }
+  __syncthreads();
   unsigned long long carry = 0;
   for (int base = 0; base < B; base += kPlanThreads) {
     const int i = base + threadIdx.x;
-    unsigned long long v = 0;
-    if (i < B) {
-      const int row = __ldcg(rows + i);
-      if (row < 0 || row >= p.R || (atomicOr(s_seen + (row >> 5), 1u << (row & 31)) & (1u << (row & 31)))) {
-        atomicOr(&s_err, KVRING_PAGES_ERR_ROW);
-      } else {
-        const int len = __ldcg(p.lens + row);
-        if (len < 0 || (long long)len > (long long)p.W * p.P) atomicOr(&s_err, KVRING_PAGES_ERR_LENGTH);
-        else v = (unsigned long long)((len + p.P - 1) >> p.logP);
-      }
-      s_row[i] = row;
-    }
     unsigned long long total;
-    const unsigned long long at = carry + block_scan(v, ws, &total);
+    const unsigned long long at = carry + block_scan(i < B ? (unsigned long long)s_off[i] : 0ull, ws, &total);
     if (i < B) s_off[i] = (int32_t)at;
     carry += total;
   }
   const int nfree = __ldcg(p.state + PST_FREE);
   if (threadIdx.x == 0) {
-    s_off[B] = (int32_t)carry;
     // more pages than the pool holds: the tables are not this cache's
     if (nfree < 0 || (unsigned long long)nfree + carry > (unsigned long long)p.num_pages)
       s_err |= KVRING_PAGES_ERR_PAGES;
@@ -270,17 +289,22 @@ __global__ void __launch_bounds__(kPlanThreads) k_pages_release(const PagesDev p
     p.state[PST_TOKENS] = 0;
     p.state[PST_TAKEN] = 0;
     if (s_err) set_error(p, s_err);
-    else p.state[PST_FREE] = nfree + s_off[B];
+    else p.state[PST_FREE] = nfree + (int)carry;
   }
   if (s_err) return;
-  for (int b = threadIdx.x >> 5; b < B; b += kPlanThreads / 32) {   // one warp per request
-    const int n = s_off[b + 1] - s_off[b];
+  if (foreign) set_error(p, foreign);
+  for (int b = threadIdx.x >> 5; b < B; b += kPlanThreads / 32) {
+    const int n = s_n[b];
     int32_t* row = p.tables + (size_t)s_row[b] * p.W;
-    for (int w = threadIdx.x & 31; w < n; w += 32) {
-      p.free_pages[nfree + s_off[b] + w] = __ldcg(row + w);
-      row[w] = -1;
+    int32_t* to = p.free_pages + nfree + s_off[b];
+    for (int w = lane; w - lane < n; w += 32) {
+      const int id = w < n ? __ldcg(row + w) : -1;
+      const unsigned back = __ballot_sync(0xFFFFFFFFu, page_ok(id));
+      if (page_ok(id)) to[__popc(back & ((1u << lane) - 1))] = id;
+      if (w < n) row[w] = -1;
+      to += __popc(back);
     }
-    if ((threadIdx.x & 31) == 0) p.lens[s_row[b]] = 0;
+    if (lane == 0) p.lens[s_row[b]] = 0;
   }
 }
 

@@ -748,3 +748,30 @@ def test_values_at_the_end_of_bf16(d, total, new, rise):
     want, tol = attention_64(p, s, q=q)
     close(p.attention(0, q).double() * 2.0 ** 100, want * 2.0 ** 100, (tol - 1e-30) * 2.0 ** 100)
     assert errors(p) == 0
+
+
+# ------------------------------------------------------------------ release
+def test_release_puts_back_no_page_that_the_pool_does_not_have():
+    p = pool(16, 100, 4, 1600, 64)
+    ids = torch.full((4, 100), -1, dtype=torch.int32, device="cuda")
+    ids[0, :3] = torch.tensor([5, 99, 100], dtype=torch.int32)
+    ids[1, :70] = torch.arange(20, 90, dtype=torch.int32)
+    ids[1, 33], ids[1, 64], ids[1, 0] = -7, 2 ** 31 - 1, -1
+    ids[2, :1] = 6
+    p.restore(i32([48, 70 * 16 - 3, 1, 0]), ids, i32([1, 2]))
+    p.release(i32([3, 2]))
+    assert errors(p) == 0 and p.free_pages[:3].tolist() == [1, 2, 6]
+    p.release(i32([1, 0]))
+    want = [1, 2, 6] + [i for i in range(20, 90) if i not in (20, 53, 84)] + [5, 99]
+    assert errors(p) == kv.PAGES_ERR_TABLE
+    assert p.lengths.tolist() == [0] * 4 and p.state[kv.PAGES_STATE["free"]].item() == len(want)
+    assert p.free_pages[:len(want)].tolist() == want
+    assert bool((p.tables == -1).all())
+    # an id that a plan took from the free list and that is no page goes out of circulation too
+    p.state[kv.PAGES_STATE["error"]] = 0
+    p.restore(i32([0] * 4), ids.fill_(-1), i32([3, 4, 777]))
+    p.plan(i32([40]), 40)
+    assert errors(p) == kv.PAGES_ERR_TABLE
+    p.commit()
+    p.release(i32([0]))
+    assert p.state[kv.PAGES_STATE["free"]].item() == 2 and sorted(p.free_pages[:2].tolist()) == [3, 4]
