@@ -459,8 +459,8 @@ kvring_status kvring_pages_release(kvring_pages_t* pages, const int32_t* rows, i
  * q, k, v: bf16, row (t, h) at base + t * token_stride + h * d (elements;
  * strides a multiple of 8, at least that of heads * d), so slices of one
  * packed projection output can be passed.  q_out must not overlap them.
- * Tokens past the plan's are not read, and their rows of q_out stay as
- * they were.  num_tokens is that of the tensors (<= max_tokens). */
+ * q, k and v hold num_tokens (<= max_tokens) tokens: rows past the plan's may be
+ * read, whatever they hold has no effect, and those of q_out stay as they were. */
 kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const void* q, const void* k, const void* v,
                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, const void* q_weight,
                                  const void* k_weight, float eps, void* q_out, int32_t num_tokens, void* stream);
