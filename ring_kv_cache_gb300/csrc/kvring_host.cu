@@ -187,11 +187,13 @@ bool make_bf16_map(CUtensorMap* m, const void* base, int rows, int cols, int box
 // so after one of them, only that kernel itself may still be running.  The
 // writes and delta rotations let theirs start at once, so a kernel after
 // them may start while kernels before them still run -- but they write no
-// caller buffer.  The attention reads its queries, and the write its frame,
-// before its wait -- unless a kernel possibly still in flight writes them.
+// caller buffer.  The attention reads its queries and their positions, and the
+// write its frame, before its wait -- unless a kernel possibly still in flight writes them.
 // So a library kernel that stores into caller buffers (attention output, the
 // projection's queries and keys/values, the legacy window, the E4M3 test
-// encoder) replaces its stream's record with those ranges; an attention or a
+// encoder, and every kernel of a paged cache, whose buffer with the step's
+// positions and slots is the caller's to read) replaces its stream's record
+// with those ranges; an attention or a
 // projection with no such output clears it; a write or delta leaves it as it
 // is (it lets older kernels stay in flight and adds nothing to them); and a
 // call whose early inputs overlap the record reads them after the wait.  A
@@ -272,6 +274,11 @@ bool late_inputs(cudaStream_t s, std::initializer_list<Range> in) {
   }
   if (late) ++g_late_reads;
   return late;
+}
+
+// A call's query positions (read as early as its queries).
+Range position_range(const kvring* r, const int32_t* pos, int n) {
+  return Range{pos, pos ? (size_t)n * (r->dev.pt ? 3 : 1) * 4 : 0};
 }
 
 // Under g_out_mu, after a launch on s succeeded: its kernel is now the last
@@ -621,7 +628,7 @@ kvring_status kvring_attention(kvring_t* r, const void* q, const int32_t* qpos, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t rows = (size_t)n_q * r->dev.H * r->dev.D;
   std::lock_guard<std::mutex> lk(g_out_mu);
-  a.q_late = late_inputs(s, {{q, 2 * rows}}) ? 1 : 0;
+  a.q_late = late_inputs(s, {{q, 2 * rows}, position_range(r, qpos, n_q)}) ? 1 : 0;
   return tracked(s, [&] { return kvr::launch_attention(r->dev, &r->tmK, &r->tmV, a, s); },
                  Range{out, rows * (a.out_bf16 ? 2 : 4)}, Range{nullptr, 0}, r);
 }
@@ -670,7 +677,7 @@ kvring_status kvring_attention_noalloc(kvring_t* r, const void* q, const int32_t
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t rows = (size_t)n_q * r->dev.H * r->dev.D;
   std::lock_guard<std::mutex> lk(g_out_mu);
-  a.q_late = late_inputs(s, {{q, 2 * rows}}) ? 1 : 0;
+  a.q_late = late_inputs(s, {{q, 2 * rows}, position_range(r, qpos, n_q)}) ? 1 : 0;
   return tracked(s, [&] { return kvr::launch_attention(d, &r->tmK, &r->tmV, a, s); },
                  Range{out, rows * (a.out_bf16 ? 2 : 4)}, Range{nullptr, 0}, r);
 }

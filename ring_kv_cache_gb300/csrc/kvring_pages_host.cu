@@ -12,6 +12,8 @@ struct kvring_pages {
   kvring_pages_config cfg;
   kvr::PagesDev dev;
   CUtensorMap tmK, tmV;   // [L * num_pages * Hkv][P][d] in boxes of a page, or 128 rows of one
+  const void* buf;        // the caller's, layout.total bytes
+  size_t bytes;
   int sm_count;
   int device;
   int max_new, requests;  // of the last plan: bound on new tokens per request, requests (they pick kernels only)
@@ -125,11 +127,13 @@ bool make_query_map(CUtensorMap* m, const void* q, int64_t stride, int n, const 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch under the library's record of written caller buffers.
+// Launch under the library's record of written caller buffers: the cache's own,
+// from which a caller may pass on what a plan made (a ring's attention reads its
+// query positions before it waits), and the call's output.
 template <typename F>
-kvring_status recorded(cudaStream_t s, F launch, const void* a = nullptr, size_t an = 0) {
+kvring_status recorded(const kvring_pages* h, cudaStream_t s, F launch, const void* a = nullptr, size_t an = 0) {
   return kvr::launch_recorded(
-      s, [](void* ctx) { return (*static_cast<F*>(ctx))(); }, &launch, a, an, nullptr, 0);
+      s, [](void* ctx) { return (*static_cast<F*>(ctx))(); }, &launch, a, an, h->buf, h->bytes);
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -169,6 +173,8 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   if (!h) return KVRING_ERR_INVALID_ARG;
   h->cfg = *cfg;
   h->device = dev;
+  h->buf = dev_buf;
+  h->bytes = p.pub.total;
   h->sm_count = sms < 1 ? 1 : (sms > kvr::kPagedMaxCtas ? kvr::kPagedMaxCtas : sms);
   h->max_new = cfg->max_tokens;
   h->requests = cfg->max_requests;
@@ -221,7 +227,7 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(b + p.pub.scales, 0, p.table - p.pub.scales, s));
   if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(d.tickets, 0, 3 * kvr::kPagedMaxCtas * 4, s));
   if (st == KVRING_OK)
-    st = recorded(s, [&] {
+    st = recorded(h, s, [&] {
       const cudaError_t e = kvr::launch_pages_table(d, reinterpret_cast<float*>(b + p.table), theta, s);
       return e == cudaSuccess ? kvr::launch_pages_reset(d, d.num_pages, true, s) : e;
     });
@@ -247,7 +253,7 @@ kvring_status kvring_pages_restore(kvring_pages_t* h, const int32_t* lengths, co
     return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const kvr::PagesDev& d = h->dev;
-  return recorded(s, [&] {
+  return recorded(h, s, [&] {
     cudaError_t e = cudaMemcpyAsync(d.lens, lengths, (size_t)d.R * 4, cudaMemcpyDeviceToDevice, s);
     if (e == cudaSuccess) e = cudaMemcpyAsync(d.tables, tables, (size_t)d.R * d.W * 4, cudaMemcpyDeviceToDevice, s);
     if (e == cudaSuccess && n_free > 0)
@@ -263,7 +269,7 @@ kvring_status kvring_pages_set_scales(kvring_pages_t* h, int32_t layer, const fl
     return KVRING_ERR_INVALID_ARG;
   if (!h->dev.e4m3) return KVRING_ERR_UNSUPPORTED;   // a bf16 cache has no scales
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return recorded(s, [&] { return kvr::launch_pages_scales(h->dev, layer, sk, sv, s); });
+  return recorded(h, s, [&] { return kvr::launch_pages_scales(h->dev, layer, sk, sv, s); });
 }
 
 kvring_status kvring_pages_plan(kvring_pages_t* h, const int32_t* rows, const int32_t* new_tokens, int32_t n,
@@ -275,7 +281,7 @@ kvring_status kvring_pages_plan(kvring_pages_t* h, const int32_t* rows, const in
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (max_new > num_tokens) max_new = num_tokens;
   const kvring_status st =
-      recorded(s, [&] { return kvr::launch_pages_plan(h->dev, rows, new_tokens, n, num_tokens, max_new, s); });
+      recorded(h, s, [&] { return kvr::launch_pages_plan(h->dev, rows, new_tokens, n, num_tokens, max_new, s); });
   if (st == KVRING_OK) {
     h->max_new = max_new;
     h->requests = n;
@@ -286,14 +292,14 @@ kvring_status kvring_pages_plan(kvring_pages_t* h, const int32_t* rows, const in
 kvring_status kvring_pages_commit(kvring_pages_t* h, void* stream) {
   if (!h || !on_device(h)) return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return recorded(s, [&] { return kvr::launch_pages_commit(h->dev, s); });
+  return recorded(h, s, [&] { return kvr::launch_pages_commit(h->dev, s); });
 }
 
 kvring_status kvring_pages_release(kvring_pages_t* h, const int32_t* rows, int32_t n, void* stream) {
   if (!h || !rows || !aligned(rows, 4) || n < 1 || !on_device(h)) return KVRING_ERR_INVALID_ARG;
   if (n > h->cfg.max_requests) return KVRING_ERR_CAPACITY;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return recorded(s, [&] { return kvr::launch_pages_release(h->dev, rows, n, s); });
+  return recorded(h, s, [&] { return kvr::launch_pages_release(h->dev, rows, n, s); });
 }
 
 kvring_status kvring_pages_write(kvring_pages_t* h, int32_t layer, const void* q, const void* k, const void* v,
@@ -329,7 +335,7 @@ kvring_status kvring_pages_write(kvring_pages_t* h, int32_t layer, const void* q
   w.T = n;
   w.layer = layer;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return recorded(s, [&] { return kvr::launch_pages_write(h->dev, w, h->sm_count, s); }, q_out, out_bytes);
+  return recorded(h, s, [&] { return kvr::launch_pages_write(h->dev, w, h->sm_count, s); }, q_out, out_bytes);
 }
 
 kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const void* q, int64_t q_stride, void* out,
@@ -369,7 +375,7 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   CUtensorMap tmQ;
   if (chunk && !make_query_map(&tmQ, q, q_stride, n, h->cfg)) return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return recorded(s, [&] {
+  return recorded(h, s, [&] {
     cudaError_t e = cudaSuccess;
     if (chunk) {
       a.min_rows = few ? kvr::kFewRows : 0;

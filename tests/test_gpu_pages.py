@@ -775,3 +775,43 @@ def test_release_puts_back_no_page_that_the_pool_does_not_have():
     p.commit()
     p.release(i32([0]))
     assert p.state[kv.PAGES_STATE["free"]].item() == 2 and sorted(p.free_pages[:2].tolist()) == [3, 4]
+
+
+# ------------------------------------------------------- beside the ring
+def test_a_plans_positions_as_a_rings_query_positions():
+    """The ring's attention reads its query positions before it waits, unless
+    a kernel in flight writes them."""
+    H, d, n = 4, 64, 50
+    ring = kv.KvRing(H, d, 300, n, 2000)
+    p = pool(16, 400, 3, 1900, n, cache_dtype=torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = [torch.randn((n, H, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    ring.calibrate(x[1], x[2])
+    for _ in range(6):
+        ring.write(x[1], x[2])
+    starts = [[0, 700, 31], [1500, 2, 900], [64, 64, 1800]]
+    new = [i32([20, 0, 30]), i32([1, 48, 1]), i32([7, 7, 7])]
+    tables = torch.arange(3 * p.W, dtype=torch.int32, device="cuda").view(3, p.W) % 400
+    want = []
+    for lens, k in zip(starts, new):
+        p.restore(i32(lens), tables, i32(list(range(200))))
+        pos = p.plan(k, n).positions.clone()
+        torch.cuda.synchronize()
+        want.append(ring.attention(x[0], qpos=pos))
+    assert errors(p) == 0 and not torch.equal(want[0], want[1])
+    lens = [i32(s) for s in starts]
+    free = i32(list(range(200)))
+    torch.cuda.synchronize()
+    for i in range(60):
+        p.restore(lens[i % 3], tables, free)
+        step = p.plan(new[i % 3], n)
+        before = kv.late_reads()
+        out = ring.attention(x[0], qpos=step.positions)
+        assert kv.late_reads() == before + 1
+        assert torch.equal(out, want[i % 3]), i
+    # a write of the ring in between lets the plan's kernel stay in flight
+    step = p.plan(new[0], n)
+    ring.write(x[1], x[2])
+    before = kv.late_reads()
+    ring.attention(x[0], qpos=step.positions)
+    assert kv.late_reads() == before + 1
