@@ -115,6 +115,18 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
       : "r"(w));
 }
 
+// The power of two that a query row is divided by on its way to f16, and its
+// inverse, from the row's largest exponent field: its largest value then lies in [1, 2) (in [2, 4) for the
+// last exponent, whose factor's inverse would not be a normal number).
+// Infinities and NaN (255) keep a factor of 1 and stay what they are, and so does a
+// row of zeros.
+__device__ __forceinline__ void query_factor(uint32_t em, float& up, float& down) {
+  const bool plain = em == 0 || em == 255;
+  const uint32_t e = min(em, 253u);
+  up = plain ? 1.0f : __uint_as_float(e << 23);
+  down = plain ? 1.0f : __uint_as_float((254u - e) << 23);
+}
+
 // One launch with the programmatic-stream-serialisation attribute.
 template <typename... KP, typename... A>
 inline cudaError_t launch_pdl(void (*kernel)(KP...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {

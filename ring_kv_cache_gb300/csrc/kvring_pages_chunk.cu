@@ -770,11 +770,11 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         }
         if (L::kHalves > 1) sync_group();              // (both halves' threads have read the row)
         if (live) {
-          const bool plain = em == 0 || em >= 254;     // zeros, infinities, NaN: a factor of 1
-          const float down = plain ? 1.0f : __uint_as_float((254u - em) << 23);
+          float up, down;
+          query_factor(em, up, down);
           // (at least 1e-30: a factor that underflows would make NaN of what is
           // masked, and such scores are all alike anyway)
-          f_row = fmaxf(f_row * __ldcg(sc + u.h) * (plain ? 1.0f : __uint_as_float(em << 23)), 1e-30f);
+          f_row = fmaxf(f_row * __ldcg(sc + u.h) * up, 1e-30f);
 #pragma unroll
           for (int i = 0; i < D / 8 / L::kHalves; ++i) {
             uint4* at = chunk_at(half * (D / 8 / L::kHalves) + i);
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         if (!live) f_row = 0.f;
         // (nothing seen yet: 2^-inf = 0)
         float moff = kShift<E4M3>;
-        // (over an E4M3 cache a score is at most 2 x 448 x 128 < 2^17, so the
+        // (over an E4M3 cache a score is at most 4 x 448 x 128 < 2^18, so the
         // factor tells)
         bool huge = E4M3 && __any_sync(0xFFFFFFFFu, f_row > 8.0f);
         // 32 scores to probabilities, as pairs of the 16-bit type; their sum

@@ -425,13 +425,11 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         for (int e = 0; e < 4; ++e) em = max(em, max((u[e] >> 7) & 0xFFu, (u[e] >> 23) & 0xFFu));
 #pragma unroll
         for (int o = kChunksQ / 2; o > 0; o >>= 1) em = max(em, __shfl_xor_sync(0xFFFFFFFFu, em, o));
-        // 2^(127 - em) and its inverse; infinities and NaN keep a factor of 1
-        // (and stay what they are), and so does a row of zeros
-        const bool plain = em == 0 || em >= 254;
-        const float down = plain ? 1.0f : __uint_as_float((254u - em) << 23);
+        float up, down;
+        query_factor(em, up, down);
         // (at least 1e-30: a factor that underflows would make NaN of what is
         // masked, and such scores are all alike anyway)
-        fac = fmaxf(fac * scale_k * (plain ? 1.0f : __uint_as_float(em << 23)), 1e-30f);
+        fac = fmaxf(fac * scale_k * up, 1e-30f);
         uint32_t hq[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)

@@ -750,6 +750,23 @@ def test_values_at_the_end_of_bf16(d, total, new, rise):
     assert errors(p) == 0
 
 
+@pytest.mark.parametrize("new", [1, 3, 50])
+@pytest.mark.parametrize("d", [64, 128])
+def test_queries_of_the_last_exponent_over_e4m3(d, new):
+    """Finite bf16 queries from 2^127 on, under scales that leave moderate scores."""
+    p, s = filled(4, 2, d, 32, [300], [new], "e4m3", seed=16)
+    p.k_cache(0).copy_((p.k_cache(0).float() * 0.01).to(torch.float8_e4m3fn))
+    s["sk"].fill_(2.0 ** -126)
+    p.set_scales(0, s["sk"], s["sv"])
+    q = s["q"].float()
+    q = ((1.0 + 0.9 * (q - q.floor())) * 2.0 ** 126 * 2.0 * torch.where(q > 0, 1.0, -1.0)).to(torch.bfloat16)
+    q[0, 0] = s["q"][0, 0]        # a row of common size among them
+    assert bool(torch.isfinite(q).all())
+    want, tol = attention_64(p, s, q=q)
+    close(p.attention(0, q), want, tol)
+    assert errors(p) == 0
+
+
 # ------------------------------------------------------------------ release
 def test_release_puts_back_no_page_that_the_pool_does_not_have():
     p = pool(16, 100, 4, 1600, 64)
