@@ -455,7 +455,9 @@ kvring_status kvring_pages_release(kvring_pages_t* pages, const int32_t* rows, i
  *   q_out[t] = rope(y_q, positions[t]), bf16 [num_tokens][Hq][d] contiguous
  *   K page   = rope(y_k, positions[t]), V page = v
  * at slots[t].  An E4M3 cache stores e4m3(value * (1/scale)).  Everything
- * between reading bf16 and the one rounding of the result is fp32.
+ * between reading bf16 and the one rounding of the result is fp32, the squares
+ * too: a normed row whose mean square leaves fp32's range (values of 2^63 and
+ * more) comes out as zeros, and with eps 0 one of 2^-60 and less has no meaning.
  * q, k, v: bf16, row (t, h) at base + t * token_stride + h * d (elements;
  * strides a multiple of 8, at least that of heads * d), so slices of one
  * packed projection output can be passed.  q_out must not overlap them.
