@@ -510,18 +510,18 @@ class KvRing:
 # ---------------------------------------------------------------------------
 # The paged cache
 # ---------------------------------------------------------------------------
-def make_pages_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_requests, max_pages_per_request,
-                      max_tokens, layers=1, cache_dtype=CACHE_E4M3, rope_pairing=ROPE_ADJACENT,
-                      rope_base=10000.0) -> KvringPagesConfig:
-    return KvringPagesConfig(int(q_heads), int(kv_heads), int(head_dim), int(layers), int(page_size), int(num_pages),
-                             int(max_requests), int(max_pages_per_request), int(max_tokens), int(cache_dtype),
-                             int(rope_pairing), 0, float(rope_base))
-
-
 def _i32(x) -> int:
     """An int argument, kept in range where ctypes would wrap it."""
     x = int(x)
     return x if -(1 << 31) <= x < 1 << 31 else (-1 if x < 0 else (1 << 31) - 1)
+
+
+def make_pages_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_requests, max_pages_per_request,
+                      max_tokens, layers=1, cache_dtype=CACHE_E4M3, rope_pairing=ROPE_ADJACENT,
+                      rope_base=10000.0) -> KvringPagesConfig:
+    return KvringPagesConfig(*map(_i32, (q_heads, kv_heads, head_dim, layers, page_size, num_pages, max_requests,
+                                         max_pages_per_request, max_tokens, cache_dtype, rope_pairing, 0)),
+                             float(rope_base))
 
 
 def _empty_on(stream, shape, dtype, device) -> torch.Tensor:

@@ -52,3 +52,15 @@ def test_null_arguments_are_refused_without_a_gpu():
     assert L.kvring_pages_attention(None, 0, None, 0, None, 1, 1, 0, 0.0, None) == 1
     assert L.kvring_pages_debug_set_wait(None, 1000, 0) == 1
     assert L.kvring_pages_destroy(None) == 0
+
+
+@pytest.mark.parametrize("at", range(9))
+def test_config_integers_do_not_wrap(at):
+    args = [32, 8, 128, 64, 1000, 16, 20, 512, 3]
+    good = kv.kvring_pages_get_layout(kv.make_pages_config(*args))
+    assert good.total > 0
+    for by in (2 ** 32, -2 ** 32, 2 ** 33):
+        bad = list(args)
+        bad[at] += by
+        with pytest.raises(kv.KvRingError):
+            kv.kvring_pages_get_layout(kv.make_pages_config(*bad))
