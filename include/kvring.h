@@ -408,7 +408,8 @@ kvring_status kvring_pages_destroy(kvring_pages_t* pages);
 
 /* Take over a state: lengths int32 [max_requests], tables int32
  * [max_requests][W], free_pages int32 [n_free] (the stack, bottom first).
- * Device pointers.  Drops a plan that awaits its commit. */
+ * Device pointers, each either outside the cache's buffer or its own array,
+ * which then stays as it is.  Drops a plan that awaits its commit. */
 kvring_status kvring_pages_restore(kvring_pages_t* pages, const int32_t* lengths, const int32_t* tables,
                                    const int32_t* free_pages, int32_t n_free, void* stream);
 
@@ -419,7 +420,8 @@ kvring_status kvring_pages_set_scales(kvring_pages_t* pages, int32_t layer, cons
 
 /* Plan a step: request i (of num_requests) is row rows[i] of the tables
  * (rows NULL: row i) and gets new_tokens[i] >= 0 new tokens, positions
- * len .. len + new - 1.  Both are device int32 arrays.  On the device:
+ * len .. len + new - 1.  Both are device int32 arrays, outside the step's own.
+ * On the device:
  *   step_cu       exclusive sums of new_tokens (num_requests + 1 entries)
  *   step_lengths  length + new
  *   tables        entries of the pages the new tokens need beyond those the
@@ -460,7 +462,8 @@ kvring_status kvring_pages_release(kvring_pages_t* pages, const int32_t* rows, i
  * more) comes out as zeros, and with eps 0 one of 2^-60 and less has no meaning.
  * q, k, v: bf16, row (t, h) at base + t * token_stride + h * d (elements;
  * strides a multiple of 8, at least that of heads * d), so slices of one
- * packed projection output can be passed.  q_out must not overlap them.
+ * packed projection output can be passed.  q_out must not overlap them, the
+ * weights or the cache's buffer.
  * q, k and v hold num_tokens (<= max_tokens) tokens: rows past the plan's may be
  * read, whatever they hold has no effect, and those of q_out stay as they were. */
 kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const void* q, const void* k, const void* v,
@@ -474,7 +477,7 @@ kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const voi
  * j > position - window; causal == 0: every cached and new token of the
  * request (window must be 0).  scale 0 means 1/sqrt(d).  q (rotated) and
  * out: bf16 [num_tokens][Hq][d], q with a token stride (elements, a multiple
- * of 8), out contiguous and not overlapping q; rows past the plan's tokens stay as
+ * of 8), out contiguous, overlapping neither q nor the cache's buffer; rows past the plan's tokens stay as
  * they were.  Scores, softmax statistics and sums are fp32; probabilities
  * are rounded once, to bf16 (f16 over an E4M3 cache).  Finite cached values
  * of any size give finite results at any length.  Cached tokens that

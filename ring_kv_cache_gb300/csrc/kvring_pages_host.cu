@@ -253,11 +253,23 @@ kvring_status kvring_pages_restore(kvring_pages_t* h, const int32_t* lengths, co
     return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const kvr::PagesDev& d = h->dev;
+  // the cache's own arrays stay where they are; other parts of its buffer would
+  // be copied over one another
+  struct Copy {
+    int32_t* to;
+    const int32_t* from;
+    size_t bytes;
+  } copies[3] = {{d.lens, lengths, (size_t)d.R * 4},
+                 {d.tables, tables, (size_t)d.R * d.W * 4},
+                 {d.free_pages, free_pages, (size_t)n_free * 4}};
+  for (Copy& c : copies) {
+    if (c.from == c.to) c.bytes = 0;
+    if (c.bytes && overlap(c.from, c.bytes, h->buf, h->bytes)) return KVRING_ERR_INVALID_ARG;
+  }
   return recorded(h, s, [&] {
-    cudaError_t e = cudaMemcpyAsync(d.lens, lengths, (size_t)d.R * 4, cudaMemcpyDeviceToDevice, s);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(d.tables, tables, (size_t)d.R * d.W * 4, cudaMemcpyDeviceToDevice, s);
-    if (e == cudaSuccess && n_free > 0)
-      e = cudaMemcpyAsync(d.free_pages, free_pages, (size_t)n_free * 4, cudaMemcpyDeviceToDevice, s);
+    cudaError_t e = cudaSuccess;
+    for (const Copy& c : copies)
+      if (e == cudaSuccess && c.bytes) e = cudaMemcpyAsync(c.to, c.from, c.bytes, cudaMemcpyDeviceToDevice, s);
     return e == cudaSuccess ? kvr::launch_pages_reset(d, n_free, false, s) : e;
   });
 }
@@ -278,6 +290,11 @@ kvring_status kvring_pages_plan(kvring_pages_t* h, const int32_t* rows, const in
       max_new < 1 || !on_device(h))
     return KVRING_ERR_INVALID_ARG;
   if (n > h->cfg.max_requests || num_tokens > h->cfg.max_tokens) return KVRING_ERR_CAPACITY;
+  // what the plan writes while it reads them
+  const uint8_t* steps = reinterpret_cast<const uint8_t*>(h->dev.rows);
+  const size_t step_bytes = static_cast<const uint8_t*>(h->buf) + h->bytes - steps;
+  if (overlap(new_tokens, (size_t)n * 4, steps, step_bytes) || (rows && overlap(rows, (size_t)n * 4, steps, step_bytes)))
+    return KVRING_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (max_new > num_tokens) max_new = num_tokens;
   const kvring_status st =
@@ -319,8 +336,10 @@ kvring_status kvring_pages_write(kvring_pages_t* h, int32_t layer, const void* q
   const size_t out_bytes = (size_t)n * qrow * 2;
   auto bytes = [&](int64_t stride, int64_t row) { return ((size_t)(n - 1) * stride + row) * 2; };
   if (overlap(q_out, out_bytes, q, bytes(qs, qrow)) || overlap(q_out, out_bytes, k, bytes(ks, krow)) ||
-      overlap(q_out, out_bytes, v, bytes(vs, krow)))
+      overlap(q_out, out_bytes, v, bytes(vs, krow)) || overlap(q_out, out_bytes, h->buf, h->bytes))
     return KVRING_ERR_INVALID_ARG;
+  for (const void* p : {qw, kw})
+    if (p && overlap(q_out, out_bytes, p, (size_t)D * 2)) return KVRING_ERR_INVALID_ARG;
   kvr::PagesWrite w{};
   w.q = static_cast<const uint16_t*>(q);
   w.k = static_cast<const uint16_t*>(k);
@@ -349,7 +368,8 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   if (!(scale >= 0.f) || !std::isfinite(scale)) return KVRING_ERR_INVALID_ARG;
   if (n > h->cfg.max_tokens) return KVRING_ERR_CAPACITY;
   const size_t out_bytes = (size_t)n * row * 2;
-  if (overlap(out, out_bytes, q, ((size_t)(n - 1) * q_stride + row) * 2)) return KVRING_ERR_INVALID_ARG;
+  if (overlap(out, out_bytes, q, ((size_t)(n - 1) * q_stride + row) * 2) || overlap(out, out_bytes, h->buf, h->bytes))
+    return KVRING_ERR_INVALID_ARG;
   kvr::PagedAttn a{};
   a.q = static_cast<const uint16_t*>(q);
   a.out = static_cast<uint16_t*>(out);

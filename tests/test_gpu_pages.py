@@ -832,3 +832,37 @@ def test_a_plans_positions_as_a_rings_query_positions():
     before = kv.late_reads()
     ring.attention(x[0], qpos=step.positions)
     assert kv.late_reads() == before + 1
+
+
+def test_arguments_in_the_caches_own_buffer():
+    p, s = filled(4, 1, 64, 16, [20, 40], [4, 4], "bf16", seed=1)
+    p.commit()
+    q = s["q"]
+    k = torch.zeros((8, 1, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    state = [t.clone() for t in (p.lengths, p.tables, p.free_pages)]
+    n = p.state[kv.PAGES_STATE["free"]].item()
+    p.restore(p.lengths, p.tables, p.free_pages[:n])     # as they are
+    step = p.plan(i32([1, 1]), 8)
+    assert step.lengths.tolist() == [21, 41] and errors(p) == 0
+    p.restore(state[0], state[1], p.free_pages[:n])
+    assert all(torch.equal(a, b) for a, b in zip(state, (p.lengths, p.tables, p.free_pages)))
+    other = torch.zeros_like(p.tables)
+    with pytest.raises(kv.KvRingError):
+        p.restore(p.lengths, p.tables, p.free_pages[1:n])
+    with pytest.raises(kv.KvRingError):
+        p.restore(p._klen, other, i32([0]))
+    with pytest.raises(kv.KvRingError):
+        p.plan(p._klen, 8)
+    with pytest.raises(kv.KvRingError):
+        p.plan(i32([1, 1]), 8, rows=p._slots[:2])
+    own = p.k_cache(0).view(-1)[:8 * 4 * 64].view(8, 4, 64)
+    with pytest.raises(kv.KvRingError):
+        p.attention(0, q, out=own)
+    with pytest.raises(kv.KvRingError):
+        p.write(0, q, k, k, q_out=own)
+    out = torch.zeros(8 * 4 * 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(kv.KvRingError):
+        p.write(0, q, k, k, k_norm=out[64:128], q_out=out.view(8, 4, 64))
+    p.write(0, q, k, k, k_norm=w, q_out=out.view(8, 4, 64))
+    assert errors(p) == 0 and all(torch.equal(a, b) for a, b in zip(state[:1], (p.lengths,)))
