@@ -378,6 +378,14 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
       phase ^= 1u;
     }
   };
+  // The slot back to the producer: behind this warp's reads of it, with the fence
+  // between them and the next copy, which is of the other proxy.
+  auto give_back = [&]() {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty(s));
+    next_slot();
+  };
   const int g = lane >> 2, c = lane & 3;
   float* s_o = reinterpret_cast<float*>(fix + L::kO);
   float2* s_ml = reinterpret_cast<float2*>(fix + L::kMl);
@@ -488,13 +496,9 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         // another's tile: waited for and given back like an own one, so that
         // no slot is filled again before every warp has seen it full (its
         // barrier then never is two phases ahead of a waiting warp)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(s));
-        next_slot();
+        give_back();
         wait_full();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty(s));
-        next_slot();
+        give_back();
         continue;
       }
       float sc_[2][4];
@@ -530,9 +534,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
-      next_slot();
+      give_back();
       // ---- probabilities, in the layout of the next product's operand
       const bool masked = tok0 < all_lo || tok0 + 16 > all_hi;
       uint32_t pa[4];
@@ -667,9 +669,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
-      next_slot();
+      give_back();
     }
 
     // ---- end of the unit, or of this CTA's part of it: merge the warps
