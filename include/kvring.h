@@ -477,8 +477,8 @@ kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const voi
  * j > position - window; causal == 0: every cached and new token of the
  * request (window must be 0).  scale 0 means 1/sqrt(d).  q (rotated) and
  * out: bf16 [num_tokens][Hq][d], q with a token stride (elements, a multiple
- * of 8), out contiguous, overlapping neither q nor the cache's buffer; rows past the plan's tokens stay as
- * they were.  Scores, softmax statistics and sums are fp32; probabilities
+ * of 8), out contiguous, overlapping neither q nor the cache's buffer; rows
+ * past the plan's tokens stay as they were.  Scores, softmax statistics and sums are fp32; probabilities
  * are rounded once, to bf16 (f16 over an E4M3 cache).  Finite cached values
  * of any size give finite results at any length.  Cached tokens that
  * a query's mask hides do not affect it, whatever they hold. */

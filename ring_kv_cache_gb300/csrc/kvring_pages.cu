@@ -60,7 +60,7 @@ __device__ __forceinline__ int last_at_most(const int32_t* a, int n, int x) {
 // words at most, in one pass with one block scan of tokens and pages packed
 // in 64 bits), so no block waits for another and the plan is one launch; a
 // block then writes its share of the token maps and of the table entries.
-// Bound by latency: 4.3 us for 48 requests and as many tokens, 6.4 us for 1,000
+// Bound by latency: 4.5 us for 48 requests and as many tokens, 6.7 us for 1,000
 // requests with 65,536 tokens (0.6 MB).
 // Tokens take 34 bits (4,096 requests x 2^20 tokens), pages 30.
 constexpr int kTokBits = 34;

@@ -55,8 +55,9 @@
 // drawn are cleared by the next plan.
 //
 // Measured (GB300): 4,096 queries behind 12,288 cached tokens, causal, 32/8
-// heads x 128, bf16: 600 to 620 us, 1,550 to 1,600 TFLOP/s (82 to 85 % of the
-// library product's 1,884, 92 to 95 % of what that keeps up for seconds); 757
+// heads x 128, bf16: 605 to 622 us in a graph, 629 us a call among others, 1,530
+// to 1,590 TFLOP/s (81 to 84 % of the library product's 1,884, 90 to 94 % of what
+// that keeps up for seconds); 757
 // queries over 5,788 E4M3 tokens, 40 heads, all seen: 84 us (1,070 TFLOP/s; 120
 // units on 152 SMs, so nearly all are split); 11 chunks of up to 900 tokens,
 // window 1,500, 20/4 heads x 64: 80 to 87 us.  At d = 128 a tile takes what a

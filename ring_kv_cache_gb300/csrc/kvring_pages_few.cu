@@ -42,9 +42,9 @@
 // what the row's small values lose is below 2^-25 of its largest.
 //
 // Measured (GB300): 128 decoding requests of 7,000 tokens on average, 32/8
-// heads x 128, bf16, 3.67 GB: 541 us, 6.79 TB/s (the copy rate is 6.80); the
-// same in E4M3 321 us, 5.7 TB/s, bound by the instructions that widen and
-// multiply; six requests of up to 32,000 tokens in pages of 16, 10 heads, E4M3,
+// heads x 128, bf16, 3.67 GB: 544 us, 6.75 TB/s (the copy rate is 6.80); the
+// same in E4M3 321 us, 5.7 TB/s, bound by the latency of each warp's chain of
+// widening and products; six requests of up to 32,000 tokens in pages of 16, 10 heads, E4M3,
 // four tokens each, 310 MB: 65 us (61 us in pages of 64); one request of 700
 // tokens: 10 us, latency.
 #include "kvring_pages.cuh"
