@@ -169,7 +169,8 @@ def _norm_case(case, g):
     h[:, :: max(1, d // 5)] *= 12.0
     s = dict(h=h.to(_type(case["stream"])), y=rand(n, d).to(torch.bfloat16))
     s["mod"] = (0.4 * rand(m, 3, d)).to(_type(case["mods"]))   # gate, scale, shift, side by side as a projection makes them
-    s["rows"] = torch.randint(0, m, (n,), generator=g, device=DEV).to(torch.int32) if m > 1 else None
+    # (a session's tokens lie together)
+    s["rows"] = torch.randint(0, m, (n,), generator=g, device=DEV).sort()[0].to(torch.int32) if m > 1 else None
     s["post_w"] = (0.5 + torch.rand(d, generator=g, device=DEV)).to(torch.bfloat16) if case["post"] != "none" else None
     s["h_out"] = torch.zeros_like(s["h"])
     s["x_out"] = torch.zeros((n, d), dtype=torch.bfloat16, device=DEV)
