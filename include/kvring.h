@@ -216,6 +216,52 @@ kvring_status kvring_project_write(kvring_t* ring, const void* x, const void* w,
                                    const int32_t* pos, int32_t n, void* q_out, void* kv_out,
                                    int32_t flags, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Between two blocks: a block's output joins the residual stream, and the
+ * stream's norm, modulated, is the next block's input (kvring_project_write's
+ * x, for instance).  For every token t, with r its row of the modulation tables:
+ *   u        = y[t], or norm(y[t]) * post_weight
+ *   h_out[t] = h[t] + residual_scale * gate[r] * u
+ *   x_out[t] = norm(h_out[t]) * weight * (1 + scale[r]) + shift[r]
+ *   KVRING_NORM_RMS    z / sqrt(mean(z^2) + eps)
+ *   KVRING_NORM_LAYER  (z - mean(z)) / sqrt(var(z) + eps), var over all `width` values
+ * h, h_out: [num_tokens][width] fp32 or bf16 (stream_dtype); y, x_out: bf16;
+ * gate, scale, shift: [mod_rows][width], fp32 or bf16 (mod_dtype), each NULL
+ * for none (1, 0, 0); weight, post_weight: bf16 [width] or NULL (ones).
+ * mod_index: int32 [num_tokens] rows, or NULL: row 0 of one, or row t of
+ * num_tokens; a token whose row is outside [0, mod_rows) gets NaN.
+ * Rows lie stride elements apart (multiples of 8, at least width where there is
+ * more than one row), so slices of packed tensors can be passed.
+ * y NULL: h is normed as it is (h_out, gate, post_weight NULL, post_norm none).
+ * x_out NULL and norm KVRING_NORM_NONE: the sum alone.  h_out may be NULL when x_out
+ * is not.  h_out may be h (with its stride); no other result may lie over an
+ * argument or the other result.  Everything between reading and the one rounding
+ * of each result is fp32, squares included; x_out comes from the unrounded sum.
+ * Works on the current device, and keeps no state.
+ * ------------------------------------------------------------------------ */
+#define KVRING_NORM_NONE 0
+#define KVRING_NORM_RMS 1
+#define KVRING_NORM_LAYER 2
+#define KVRING_NORM_MAX_WIDTH 16384
+
+typedef struct {
+  int32_t num_tokens;     /* n >= 1 */
+  int32_t width;          /* a multiple of 8, 8 .. KVRING_NORM_MAX_WIDTH */
+  int32_t stream_dtype;   /* KVRING_OUT_F32 or KVRING_OUT_BF16 */
+  int32_t mod_dtype;      /* the same, of gate, scale and shift */
+  int32_t mod_rows;       /* rows of gate, scale and shift (ignored without them) */
+  int32_t post_norm;      /* KVRING_NORM_*: of y */
+  int32_t norm;           /* KVRING_NORM_*: of the stream */
+  int32_t reserved;       /* 0 */
+  int64_t h_stride, y_stride, mod_stride, h_out_stride, x_out_stride;
+  float eps, residual_scale;
+} kvring_norm_config;
+
+kvring_status kvring_residual_norm(const kvring_norm_config* cfg, const void* h, const void* y, const void* gate,
+                                   const void* scale, const void* shift, const int32_t* mod_index,
+                                   const void* post_weight, const void* weight, void* h_out, void* x_out,
+                                   void* stream);
+
 /* The cache upkeep the ring replaced, kept as the comparison path ("Where
  * the Time Went": before the ring, every attention call re-applied RoPE to
  * every cached key, re-quantised the cache to FP8 and shifted the window by

@@ -24,7 +24,7 @@ __all__ = [
     "kvring_required_bytes", "kvring_create", "kvring_destroy", "kvring_calibrate_scales",
     "kvring_write_frame", "kvring_delta_rotate", "kvring_attention", "kvring_attention_noalloc",
     "kvring_write_frames_many", "kvring_delta_rotate_many", "write_frames_many", "delta_rotate_many",
-    "kvring_legacy_upkeep", "LegacyWindows", "kvring_project_write",
+    "kvring_legacy_upkeep", "LegacyWindows", "kvring_project_write", "kvring_residual_norm", "residual_norm",
     "kvring_export",
     "kvring_status_string", "encode_e4m3", "STATE",
     "KvPages", "KvStep", "PAGES_STATE", "kvring_pages_get_layout", "kvring_pages_create", "kvring_pages_destroy",
@@ -65,6 +65,16 @@ PAGES_STATE = dict(free=0, error=1, planned=2, requests=3, tokens=4, taken=5)
 PAGES_STATE_WORDS = 8
 PAGES_ERR_ROW, PAGES_ERR_TOKENS, PAGES_ERR_LENGTH, PAGES_ERR_PAGES = 1, 2, 4, 8
 PAGES_ERR_COMMIT, PAGES_ERR_TABLE, PAGES_ERR_TIMEOUT = 16, 32, 64
+
+
+NORMS = {None: 0, "rms": 1, "layer": 2}
+
+
+class KvringNormConfig(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in (
+        "num_tokens", "width", "stream_dtype", "mod_dtype", "mod_rows", "post_norm", "norm", "reserved")] + [
+        (f, ctypes.c_int64) for f in ("h_stride", "y_stride", "mod_stride", "h_out_stride", "x_out_stride")] + [
+        ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)]
 
 
 class KvringPagesConfig(ctypes.Structure):
@@ -117,6 +127,7 @@ def lib():
         "kvring_attention": (i32, [vp, vp, vp, i32, vp, i32, vp]),
         "kvring_attention_noalloc": (i32, [vp, vp, vp, i32, vp, i32, vp]),
         "kvring_project_write": (i32, [vp, vp, vp, i32, vp, i32, vp, vp, i32, vp]),
+        "kvring_residual_norm": (i32, [ctypes.POINTER(KvringNormConfig)] + [vp] * 11),
         "kvring_export": (i32, [vp, vp, vp, vp, vp, vp, vp]),
         "kvring_pages_get_layout": (i32, [ctypes.POINTER(KvringPagesConfig), ctypes.POINTER(KvringPagesLayout)]),
         "kvring_pages_create": (i32, [ctypes.POINTER(KvringPagesConfig), vp, sz, vp, ctypes.POINTER(vp)]),
@@ -332,6 +343,95 @@ def kvring_attention_noalloc(handle, q, qpos, n_q, out, out_dtype, stream_ptr) -
 def kvring_project_write(handle, x, w, d_model, pos, n, q_out, kv_out, flags, stream_ptr) -> None:
     _check(lib().kvring_project_write(handle, _ptr(x), _ptr(w), int(d_model), _ptr(pos), int(n), _ptr(q_out),
                                       _ptr(kv_out), int(flags), stream_ptr), "kvring_project_write")
+
+
+def kvring_residual_norm(cfg: KvringNormConfig, h, y, gate, scale, shift, mod_index, post_weight, weight, h_out, x_out,
+                         stream_ptr) -> None:
+    _check(lib().kvring_residual_norm(ctypes.byref(cfg), _ptr(h), _ptr(y), _ptr(gate), _ptr(scale), _ptr(shift),
+                                      _ptr(mod_index), _ptr(post_weight), _ptr(weight), _ptr(h_out), _ptr(x_out),
+                                      stream_ptr), "kvring_residual_norm")
+
+
+def _rows(x, dtypes, shape, name: str, device) -> int:
+    """Check a 2-D tensor of whole rows (a slice of a packed tensor is one); returns its row stride."""
+    if not isinstance(x, torch.Tensor) or x.device != device or x.dtype not in dtypes:
+        raise ValueError(f"{name} must be a {' or '.join(str(d)[6:] for d in dtypes)} tensor on {device}")
+    if x.dim() != 2 or (shape[0] is not None and x.shape[0] != shape[0]) or x.shape[1] != shape[1]:
+        raise ValueError(f"{name} must have shape {[s if s is not None else 'rows' for s in shape]}, got {tuple(x.shape)}")
+    st, s1 = x.stride()
+    n = x.shape[0]
+    if s1 != 1 or (n > 1 and (st < shape[1] or st % 8)):
+        raise ValueError(f"{name}: rows must be contiguous, a multiple of 8 elements apart and must not overlap")
+    return st if n > 1 else shape[1]
+
+
+def residual_norm(h, y=None, gate=None, residual_scale: float = 1.0, post_norm: str | None = None, post_weight=None,
+                  norm: str | None = "rms", weight=None, scale=None, shift=None, mod_rows=None, eps: float = 1e-6,
+                  h_out=None, x_out=None, stream=None):
+    """The step between two blocks (kvring_residual_norm): a block's output y
+    (bf16 [n, width]; normed by ``post_norm`` where given) joins the residual
+    stream h (float32 or bf16), and the stream's ``norm``, modulated, is the next
+    block's input:
+
+        h_out = h + residual_scale * gate * (post_norm(y) * post_weight)
+        x     = norm(h_out) * weight * (1 + scale) + shift
+
+    ``gate``, ``scale`` and ``shift`` are [rows, width], all float32 or all
+    bfloat16 (slices of one packed tensor are fine); token t takes row
+    ``mod_rows[t]`` (int32), else row 0 of one or row t of n.  Norms are "rms",
+    "layer" or None.  Returns (h_out, x): h_out is h itself without y, x is None
+    without ``norm``; ``h_out=h`` updates the stream in place."""
+    if not isinstance(h, torch.Tensor) or not h.is_cuda or h.dim() != 2:
+        raise ValueError("h must be a 2-D CUDA tensor")
+    dev, (n, width) = h.device, h.shape
+    if width < 8 or width % 8 or width > 16384:
+        raise ValueError("width must be a multiple of 8, at most 16384")
+    if norm not in NORMS or post_norm not in NORMS:
+        raise ValueError("norms are 'rms', 'layer' or None")
+    bf, f32 = (torch.bfloat16,), (torch.float32, torch.bfloat16)
+    hs = _rows(h, f32, (n, width), "h", dev)
+    ys = _rows(y, bf, (n, width), "y", dev) if y is not None else 0
+    if y is None and (gate is not None or post_norm or post_weight is not None or h_out is not None):
+        raise ValueError("gate, post_norm, post_weight and h_out need y")
+    if norm is None and (weight is not None or scale is not None or shift is not None or x_out is not None):
+        raise ValueError("weight, scale, shift and x_out need a norm")
+    if y is None and norm is None:
+        raise ValueError("nothing to compute")
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight needs a post_norm")
+    m, ms, mod = 0, 0, None
+    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if t is None:
+            continue
+        st = _rows(t, f32, (None, width) if mod is None else (m, width), name, dev)
+        if mod is not None and (t.dtype != mod or st != ms):
+            raise ValueError("gate, scale and shift must have one type and one row stride")
+        m, ms, mod = t.shape[0], st, t.dtype
+    if mod_rows is not None:
+        if mod is None:
+            raise ValueError("mod_rows needs gate, scale or shift")
+        if not isinstance(mod_rows, torch.Tensor) or mod_rows.device != dev or mod_rows.dtype != torch.int32 \
+                or tuple(mod_rows.shape) != (n,) or not mod_rows.is_contiguous():
+            raise ValueError(f"mod_rows must be a contiguous int32 tensor [{n}] on {dev}")
+    elif mod is not None and m not in (1, n):
+        raise ValueError(f"gate, scale and shift have {m} rows: mod_rows says which is whose")
+    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.device != dev
+                              or t.shape != (width,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{width}] on {dev}")
+    if y is not None and h_out is None:
+        h_out = _empty_on(stream, (n, width), h.dtype, dev)
+    if norm is not None and x_out is None:
+        x_out = _empty_on(stream, (n, width), torch.bfloat16, dev)
+    os_ = _rows(h_out, (h.dtype,), (n, width), "h_out", dev) if h_out is not None else 0
+    xs = _rows(x_out, bf, (n, width), "x_out", dev) if x_out is not None else 0
+    cfg = KvringNormConfig(n, width, OUT_F32 if h.dtype == torch.float32 else OUT_BF16,
+                           OUT_BF16 if mod == torch.bfloat16 else OUT_F32, m, NORMS[post_norm], NORMS[norm], 0,
+                           hs, ys, ms, os_, xs, float(eps), float(residual_scale))
+    with torch.cuda.device(dev):
+        kvring_residual_norm(cfg, h, y, gate, scale, shift, mod_rows, post_weight, weight, h_out, x_out,
+                             _stream_ptr(stream, dev))
+    return (h if y is None else h_out), x_out
 
 
 def kvring_export(handle, k_out, v_out, scales, slot_pos, state, stream_ptr) -> None:

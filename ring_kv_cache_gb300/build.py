@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libkvring.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["kvring_host.cu", "kvring_cache.cu", "kvring_attn.cu", "kvring_pages_host.cu", "kvring_pages.cu",
-           "kvring_pages_few.cu", "kvring_pages_chunk.cu"]
+           "kvring_pages_few.cu", "kvring_pages_chunk.cu", "kvring_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]
