@@ -12,8 +12,17 @@
 //
 // Bound by HBM: h and y are read once, h' and x written once.  A row's values stay
 // in the registers of the threads that share it, eight per 16-byte load, so a norm
-// costs one exchange (two for a layer norm).
+// costs one exchange (two for a layer norm).  The tables' rows come from L1, where
+// the rows of an SM find them (a session's tokens lie together).  Measured (GB300):
+// 16,384 rows of 5,120, bf16, post norm, gate, 16 rows of fp32 tables, 674 MB: 148 us,
+// 4.5 TB/s; the instructions of a row's start and sums and the trips to L1 for 61 KB
+// of tables per row take what is left.  757 rows of 5,120, fp32 stream: 8.8 us; nine
+// rows of 1,280: 2.0 us.  Measured and slower: persistent blocks with rows ahead in
+// shared memory (cp.async), the tables from L1 (283 us: shared memory takes L1's
+// room) or held in registers (208 us: eight columns a thread, 534 instructions a warp
+// and row).
 #include <cmath>
+#include <type_traits>
 
 #include "kvring_pages.cuh"
 
@@ -32,55 +41,97 @@ struct NormDev {
   int n, vecs;          // rows, groups of eight columns
   int mods, mods_f32;   // rows of the modulation tables, their type
   int post, norm;       // KVRING_NORM_*
+  bool h_wide, ho_wide, m_wide;   // fp32 rows aligned to 32 bytes
   float eps, alpha, inv_width;
 };
 
-__device__ __forceinline__ void widen8(uint4 v, float (&x)[8]) {
+// Eight columns as four pairs: Blackwell multiplies and adds fp32 two at a time.
+using Pairs = float2[4];
+__device__ __forceinline__ void widen8(uint4 v, Pairs& x) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 narrow8(const Pairs& x) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[i].x, x[i].y);
     o[i] = *reinterpret_cast<const uint32_t*>(&b2);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// Eight values of a table of either type.
-__device__ __forceinline__ void table8(const void* base, long long at, bool f32, float (&x)[8]) {
-  if (f32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    widen8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at), x);
+// Eight columns of a row of either type, as they lie in memory.  fp32: one
+// 32-byte access, so that a warp's lies in whole lines; two of 16 where the
+// row is not aligned for it.  CACHED: tables, which other rows of the SM read too;
+// else past L1.
+template <bool F32>
+struct Raw8;
+template <>
+struct Raw8<true> {
+  float x[8];
+  template <bool CACHED>
+  __device__ __forceinline__ void load(const void* base, long long at, bool wide) {
+    const float* p = static_cast<const float*>(base) + at;
+    if (wide) {
+      if constexpr (CACHED)
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                     : "l"(p));
+      else
+        asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                     : "l"(p));
+    } else {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
   }
-}
+  __device__ __forceinline__ void widen(Pairs& y) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = make_float2(x[2 * e], x[2 * e + 1]);
+  }
+};
+template <>
+struct Raw8<false> {
+  uint4 v;
+  template <bool CACHED>
+  __device__ __forceinline__ void load(const void* base, long long at, bool) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+    v = CACHED ? *p : __ldcg(p);
+  }
+  __device__ __forceinline__ void widen(Pairs& x) const { widen8(v, x); }
+};
 
-// T threads share a row, NV groups of eight columns each; F32: the stream's type.
-template <int T, int NV, bool F32>
-__global__ void __launch_bounds__(T < 128 ? 128 : T) k_residual_norm(const NormDev a) {
-  constexpr int kRows = T < 128 ? 128 / T : 1;   // rows of a block
-  __shared__ float s_sum[4][T / 32];
-  const int tid = threadIdx.x % T, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kRows + (kRows > 1 ? (int)threadIdx.x / T : 0);
+constexpr int kRowWarps = 4;   // rows of a block where a warp is enough for one
+
+// T threads share a row, NV groups of eight columns each (FULL: exactly).  F32,
+// M32: the stream's and the tables' type.
+template <int NV, bool FULL, bool F32, bool M32>
+__global__ void __launch_bounds__(NV < 4 ? 1024 : (NV == 4 ? 512 : 416), 1)
+    k_residual_norm(const NormDev a, const int T) {
+  __shared__ float4 s_sum[4][8];
+  const bool one_warp = T == 32;                 // then a block holds several rows
+  const int tid = one_warp ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31;
+  const int row = one_warp ? blockIdx.x * kRowWarps + (threadIdx.x >> 5) : blockIdx.x;
+  if (!one_warp) {
+    if (threadIdx.x < 32) reinterpret_cast<float4*>(s_sum)[threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+  }
   int round = 0;
+  // (a place of its own for each of the at most four sums of a row)
   auto sum_row = [&](float v) -> float {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if constexpr (T > 32) {   // (a place for each of the at most four sums of a row)
-      if (lane == 0) s_sum[round][tid >> 5] = v;
+    if (!one_warp) {
+      if (lane == 0) reinterpret_cast<float*>(s_sum[round])[threadIdx.x >> 5] = v;
       __syncthreads();
       v = 0.f;
-#pragma unroll
-      for (int w = 0; w < T / 32; ++w) v += s_sum[round][w];
+      for (int w = 0; w < T; w += 128) {
+        const float4 p = s_sum[round][w >> 7];
+        v += (p.x + p.y) + (p.z + p.w);
+      }
       ++round;
     }
     return v;
@@ -89,129 +140,144 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) k_residual_norm(const NormD
   griddep_launch_dependents();
   if (row >= a.n) return;   // (whole warps, and no block-wide sum where a block has several rows)
   const int r = a.index ? __ldcg(a.index + row) : (a.mods > 1 ? row : 0);
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (FULL || i * T + tid < a.vecs) f(i, i * T + tid);
+  };
+  Raw8<F32> hr[NV];
+  uint4 yr[NV];
+  Pairs z[NV];
+  if (a.y) {
+    const uint4* y = reinterpret_cast<const uint4*>(a.y + row * a.y_stride);
+    each([&](int i, int v) { yr[i] = __ldcg(y + v); });
+  }
+  each([&](int i, int v) { hr[i].template load<false>(a.h, row * a.h_stride + 8 * v, a.h_wide); });
   const bool known = r >= 0 && r < a.mods;
   const long long mrow = known ? (long long)r * a.mod_stride : 0;
-  float z[NV][8], u[NV][8];
+  const float nan = __int_as_float(0x7FFFFFFF);
+  // z = f(z, table), in two steps, so that every load is on its way before the first
+  // value is used and no store lies between (over which none would be moved)
+  auto ask = [&](auto& t, const void* base, long long at, bool wide) {
+    each([&](int i, int v) { t[i].template load<true>(base, at + 8 * v, wide); });
+  };
+  auto with = [&](const auto& t, auto f) {
+    each([&](int i, int) {
+      Pairs g;
+      t[i].widen(g);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = i * T + tid;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[i][e] = u[i][e] = 0.f;
-    if (v >= a.vecs) continue;
-    if constexpr (F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.h) + row * a.h_stride) + 2 * v;
-      const float4 b = __ldcg(p), c = __ldcg(p + 1);
-      z[i][0] = b.x, z[i][1] = b.y, z[i][2] = b.z, z[i][3] = b.w;
-      z[i][4] = c.x, z[i][5] = c.y, z[i][6] = c.z, z[i][7] = c.w;
-    } else {
-      widen8(__ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.h) + row * a.h_stride) + v), z[i]);
-    }
-    if (a.y) widen8(__ldcg(reinterpret_cast<const uint4*>(a.y + row * a.y_stride) + v), u[i]);
-  }
-  // x - mean (layer) and 1 / sqrt(mean square + eps) of a row
-  auto standard = [&](float (&x)[NV][8], int kind) -> float {
+      for (int e = 0; e < 4; ++e) z[i][e] = f(z[i][e], g[e]);
+    });
+  };
+  auto times = [](float2 x, float2 y) { return __fmul2_rn(x, y); };
+  // 1 / sqrt(mean square + eps), after the mean is taken away (layer); places
+  // behind the row's end hold zeros
+  auto standard = [&](int kind) -> float {
     if (kind == KVRING_NORM_LAYER) {
-      float s = 0.f;
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += x[i][e];
-      const float mean = sum_row(s) * a.inv_width;
+        for (int e = 0; e < 4; ++e) s = __fadd2_rn(s, z[i][e]);
+      const float mean = sum_row(s.x + s.y) * -a.inv_width;
+      each([&](int i, int) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i * T + tid < a.vecs) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][e] -= mean;
-        }
+        for (int e = 0; e < 4; ++e) z[i][e] = __fadd2_rn(z[i][e], make_float2(mean, mean));
+      });
     }
-    float q = 0.f;
+    float2 q = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(x[i][e], x[i][e], q);
-    return rsqrtf(sum_row(q) * a.inv_width + a.eps);
+      for (int e = 0; e < 4; ++e) q = __ffma2_rn(z[i][e], z[i][e], q);
+    return rsqrtf(sum_row(q.x + q.y) * a.inv_width + a.eps);
   };
+  if constexpr (!FULL) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[i][e] = make_float2(0.f, 0.f);
+  }
   if (a.y) {
-    const float f = a.post != KVRING_NORM_NONE ? standard(u, a.post) : 1.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = i * T + tid;
-      if (v >= a.vecs) continue;
-      float g[8];
-      if (a.post_w) {
-        widen8(reinterpret_cast<const uint4*>(a.post_w)[v], g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[i][e] *= g[e];
-      }
-      if (a.gate) {
-        table8(a.gate, mrow + 8 * v, a.mods_f32, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[i][e] *= g[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[i][e] = fmaf(u[i][e] * f, a.alpha, z[i][e]);
-      if (!known) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[i][e] = __int_as_float(0x7FFFFFFF);
-      }
-      if (!a.h_out) continue;
-      if constexpr (F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.h_out) + row * a.ho_stride) + 2 * v;
-        p[0] = make_float4(z[i][0], z[i][1], z[i][2], z[i][3]);
-        p[1] = make_float4(z[i][4], z[i][5], z[i][6], z[i][7]);
-      } else {
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h_out) + row * a.ho_stride)[v] = narrow8(z[i]);
-      }
+    Raw8<false> pw[NV];
+    Raw8<M32> gr[NV];
+    if (a.post_w) ask(pw, a.post_w, 0, false);
+    if (a.gate) ask(gr, a.gate, mrow, a.m_wide);
+    each([&](int i, int) { widen8(yr[i], z[i]); });
+    float f = a.post != KVRING_NORM_NONE ? standard(a.post) : 1.0f;
+    if (a.post_w) with(pw, times);
+    if (a.gate) with(gr, times);
+    f = known ? f * a.alpha : nan;
+    with(hr, [f](float2 x, float2 h) { return __ffma2_rn(x, make_float2(f, f), h); });
+    if (a.h_out) {
+      each([&](int i, int v) {
+        if constexpr (F32) {
+          float* p = static_cast<float*>(a.h_out) + row * a.ho_stride + 8 * v;
+          if (a.ho_wide) {
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(z[i][0].x), "f"(z[i][0].y),
+                         "f"(z[i][1].x), "f"(z[i][1].y), "f"(z[i][2].x), "f"(z[i][2].y), "f"(z[i][3].x), "f"(z[i][3].y)
+                         : "memory");
+          } else {
+            reinterpret_cast<float4*>(p)[0] = make_float4(z[i][0].x, z[i][0].y, z[i][1].x, z[i][1].y);
+            reinterpret_cast<float4*>(p)[1] = make_float4(z[i][2].x, z[i][2].y, z[i][3].x, z[i][3].y);
+          }
+        } else {
+          reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h_out) + row * a.ho_stride)[v] = narrow8(z[i]);
+        }
+      });
     }
+  } else {
+    each([&](int i, int) { hr[i].widen(z[i]); });
   }
   if (a.norm == KVRING_NORM_NONE) return;
-  const float f = standard(z, a.norm);
+  Raw8<false> w[NV];
+  Raw8<M32> sr[NV], br[NV];
+  if (a.w) ask(w, a.w, 0, false);
+  if (a.scale) ask(sr, a.scale, mrow, a.m_wide);
+  if (NV < 4 && a.shift) ask(br, a.shift, mrow, a.m_wide);
+  float f = standard(a.norm);
+  if (!known) f = nan;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = i * T + tid;
-    if (v >= a.vecs) continue;
-    float g[8];
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[i][e] *= f;
-    if (a.w) {
-      widen8(reinterpret_cast<const uint4*>(a.w)[v], g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[i][e] *= g[e];
-    }
-    if (a.scale) {
-      table8(a.scale, mrow + 8 * v, a.mods_f32, g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[i][e] *= 1.0f + g[e];
-    }
-    if (a.shift) {
-      table8(a.shift, mrow + 8 * v, a.mods_f32, g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[i][e] += g[e];
-    }
-    if (!known) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[i][e] = __int_as_float(0x7FFFFFFF);
-    }
-    reinterpret_cast<uint4*>(a.x_out + row * a.x_stride)[v] = narrow8(z[i]);
-  }
+    for (int e = 0; e < 4; ++e) z[i][e] = __fmul2_rn(z[i][e], make_float2(f, f));
+  if (a.w) with(w, times);
+  if (a.scale) with(sr, [](float2 x, float2 y) { return __ffma2_rn(x, y, x); });
+  if (NV >= 4 && a.shift) ask(br, a.shift, mrow, a.m_wide);   // (the registers do not hold more)
+  if (a.shift) with(br, [](float2 x, float2 y) { return __fadd2_rn(x, y); });
+  uint4* o = reinterpret_cast<uint4*>(a.x_out + row * a.x_stride);
+  each([&](int i, int v) { o[v] = narrow8(z[i]); });
 }
 
-template <int T, int NV>
-cudaError_t go(const NormDev& d, bool f32, cudaStream_t s) {
-  constexpr int kRows = T < 128 ? 128 / T : 1;
-  const dim3 grid((unsigned)((d.n - 1) / kRows + 1)), block(T < 128 ? 128 : T);
-  return f32 ? launch_pdl(k_residual_norm<T, NV, true>, grid, block, 0, s, d)
-             : launch_pdl(k_residual_norm<T, NV, false>, grid, block, 0, s, d);
+template <int NV, bool FULL>
+cudaError_t go(const NormDev& d, bool f32, int T, cudaStream_t s) {
+  const int rows = T == 32 ? kRowWarps : 1;   // of a block
+  const dim3 grid((unsigned)((d.n - 1) / rows + 1)), block((unsigned)(T * rows));
+  if (f32)
+    return d.mods_f32 ? launch_pdl(k_residual_norm<NV, FULL, true, true>, grid, block, 0, s, d, T)
+                      : launch_pdl(k_residual_norm<NV, FULL, true, false>, grid, block, 0, s, d, T);
+  return d.mods_f32 ? launch_pdl(k_residual_norm<NV, FULL, false, true>, grid, block, 0, s, d, T)
+                    : launch_pdl(k_residual_norm<NV, FULL, false, false>, grid, block, 0, s, d, T);
 }
 
 cudaError_t launch_residual_norm(const NormDev& d, bool f32, cudaStream_t s) {
-  if (d.vecs <= 32) return go<32, 1>(d, f32, s);
-  if (d.vecs <= 96) return go<32, 3>(d, f32, s);
-  if (d.vecs <= 160) return go<32, 5>(d, f32, s);
-  if (d.vecs <= 384) return go<128, 3>(d, f32, s);
-  if (d.vecs <= 640) return go<128, 5>(d, f32, s);
-  if (d.vecs <= 1280) return go<256, 5>(d, f32, s);
-  return go<512, 4>(d, f32, s);
+  // Groups of eight columns a thread.  Few rows: one, for latency (9 rows of 1,280:
+  // 2.0 us, with five 2.4).  Else four or five, for a row's fixed instructions are
+  // then shared by more columns (16,384 rows of 5,120, one: 287 us, two: 167,
+  // four: 148), or what leaves the fewest places empty.
+  auto threads = [&](int nv) { return (d.vecs + 32 * nv - 1) / (32 * nv) * 32; };
+  int nv = 4;
+  for (int k : {5, 2})
+    if (threads(k) * k < threads(nv) * nv) nv = k;
+  if (d.vecs <= 1024 && (long long)d.n * d.vecs <= 152 * 1024) nv = 1;
+  const int T = threads(nv);
+  const bool full = d.vecs == T * nv;
+  switch (nv) {
+    case 1: return full ? go<1, true>(d, f32, T, s) : go<1, false>(d, f32, T, s);
+    case 2: return full ? go<2, true>(d, f32, T, s) : go<2, false>(d, f32, T, s);
+    case 4: return full ? go<4, true>(d, f32, T, s) : go<4, false>(d, f32, T, s);
+    default: return full ? go<5, true>(d, f32, T, s) : go<5, false>(d, f32, T, s);
+  }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -294,6 +360,11 @@ extern "C" kvring_status kvring_residual_norm(const kvring_norm_config* c, const
   d.mod_stride = c->mod_stride;
   d.n = c->num_tokens;
   d.vecs = c->width / 8;
+  // fp32 rows of 32-byte groups (strides are multiples of them)
+  auto wide = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; };
+  d.h_wide = wide(h);
+  d.ho_wide = wide(h_out);
+  d.m_wide = wide(gate) && wide(scale) && wide(shift);
   d.mods = tables ? c->mod_rows : 1;
   d.mods_f32 = c->mod_dtype == KVRING_OUT_F32;
   d.post = c->post_norm;
