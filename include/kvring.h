@@ -403,7 +403,25 @@ typedef struct {
   int32_t rope_pairing;  /* KVRING_ROPE_* */
   int32_t reserved;      /* 0 */
   double rope_base;
+  int32_t scale_block;   /* E4M3: 0 = a scale per layer and head (kvring_pages_set_scales), or
+                            KVRING_SCALE_BLOCK = a scale for every 16 tokens of a page and head, set by
+                            kvring_pages_write */
+  int32_t rope_pairs_t;  /* 0 = 1-D RoPE by a token's position in its request.  Else 3-D: of the
+                            head_dim/2 pairs, [0, T) turn with t, [T, T + Y) with y, the rest with x
+                            (any sizes, T >= 1), the coordinates being given to
+                            kvring_pages_write_3d */
+  int32_t rope_pairs_y;  /* Y (0 with 1-D RoPE) */
+  int32_t rope_frequencies; /* KVRING_FREQ_* of 3-D RoPE (0 with 1-D) */
+  int32_t max_position;  /* 3-D: coordinates lie in [0, max_position), at most 2^24; 0 = W * page_size
+                            (0 with 1-D) */
+  int32_t reserved2;     /* 0 */
 } kvring_pages_config;
+
+#define KVRING_SCALE_BLOCK 16
+#define KVRING_FREQ_SECTION 0    /* each section a RoPE of its own: its j-th of m pairs turns by
+                                    coordinate * base^(-j/m), as the ring's */
+#define KVRING_FREQ_HEAD 1       /* pair i turns by coordinate * base^(-2i/d), so equal coordinates turn
+                                    a head as the 1-D position does */
 
 /* Where things lie in the buffer given to kvring_pages_create (byte
  * offsets), for a caller's own kernels, snapshots and tests. */
@@ -420,6 +438,9 @@ typedef struct {
   size_t step_lengths; /* int32 [max_requests]: their lengths with the new tokens */
   size_t positions;    /* int32 [max_tokens]: position of each new token in its request */
   size_t slots;        /* int32 [max_tokens]: page * page_size + offset, -1 for padding */
+  size_t k_block_scales; /* uint8 [L][num_pages][Hkv][page_size / 16]: a block's scale is 2^(byte - 127),
+                            E8M0 (127 at create); with scale_block only */
+  size_t v_block_scales; /* the same */
   size_t total;        /* bytes of the whole buffer */
 } kvring_pages_layout;
 
@@ -438,6 +459,7 @@ typedef struct {
 #define KVRING_PAGES_ERR_COMMIT 16u  /* a commit with no plan before it */
 #define KVRING_PAGES_ERR_TABLE 32u   /* a page id outside [0, num_pages) in a table or the free list */
 #define KVRING_PAGES_ERR_TIMEOUT 64u /* a wait in the attention kernel gave up */
+#define KVRING_PAGES_ERR_POSITION 128u /* a coordinate outside [0, max_position): the token was skipped */
 
 /* The layout for a config; INVALID_ARG if the config is invalid (*out is
  * then zeroed).  layout.total is what kvring_pages_create needs. */
@@ -515,6 +537,27 @@ kvring_status kvring_pages_release(kvring_pages_t* pages, const int32_t* rows, i
 kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const void* q, const void* k, const void* v,
                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, const void* q_weight,
                                  const void* k_weight, float eps, void* q_out, int32_t num_tokens, void* stream);
+
+/* kvring_pages_write for a cache with 3-D RoPE: coords int32 [num_tokens][3] = (t, y, x)
+ * of every token (device; outside q_out and the cache's buffer).  Where tokens
+ * go and what attention lets them see stays with their places in the request.  A
+ * token with a coordinate outside [0, max_position) sets
+ * KVRING_PAGES_ERR_POSITION; its row of q_out and its place in the cache stay as
+ * they were.  kvring_pages_write refuses such a cache, and this call a 1-D one.
+ *
+ * In a cache with block scales (either call) 16 tokens at places 16 b .. 16 b + 15
+ * of a request share a scale per head, of keys and of values:
+ *   need  = least 2^e with |value| <= 448 2^e for the step's tokens in the block,
+ *           e in [-40, 40] (beyond, values saturate or vanish)
+ *   scale = need, or max(need, the scale so far) where the block holds tokens
+ *           from before; these are then rounded to the new scale,
+ *           code = e4m3(code * (old / new))
+ *   code  = e4m3(value / scale)
+ * Values that are not finite have no part in `need`: infinities saturate, NaN stays. */
+kvring_status kvring_pages_write_3d(kvring_pages_t* pages, int32_t layer, const void* q, const void* k, const void* v,
+                                    int64_t q_stride, int64_t k_stride, int64_t v_stride, const void* q_weight,
+                                    const void* k_weight, float eps, const int32_t* coords, void* q_out,
+                                    int32_t num_tokens, void* stream);
 
 /* Attention of the planned tokens' queries over their requests' cached
  * tokens, the new ones included:

@@ -61,10 +61,12 @@ class KvringConfig(ctypes.Structure):
 
 CACHE_E4M3, CACHE_BF16 = 0, 1
 ROPE_ADJACENT, ROPE_HALVES = 0, 1
+FREQ_SECTION, FREQ_HEAD = 0, 1
+SCALE_BLOCK = 16
 PAGES_STATE = dict(free=0, error=1, planned=2, requests=3, tokens=4, taken=5)
 PAGES_STATE_WORDS = 8
 PAGES_ERR_ROW, PAGES_ERR_TOKENS, PAGES_ERR_LENGTH, PAGES_ERR_PAGES = 1, 2, 4, 8
-PAGES_ERR_COMMIT, PAGES_ERR_TABLE, PAGES_ERR_TIMEOUT = 16, 32, 64
+PAGES_ERR_COMMIT, PAGES_ERR_TABLE, PAGES_ERR_TIMEOUT, PAGES_ERR_POSITION = 16, 32, 64, 128
 
 
 NORMS = {None: 0, "rms": 1, "layer": 2}
@@ -81,13 +83,14 @@ class KvringPagesConfig(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in (
         "num_q_heads", "num_kv_heads", "head_dim", "num_layers", "page_size", "num_pages", "max_requests",
         "max_pages_per_request", "max_tokens", "cache_dtype", "rope_pairing", "reserved")] + [
-        ("rope_base", ctypes.c_double)]
+        ("rope_base", ctypes.c_double)] + [(f, ctypes.c_int32) for f in (
+            "scale_block", "rope_pairs_t", "rope_pairs_y", "rope_frequencies", "max_position", "reserved2")]
 
 
 class KvringPagesLayout(ctypes.Structure):
     _fields_ = [(f, ctypes.c_size_t) for f in (
         "k_cache", "v_cache", "scales", "lengths", "tables", "free_pages", "state", "step_rows", "step_cu",
-        "step_lengths", "positions", "slots", "total")]
+        "step_lengths", "positions", "slots", "k_block_scales", "v_block_scales", "total")]
 
 
 class KvRingError(RuntimeError):
@@ -138,6 +141,7 @@ def lib():
         "kvring_pages_commit": (i32, [vp, vp]),
         "kvring_pages_release": (i32, [vp, vp, i32, vp]),
         "kvring_pages_write": (i32, [vp, i32, vp, vp, vp, i64, i64, i64, vp, vp, ctypes.c_float, vp, i32, vp]),
+        "kvring_pages_write_3d": (i32, [vp, i32, vp, vp, vp, i64, i64, i64, vp, vp, ctypes.c_float, vp, vp, i32, vp]),
         "kvring_pages_attention": (i32, [vp, i32, vp, i64, vp, i32, i32, i32, ctypes.c_float, vp]),
         "kvring_pages_debug_set_wait": (i32, [vp, i64, i32]),
         "kvring_debug_encode_e4m3": (i32, [vp, vp, i64, vp]),
@@ -618,10 +622,12 @@ def _i32(x) -> int:
 
 def make_pages_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_requests, max_pages_per_request,
                       max_tokens, layers=1, cache_dtype=CACHE_E4M3, rope_pairing=ROPE_ADJACENT,
-                      rope_base=10000.0) -> KvringPagesConfig:
+                      rope_base=10000.0, scale_block=0, rope3d=None, rope_frequencies=FREQ_SECTION,
+                      max_position=0) -> KvringPagesConfig:
+    pt, py = (0, 0) if rope3d is None else rope3d
     return KvringPagesConfig(*map(_i32, (q_heads, kv_heads, head_dim, layers, page_size, num_pages, max_requests,
                                          max_pages_per_request, max_tokens, cache_dtype, rope_pairing, 0)),
-                             float(rope_base))
+                             float(rope_base), *map(_i32, (scale_block, pt, py, rope_frequencies, max_position, 0)))
 
 
 def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
@@ -673,7 +679,9 @@ class KvPages:
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int, num_pages: int, max_requests: int,
                  max_request_tokens: int, max_tokens: int, layers: int = 1, cache_dtype=torch.float8_e4m3fn,
-                 rope_pairing: str = "adjacent", rope_base: float = 10000.0, device=None, stream=None):
+                 rope_pairing: str = "adjacent", rope_base: float = 10000.0, device=None, stream=None,
+                 block_scales: bool = False, rope3d=None, rope_frequencies: str = "section",
+                 max_position: int | None = None):
         if not torch.cuda.is_available():
             raise RuntimeError("KvPages needs a CUDA device")
         d = torch.device(device) if device is not None else torch.device("cuda")
@@ -683,6 +691,14 @@ class KvPages:
             raise ValueError("cache_dtype must be float8_e4m3fn or bfloat16")
         if rope_pairing not in ("adjacent", "halves"):
             raise ValueError("rope_pairing must be 'adjacent' or 'halves'")
+        if block_scales and cache_dtype != torch.float8_e4m3fn:
+            raise ValueError("block_scales are of a float8_e4m3fn cache")
+        if rope_frequencies not in ("section", "head"):
+            raise ValueError("rope_frequencies must be 'section' or 'head'")
+        if rope3d is None and (rope_frequencies != "section" or max_position is not None):
+            raise ValueError("rope_frequencies and max_position need rope3d")
+        if rope3d is not None and (len(rope3d) != 2 or int(rope3d[0]) < 1 or (max_position is not None and max_position < 1)):
+            raise ValueError("rope3d must be (pairs of t, pairs of y), max_position positive")
         self.device = d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
         self.Hq, self.Hkv, self.d, self.P = int(q_heads), int(kv_heads), int(head_dim), int(page_size)
         self.L, self.num_pages, self.R = int(layers), int(num_pages), int(max_requests)
@@ -691,7 +707,9 @@ class KvPages:
         self.cfg = make_pages_config(q_heads, kv_heads, head_dim, page_size, num_pages, max_requests, self.W,
                                      max_tokens, layers, CACHE_E4M3 if cache_dtype == torch.float8_e4m3fn
                                      else CACHE_BF16, ROPE_HALVES if rope_pairing == "halves" else ROPE_ADJACENT,
-                                     rope_base)
+                                     rope_base, SCALE_BLOCK if block_scales else 0, rope3d,
+                                     FREQ_HEAD if rope_frequencies == "head" else FREQ_SECTION, max_position or 0)
+        self.block_scales, self.three_d = bool(block_scales), rope3d is not None
         try:
             self.layout = kvring_pages_get_layout(self.cfg)
         except KvRingError:
@@ -740,6 +758,26 @@ class KvPages:
     def v_cache(self, layer: int = 0) -> torch.Tensor:
         """The layer's values [num_pages, Hkv, page_size, d], a view of the buffer."""
         return self._cache(self.layout.v_cache, layer)
+
+    def _scales(self, off: int, layer: int) -> torch.Tensor:
+        if not self.block_scales:
+            raise ValueError("the cache has no block scales")
+        if (off, layer) not in self._caches:
+            if not 0 <= layer < self.L:
+                raise ValueError(f"layer must be in [0, {self.L})")
+            shape = (self.num_pages, self.Hkv, self.P // SCALE_BLOCK)
+            n = shape[0] * shape[1] * shape[2]
+            self._caches[off, layer] = self.buf[off + layer * n:off + (layer + 1) * n].view(torch.float8_e8m0fnu).view(shape)
+        return self._caches[off, layer]
+
+    def k_scales(self, layer: int = 0) -> torch.Tensor:
+        """The scales of the layer's keys, float8_e8m0fnu [num_pages, Hkv,
+        page_size / 16], a view of the buffer (with ``block_scales``)."""
+        return self._scales(self.layout.k_block_scales, layer)
+
+    def v_scales(self, layer: int = 0) -> torch.Tensor:
+        """The scales of the layer's values, as ``k_scales``."""
+        return self._scales(self.layout.v_block_scales, layer)
 
     def _int_arg(self, x, name: str, shape=None):
         if not isinstance(x, torch.Tensor) or x.device != self.device or x.dtype != torch.int32 \
@@ -819,11 +857,12 @@ class KvPages:
         return x
 
     def write(self, layer: int, q, k, v, q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None,
-              stream=None) -> torch.Tensor:
+              stream=None, pos=None) -> torch.Tensor:
         """Head norms (where weights bf16 [d] are given), RoPE and the write of
         the planned tokens' keys and values; returns the rotated queries
         (bf16 [n, Hq, d]).  Rows of ``q_out`` past the plan's tokens are left
-        as they were (undefined in a new tensor)."""
+        as they were (undefined in a new tensor).  ``pos``: with ``rope3d``, and
+        only then, the tokens' (t, y, x), int32 [n, 3]."""
         n, qs = self._heads(q, self.Hq, "q")
         nk, ks = self._heads(k, self.Hkv, "k")
         nv, vs = self._heads(v, self.Hkv, "v")
@@ -833,9 +872,16 @@ class KvPages:
             if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16
                                   or t.device != self.device or t.shape != (self.d,) or not t.is_contiguous()):
                 raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{self.d}] on {self.device}")
+        if self.three_d:
+            self._int_arg(pos, "pos", (n, 3))
+        elif pos is not None:
+            raise ValueError("pos needs a cache with rope3d")
         q_out = self._result(q_out, n, "q_out", stream)
-        self._call(_LIB.kvring_pages_write, "kvring_pages_write", stream, _i32(layer), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                   qs, ks, vs, _ptr(q_norm), _ptr(k_norm), float(eps), q_out.data_ptr(), n)
+        args = (_i32(layer), q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_norm), _ptr(k_norm), float(eps))
+        if self.three_d:
+            self._call(_LIB.kvring_pages_write_3d, "kvring_pages_write_3d", stream, *args, pos.data_ptr(), q_out.data_ptr(), n)
+        else:
+            self._call(_LIB.kvring_pages_write, "kvring_pages_write", stream, *args, q_out.data_ptr(), n)
         return q_out
 
     def attention(self, layer: int, q, out=None, causal: bool = True, window: int = 0, scale: float = 0.0,

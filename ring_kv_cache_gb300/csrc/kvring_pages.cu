@@ -4,6 +4,8 @@
 // All kernels wait for the preceding kernel on the stream
 // (griddepcontrol.wait) before they read anything, and let the next one
 // start right after that.
+#include <type_traits>
+
 #include "kvring_pages.cuh"
 
 namespace kvr {
@@ -346,6 +348,18 @@ __global__ void k_pages_table(float* table, const Thetas th, int half, size_t n)
   }
 }
 
+// --------------------------------------------------------- 3-D positions ---
+__device__ __forceinline__ bool coords_ok(const PagesDev& p, const int (&xyz)[3]) {
+  const unsigned n = (unsigned)p.max_pos;
+  return (unsigned)xyz[0] < n && (unsigned)xyz[1] < n && (unsigned)xyz[2] < n;
+}
+// cos and sin of a pair, from the row of its section's coordinate.
+template <int D>
+__device__ __forceinline__ float2 turn_of(const PagesDev& p, const int (&xyz)[3], int pair) {
+  const int row = pair < p.pt ? xyz[0] : (pair < p.pt + p.py ? xyz[1] : xyz[2]);
+  return __ldg(reinterpret_cast<const float2*>(p.table) + (size_t)row * (D / 2) + pair);
+}
+
 // ----------------------------------------------------------------- write ---
 // y = x rsqrt(mean x^2 + eps) w, rotated; one rounding at the end.  Bound by
 // HBM: each bf16 head row is read once and its result written once.
@@ -370,7 +384,11 @@ __global__ void k_pages_table(float* table, const Thetas th, int half, size_t n)
 constexpr int kWriteWarps = 4;
 constexpr int kWriteBatch = 4;
 
-template <int D, bool E4M3, bool HALVES>
+// AXES: 3-D positions: each pair's cos and sin from the row of its own coordinate,
+// once per token.  KV false: the queries alone, beside the kernel that writes blocks
+// with scales: it starts when that one has seen its predecessors done, and waits
+// for it at the end.
+template <int D, bool E4M3, bool HALVES, bool AXES, bool KV>
 __global__ void __launch_bounds__(kWriteWarps * 32, 8)
     k_pages_write(const PagesDev p, const PagesWrite w) {
   constexpr int LPR = D / 8, TPW = 32 / LPR;
@@ -419,28 +437,55 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
       inv_v = __ldcg(inv + p.Hkv + h);
     }
   };
-  griddep_wait();
+  if constexpr (KV) griddep_wait();
   griddep_launch_dependents();
   // Everything that depends on nothing else is asked for at once; only the
   // cos/sin row waits, for the position.  Key/value heads are dealt out from
   // the other end, so that warps without a query head take them first.
   const int hk0 = step - 1 - gw;
   load_q(gw);
-  if (hk0 < p.Hkv) load_kv(hk0);
+  if constexpr (KV) {
+    if (hk0 < p.Hkv) load_kv(hk0);
+  }
   int tokens = __ldcg(p.state + PST_TOKENS);
   int slot = mine ? __ldcg(p.slots + t) : -1;
-  int pos = mine ? __ldcg(p.pos + t) : 0;
+  int pos = mine && !AXES ? __ldcg(p.pos + t) : 0;
+  int xyz[3] = {0, 0, 0};
+  if constexpr (AXES) {
+    if (mine) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) xyz[i] = __ldcg(w.coords + 3 * (size_t)t + i);
+    }
+  }
   const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // bf16 ones
   const uint4 gq = w.qw ? load(w.qw) : one, gk = w.kw ? load(w.kw) : one;
   tokens = tokens < w.T ? tokens : w.T;
-  if (blockIdx.x * TPW >= tokens) return;
-  const bool valid = t < tokens;
+  if (blockIdx.x * TPW >= tokens) {
+    if constexpr (!KV) griddep_wait();
+    return;
+  }
+  bool valid = t < tokens;
   if (!valid) {
     slot = -1;
     pos = 0;
   }
-  const float4 cs0 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c));
-  const float4 cs1 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c + 4));
+  float4 cs0, cs1;
+  if constexpr (!AXES) {
+    cs0 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c));
+    cs1 = __ldg(reinterpret_cast<const float4*>(p.table + (size_t)pos * D + 8 * c + 4));
+  } else {
+    if (!coords_ok(p, xyz)) {
+      if (valid) set_error(p, KVRING_PAGES_ERR_POSITION);
+      valid = false;
+      slot = -1;
+      xyz[0] = xyz[1] = xyz[2] = 0;
+    }
+    float2 cs[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cs[e] = turn_of<D>(p, xyz, 4 * c + e);
+    cs0 = make_float4(cs[0].x, cs[0].y, cs[1].x, cs[1].y);
+    cs1 = make_float4(cs[2].x, cs[2].y, cs[3].x, cs[3].y);
+  }
   // pair e: values lo(e), hi(e) of the lane's eight
   auto lo = [](int e) { return HALVES ? e : 2 * e; };
   auto hi = [](int e) { return HALVES ? 4 + e : 2 * e + 1; };
@@ -517,6 +562,10 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
       if (valid) store_bf16(q_out + h * D, x);
     }
   }
+  if constexpr (!KV) {
+    griddep_wait();
+    return;
+  }
   if (hk0 >= p.Hkv) return;
   matrix(gk);
   // row of (page, head 0, offset) in the layer's caches; heads are P rows apart
@@ -530,6 +579,279 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
     if (slot >= 0) store_cache(p.k, row, x, inv_k);
     widen(vraw, x);
     if (slot >= 0) store_cache(p.v, row, x, inv_v);
+  }
+}
+
+// ------------------------------------------- write into blocks with scales ---
+// Keys and values into an E4M3 cache whose blocks of 16 tokens have a scale
+// 2^e each:  e = least with amax <= 448 2^e over the step's tokens of the block,
+// not below the block's so far where it holds tokens; those are then rounded
+// again, code * 2^(e_old - e_new).  Powers of two, so that neither a value's
+// division by its scale nor a code's move to a larger one rounds, but for the one
+// rounding to E4M3's step (a code that has moved loses bits only among the
+// subnormals): a scale of amax / 448 itself would use the top binade better by less than
+// one step in 16 and round every code again with each growth.
+//
+// Bound by HBM as the write above.  A warp takes the tokens of a block that are
+// new (a run: the step's tokens with consecutive slots of one block) and a
+// head: all its values are in registers when their size is known, so each is
+// read once, and a block's codes leave as whole lines.  Runs begin anywhere, so a
+// group of 16 consecutive tokens of the step owns those that begin in it: up to
+// 16 runs (single tokens) and up to 31 tokens, of which the first 16 and a last
+// run of up to 16 make two turns at most (mostly one).  Sizes of rows are
+// exchanged through shared memory, a lane per row: segmented maximum over the
+// runs, the exponent, and back by shuffles.  cos/sin rows of the group's tokens lie in
+// shared memory for all heads of the block's four warps.
+constexpr int kBlockWarps = 4;
+
+__device__ __forceinline__ int block_exponent(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u);   // 448 = 1.75 x 2^8
+  return min(max(e, kMinExp), kMaxExp);
+}
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // 2^e
+
+template <int D, bool HALVES, bool AXES>
+__global__ void __launch_bounds__(kBlockWarps * 32, 3) k_pages_write_blocks(const PagesDev p, const PagesWrite w) {
+  constexpr int LPR = D / 8, TPW = 32 / LPR, IT = 16 / TPW;
+  constexpr int B = KVRING_SCALE_BLOCK;
+  static_assert(B == 16, "a turn is one block");
+  __shared__ __align__(16) float s_cs[32][D];        // cos, sin of the window's tokens
+  __shared__ float s_max[kBlockWarps][16];
+  const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+  const int e0 = HALVES ? 4 * c : 8 * c, e1 = HALVES ? D / 2 + 4 * c : 8 * c + 4;
+  const int step = kBlockWarps * gridDim.y, h0 = blockIdx.y * kBlockWarps + warp;
+  griddep_wait();
+  griddep_launch_dependents();
+  // The window: lane i looks at token 16 g - 1 + i.
+  const int t_lane = blockIdx.x * B - 1 + lane;
+  int tokens = __ldcg(p.state + PST_TOKENS);
+  int slot = t_lane >= 0 && t_lane < w.T ? __ldcg(p.slots + t_lane) : -1;
+  tokens = tokens < w.T ? tokens : w.T;
+  if (t_lane >= tokens) slot = -1;
+  const int prev = __shfl_up_sync(0xFFFFFFFFu, slot, 1);
+  const bool follows = lane > 0 && slot >= 0 && slot == prev + 1 && (slot & (B - 1)) != 0;
+  const unsigned cont = __ballot_sync(0xFFFFFFFFu, follows);
+  const unsigned lead = __ballot_sync(0xFFFFFFFFu, slot >= 0 && !follows) & 0x1FFFEu;
+  if (lead == 0) return;   // (the same in every warp)
+  const int f = __ffs(lead) - 1, last = 31 - __clz(lead);
+  // end of the last run: the first lane behind `last` that does not follow
+  const unsigned stops = ~cont & ~((2u << last) - 1);
+  const int end = stops ? __ffs(stops) - 1 : 32;
+  // lanes that belong to a run of this group
+  const unsigned members = (lead | cont) & (0xFFFFFFFFu << f) & (end == 32 ? 0xFFFFFFFFu : (1u << end) - 1);
+  const bool member = members >> lane & 1u;
+  bool stored = member;
+  // cos and sin of the members' tokens
+  int at[3] = {0, 0, 0};
+  if (member) {
+    if constexpr (AXES) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) at[i] = __ldcg(w.coords + 3 * (size_t)t_lane + i);
+      if (!coords_ok(p, at)) {
+        set_error(p, KVRING_PAGES_ERR_POSITION);
+        stored = false;
+        at[0] = at[1] = at[2] = 0;
+      }
+    } else {
+      at[0] = __ldcg(p.pos + t_lane);
+    }
+  }
+  const unsigned store_mask = __ballot_sync(0xFFFFFFFFu, stored);
+  auto widen = [](uint4 v, float (&x)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  };
+  auto load = [&](const uint16_t* row) -> uint4 {
+    if constexpr (HALVES) {
+      const uint2 a = __ldcg(reinterpret_cast<const uint2*>(row + e0));
+      const uint2 b = __ldcg(reinterpret_cast<const uint2*>(row + e1));
+      return make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      return __ldcg(reinterpret_cast<const uint4*>(row + e0));
+    }
+  };
+  // The rows of a turn, `base` its first lane: whole runs, at most 16.
+  auto rows_of = [&](int base) { return end - base > 16 ? last - base : end - base; };
+  uint4 kr[IT], vr[IT];
+  auto fetch = [&](int h, int base) {
+    const unsigned live = (store_mask >> base) & ((1u << rows_of(base)) - 1);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int r = i * TPW + sub;
+      kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live >> r & 1u) {
+        const long long t = (long long)blockIdx.x * B - 1 + base + r;
+        kr[i] = load(w.k + t * w.k_stride + h * D);
+        vr[i] = load(w.v + t * w.v_stride + h * D);
+      }
+    }
+  };
+  if (h0 < p.Hkv) fetch(h0, f);
+  {
+    constexpr int kPer = 32 / kBlockWarps, kPart = D / 64;   // rows of a warp, pairs of a lane
+    float2 v[kPer][kPart];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = f + j * kBlockWarps + warp;
+      const int xyz[3] = {__shfl_sync(0xFFFFFFFFu, at[0], i & 31), __shfl_sync(0xFFFFFFFFu, at[1], i & 31),
+                          __shfl_sync(0xFFFFFFFFu, at[2], i & 31)};
+      if (i < end) {
+#pragma unroll
+        for (int k = 0; k < kPart; ++k)
+          v[j][k] = AXES ? turn_of<D>(p, xyz, lane + 32 * k)
+                         : __ldg(reinterpret_cast<const float2*>(p.table) + (size_t)xyz[0] * (D / 2) + lane + 32 * k);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = f + j * kBlockWarps + warp;
+      if (i < end) {
+#pragma unroll
+        for (int k = 0; k < kPart; ++k) reinterpret_cast<float2*>(s_cs[i])[lane + 32 * k] = v[j][k];
+      }
+    }
+  }
+  __syncthreads();
+  float gk[8];
+  if (w.kw) {
+    widen(load(w.kw), gk);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gk[e] = 1.0f;
+  }
+  const long long page_lane = member ? slot >> p.logP : 0;
+  // rows of the cache [layer][page][head][offset], of this lane's token at head 0
+  const size_t row_lane = (((size_t)w.layer * p.num_pages + page_lane) * p.Hkv << p.logP) + (slot & (p.P - 1));
+  for (int h = h0; h < p.Hkv; h += step) {
+    int base = f;
+    while (base < end) {
+      const int n = rows_of(base);
+      const unsigned here = (members >> base) & ((1u << n) - 1);
+      const unsigned firsts = (lead >> base) & here, live = (store_mask >> base) & here;
+      // Lane r < 16: row r of the turn, its run's first row and the row behind its last.
+      const int r = lane & 15;
+      const size_t row_r = __shfl_sync(0xFFFFFFFFu, row_lane, (base + r) & 31) + ((size_t)h << p.logP);
+      const int slot_r = __shfl_sync(0xFFFFFFFFu, slot, (base + r) & 31);
+      const unsigned upto = firsts & ((2u << r) - 1), behind = (firsts | ~here) & ~((2u << r) - 1);
+      const int from = upto ? 31 - __clz(upto) : 0;
+      const int to = __ffs(behind) - 1;              // (here has at most 16 bits: there is one)
+      const bool row_here = (here >> r & 1u) && lane < 16;
+      const int held = (slot_r & (B - 1)) - (r - from);   // tokens the block held before
+      const size_t block = row_r >> 4;
+      int old_k = 0, old_v = 0;
+      if (row_here && held > 0) {
+        old_k = min(max((int)__ldcg(p.ks + block), kMinExp), kMaxExp);
+        old_v = min(max((int)__ldcg(p.vs + block), kMinExp), kMaxExp);
+      }
+      auto put = [&](const float (&x)[IT][8], uint8_t* cache, uint8_t* scales, int old) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float y = fabsf(x[i][e]);
+            m = fmaxf(m, y < INFINITY ? y : 0.f);    // (not the infinite ones, nor NaN)
+          }
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          if (c == 0) s_max[warp][i * TPW + sub] = m;
+        }
+        __syncwarp();
+        float m = s_max[warp][r];
+        __syncwarp();
+        // maximum over the run: up to its last row, then back from there
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+          const float y = __shfl_up_sync(0xFFFFFFFFu, m, o, 16);
+          if (r - o >= from) m = fmaxf(m, y);
+        }
+        m = __shfl_sync(0xFFFFFFFFu, m, to - 1, 16);
+        const int need = block_exponent(m), exp = held > 0 ? max(need, old) : need;
+        const float inv = power(127 - exp);           // 2^-(exp - 127)
+        if (row_here && r == from) scales[block] = (uint8_t)exp;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int k = i * TPW + sub;
+          const float s = __shfl_sync(0xFFFFFFFFu, inv, k);
+          const size_t row = __shfl_sync(0xFFFFFFFFu, row_r, k);
+          if (!(live >> k & 1u)) continue;
+          const uint32_t a =
+              f32x2_to_e4m3x2(x[i][0] * s, x[i][1] * s) | ((uint32_t)f32x2_to_e4m3x2(x[i][2] * s, x[i][3] * s) << 16);
+          const uint32_t b =
+              f32x2_to_e4m3x2(x[i][4] * s, x[i][5] * s) | ((uint32_t)f32x2_to_e4m3x2(x[i][6] * s, x[i][7] * s) << 16);
+          uint8_t* dst = cache + row * D;
+          if constexpr (HALVES) {
+            *reinterpret_cast<uint32_t*>(dst + e0) = a;
+            *reinterpret_cast<uint32_t*>(dst + e1) = b;
+          } else {
+            *reinterpret_cast<uint2*>(dst + e0) = make_uint2(a, b);
+          }
+        }
+        // blocks whose tokens from before move to a larger scale
+        unsigned grown = __ballot_sync(0xFFFFFFFFu, row_here && r == from && held > 0 && exp > old);
+        while (grown) {
+          const int k = __ffs(grown) - 1;
+          grown &= grown - 1;
+          const int n_old = __shfl_sync(0xFFFFFFFFu, held, k);
+          const float ratio = power(__shfl_sync(0xFFFFFFFFu, old - exp, k));
+          uint8_t* rows = cache + (__shfl_sync(0xFFFFFFFFu, row_r, k) - n_old) * D;
+          for (int i = lane; i < n_old * (D / 8); i += 32) {
+            const uint2 u = __ldcg(reinterpret_cast<const uint2*>(rows) + i);
+            uint32_t o[2];
+            const uint32_t in[2] = {u.x, u.y};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 lo = e4m3x2_to_f32x2((uint16_t)in[e]), hi = e4m3x2_to_f32x2((uint16_t)(in[e] >> 16));
+              o[e] = f32x2_to_e4m3x2(lo.x * ratio, lo.y * ratio) |
+                     ((uint32_t)f32x2_to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
+            }
+            reinterpret_cast<uint2*>(rows)[i] = make_uint2(o[0], o[1]);
+          }
+        }
+      };
+      float x[IT][8];
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        widen(kr[i], x[i]);
+        float rs = 1.0f;
+        if (w.kw) {
+          float sq = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sq = fmaf(x[i][e], x[i][e], sq);
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+          rs = rsqrtf(sq * (1.0f / D) + w.eps);
+        }
+        const float* cs = s_cs[(base + i * TPW + sub) & 31] + 8 * c;   // (anything in rows that are none)
+        const float4 a = *reinterpret_cast<const float4*>(cs), b = *reinterpret_cast<const float4*>(cs + 4);
+        const float cc[4] = {a.x, a.z, b.x, b.z}, ss[4] = {a.y, a.w, b.y, b.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int lo = HALVES ? e : 2 * e, hi = HALVES ? 4 + e : 2 * e + 1;
+          const float u = x[i][lo] * rs * gk[lo], v = x[i][hi] * rs * gk[hi];
+          x[i][lo] = u * cc[e] - v * ss[e];
+          x[i][hi] = u * ss[e] + v * cc[e];
+        }
+        if (!(live >> (i * TPW + sub) & 1u)) {        // (its cos and sin may be anything)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+        }
+      }
+      put(x, p.k, p.ks, old_k);
+#pragma unroll
+      for (int i = 0; i < IT; ++i) widen(vr[i], x[i]);
+      base += n;
+      // (the next turn's values, or the next head's, on their way)
+      if (base < end) fetch(h, base);
+      else if (h + step < p.Hkv) fetch(h + step, f);
+      put(x, p.v, p.vs, old_v);
+    }
   }
 }
 
@@ -547,7 +869,7 @@ cudaError_t pages_prepare() {
 cudaError_t launch_pages_table(const PagesDev& p, float* table, const double* theta, cudaStream_t s) {
   Thetas th{};
   for (int i = 0; i < p.D / 2; ++i) th.t[i] = theta[i];
-  const size_t n = (size_t)p.W * p.P * (p.D / 2);
+  const size_t n = (size_t)p.max_pos * (p.D / 2);
   const size_t blocks = (n + 255) / 256;
   k_pages_table<<<(unsigned)(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(table, th, p.D / 2, n);
   return cudaGetLastError();
@@ -578,19 +900,39 @@ cudaError_t launch_pages_release(const PagesDev& p, const int32_t* rows, int B, 
 
 cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_count, cudaStream_t s) {
   const int tpw = 32 / (p.D / 8), blocks = (w.T + tpw - 1) / tpw;
-  const int htot = p.Hq + 2 * p.Hkv, most = (htot + kWriteWarps - 1) / kWriteWarps;
+  const int htot = p.Hq + (p.ks ? 0 : 2 * p.Hkv), most = (htot + kWriteWarps - 1) / kWriteWarps;
   // few tokens: split the heads over blocks too, until every SM has the eight
   // blocks that it holds
   int split = (8 * sm_count + blocks - 1) / blocks;
   split = split < 1 ? 1 : (split > most ? most : split);
   const dim3 grid((unsigned)blocks, (unsigned)split), block(kWriteWarps * 32);
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, s, p, w); };
+  // a kernel by head size, pairing and positions
+  auto pick = [&](auto e4m3, auto kv) {
+    constexpr bool E = decltype(e4m3)::value, KV = decltype(kv)::value;
+    if (p.D == 128) {
+      if (p.pt) return p.halves ? go(k_pages_write<128, E, true, true, KV>) : go(k_pages_write<128, E, false, true, KV>);
+      return p.halves ? go(k_pages_write<128, E, true, false, KV>) : go(k_pages_write<128, E, false, false, KV>);
+    }
+    if (p.pt) return p.halves ? go(k_pages_write<64, E, true, true, KV>) : go(k_pages_write<64, E, false, true, KV>);
+    return p.halves ? go(k_pages_write<64, E, true, false, KV>) : go(k_pages_write<64, E, false, false, KV>);
+  };
+  if (!p.ks) return p.e4m3 ? pick(std::true_type{}, std::true_type{}) : pick(std::false_type{}, std::true_type{});
+  // keys and values first; the queries' kernel starts beside that one
+  const int groups = (w.T + KVRING_SCALE_BLOCK - 1) / KVRING_SCALE_BLOCK, each = (p.Hkv + kBlockWarps - 1) / kBlockWarps;
+  int heads = (3 * sm_count + groups - 1) / groups;   // three blocks to an SM, as long as that leaves a head per warp
+  heads = heads < 1 ? 1 : (heads > each ? each : heads);
+  const dim3 bgrid((unsigned)groups, (unsigned)heads), bblock(kBlockWarps * 32);
+  auto put = [&](auto kernel) { return launch_pdl(kernel, bgrid, bblock, 0, s, p, w); };
+  cudaError_t e;
   if (p.D == 128) {
-    if (p.e4m3) return p.halves ? go(k_pages_write<128, true, true>) : go(k_pages_write<128, true, false>);
-    return p.halves ? go(k_pages_write<128, false, true>) : go(k_pages_write<128, false, false>);
+    if (p.pt) e = p.halves ? put(k_pages_write_blocks<128, true, true>) : put(k_pages_write_blocks<128, false, true>);
+    else e = p.halves ? put(k_pages_write_blocks<128, true, false>) : put(k_pages_write_blocks<128, false, false>);
+  } else {
+    if (p.pt) e = p.halves ? put(k_pages_write_blocks<64, true, true>) : put(k_pages_write_blocks<64, false, true>);
+    else e = p.halves ? put(k_pages_write_blocks<64, true, false>) : put(k_pages_write_blocks<64, false, false>);
   }
-  if (p.e4m3) return p.halves ? go(k_pages_write<64, true, true>) : go(k_pages_write<64, true, false>);
-  return p.halves ? go(k_pages_write<64, false, true>) : go(k_pages_write<64, false, false>);
+  return e == cudaSuccess ? pick(std::false_type{}, std::false_type{}) : e;
 }
 
 }  // namespace kvr

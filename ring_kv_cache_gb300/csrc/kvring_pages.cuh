@@ -51,7 +51,7 @@ struct PagesDev {
   int32_t* klen;          // [R]
   int32_t* pos;           // [max_tokens]
   int32_t* slots;         // [max_tokens]
-  const float* table;     // [W * P][D/2][2] fp32 (cos, sin)
+  const float* table;     // [max_pos][D/2][2] fp32 (cos, sin)
   float* part_o;          // [2 * kPagedMaxCtas][kPartRows x D] attention partials, laid out by the kernel
   float* part_ml;         // [2 * kPagedMaxCtas][kPartRows][2] their running maxima and sums
   int32_t* tickets;       // [2 * kPagedMaxCtas] arrivals per split unit (0 between calls)
@@ -61,7 +61,16 @@ struct PagesDev {
   int Hq, Hkv, D, L, P, logP, num_pages, R, W, max_tokens;
   int e4m3;               // cache type
   int halves;             // rotation pairs (i, i + d/2)
+  uint8_t* ks;            // [L][num_pages][Hkv][P/16] exponents of block scales (NULL: scales per head)
+  uint8_t* vs;
+  int pt, py;             // 3-D RoPE: pairs of t and y (pt = 0: 1-D)
+  int max_pos;            // rows of `table`: W * P, or as many as coordinates go
 };
+
+// Exponents (biased by 127) that a block's scale may have; others are read as the
+// nearest of these.  With both products' range in mind: a weight 2^(score + e - m)
+// that counts is never lost beside the normaliser's 2^(score - m).
+constexpr int kMinExp = 127 - 40, kMaxExp = 127 + 40;
 
 struct PagedAttn {
   const uint16_t* q;
@@ -93,6 +102,7 @@ struct PagesWrite {
   long long q_stride, k_stride, v_stride;
   const uint16_t *qw, *kw;
   uint16_t* q_out;
+  const int32_t* coords;  // [T][3], 3-D RoPE
   float eps;
   int T, layer;
 };

@@ -43,7 +43,18 @@ bool config_ok(const kvring_pages_config* c) {
   if (c->max_tokens < 1 || c->max_tokens > (1 << 20)) return false;
   if (c->cache_dtype != KVRING_CACHE_E4M3 && c->cache_dtype != KVRING_CACHE_BF16) return false;
   if (c->rope_pairing != KVRING_ROPE_ADJACENT && c->rope_pairing != KVRING_ROPE_HALVES) return false;
-  if (c->reserved != 0) return false;
+  if (c->reserved != 0 || c->reserved2 != 0) return false;
+  if (c->scale_block != 0 && (c->scale_block != KVRING_SCALE_BLOCK || c->cache_dtype != KVRING_CACHE_E4M3)) return false;
+  if (c->rope_pairs_t == 0) {
+    if (c->rope_pairs_y != 0 || c->rope_frequencies != 0 || c->max_position != 0) return false;
+  } else {
+    const int pairs = c->head_dim / 2;
+    if (c->rope_pairs_t < 1 || c->rope_pairs_t > pairs || c->rope_pairs_y < 0 ||
+        c->rope_pairs_y > pairs - c->rope_pairs_t)
+      return false;
+    if (c->rope_frequencies != KVRING_FREQ_SECTION && c->rope_frequencies != KVRING_FREQ_HEAD) return false;
+    if (c->max_position < 0 || c->max_position > 1 << 24) return false;
+  }
   return c->rope_base > 0.0 && std::isfinite(c->rope_base);
 }
 
@@ -51,7 +62,13 @@ struct Plan {
   kvring_pages_layout pub;
   size_t table, part_o, part_ml, tickets, few_o, few_ml;
   size_t cache_bytes;   // of K, and of V
+  size_t scale_bytes;   // block scales of K, and of V
 };
+
+// Rows of the cos/sin table.
+int table_rows(const kvring_pages_config* c) {
+  return c->rope_pairs_t && c->max_position ? c->max_position : c->max_pages_per_request * c->page_size;
+}
 
 Plan plan_for(const kvring_pages_config* c) {
   Plan p{};
@@ -76,7 +93,10 @@ Plan plan_for(const kvring_pages_config* c) {
   p.pub.step_lengths = take(R * 4);
   p.pub.positions = take(T * 4);
   p.pub.slots = take(T * 4);
-  p.table = take(W * c->page_size * D * 4);
+  p.scale_bytes = c->scale_block ? p.cache_bytes / D / KVRING_SCALE_BLOCK : 0;
+  p.pub.k_block_scales = take(p.scale_bytes);
+  p.pub.v_block_scales = take(p.scale_bytes);
+  p.table = take((size_t)table_rows(c) * D * 4);
   p.part_o = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * D * 4);
   p.part_ml = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * 8);
   p.tickets = take((size_t)3 * kvr::kPagedMaxCtas * 4);   // two per CTA, and one of the other kernel
@@ -215,8 +235,19 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   d.max_tokens = cfg->max_tokens;
   d.e4m3 = cfg->cache_dtype == KVRING_CACHE_E4M3;
   d.halves = cfg->rope_pairing == KVRING_ROPE_HALVES;
+  d.ks = cfg->scale_block ? b + p.pub.k_block_scales : nullptr;
+  d.vs = cfg->scale_block ? b + p.pub.v_block_scales : nullptr;
+  d.pt = cfg->rope_pairs_t;
+  d.py = cfg->rope_pairs_y;
+  d.max_pos = table_rows(cfg);
   double theta[64] = {};
-  for (int i = 0; i < d.D / 2; ++i) theta[i] = std::pow(cfg->rope_base, (-2.0 * i) / (double)d.D);
+  const bool sections = d.pt && cfg->rope_frequencies == KVRING_FREQ_SECTION;
+  const int ends[4] = {0, d.pt, d.pt + d.py, d.D / 2};
+  for (int i = 0; i < d.D / 2; ++i) {
+    const int ax = i < ends[1] ? 0 : (i < ends[2] ? 1 : 2);
+    const double rate = sections ? (double)(i - ends[ax]) / (ends[ax + 1] - ends[ax]) : 2.0 * i / (double)d.D;
+    theta[i] = std::pow(cfg->rope_base, -rate);
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   kvring_status st = KVRING_OK;
   if (!make_pool_map(&h->tmK, d.k, cfg) || !make_pool_map(&h->tmV, d.v, cfg)) st = KVRING_ERR_UNSUPPORTED;
@@ -225,6 +256,8 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   if (st == KVRING_OK) st = cuda_status(kvr::paged_chunk_prepare());
   // everything but the caches and the workspace's partial rows starts as zeros
   if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(b + p.pub.scales, 0, p.table - p.pub.scales, s));
+  if (st == KVRING_OK && p.scale_bytes) st = cuda_status(cudaMemsetAsync(d.ks, 127, p.scale_bytes, s));
+  if (st == KVRING_OK && p.scale_bytes) st = cuda_status(cudaMemsetAsync(d.vs, 127, p.scale_bytes, s));
   if (st == KVRING_OK) st = cuda_status(cudaMemsetAsync(d.tickets, 0, 3 * kvr::kPagedMaxCtas * 4, s));
   if (st == KVRING_OK)
     st = recorded(h, s, [&] {
@@ -279,7 +312,7 @@ kvring_status kvring_pages_set_scales(kvring_pages_t* h, int32_t layer, const fl
   if (!h || !sk || !sv || !aligned(sk, 4) || !aligned(sv, 4) || layer < 0 || layer >= h->cfg.num_layers ||
       !on_device(h))
     return KVRING_ERR_INVALID_ARG;
-  if (!h->dev.e4m3) return KVRING_ERR_UNSUPPORTED;   // a bf16 cache has no scales
+  if (!h->dev.e4m3 || h->dev.ks) return KVRING_ERR_UNSUPPORTED;   // no scales, or one per block
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return recorded(h, s, [&] { return kvr::launch_pages_scales(h->dev, layer, sk, sv, s); });
 }
@@ -319,9 +352,9 @@ kvring_status kvring_pages_release(kvring_pages_t* h, const int32_t* rows, int32
   return recorded(h, s, [&] { return kvr::launch_pages_release(h->dev, rows, n, s); });
 }
 
-kvring_status kvring_pages_write(kvring_pages_t* h, int32_t layer, const void* q, const void* k, const void* v,
-                                 int64_t qs, int64_t ks, int64_t vs, const void* qw, const void* kw, float eps,
-                                 void* q_out, int32_t n, void* stream) {
+static kvring_status write_tokens(kvring_pages_t* h, int32_t layer, const void* q, const void* k, const void* v,
+                                  int64_t qs, int64_t ks, int64_t vs, const void* qw, const void* kw, float eps,
+                                  const int32_t* coords, void* q_out, int32_t n, void* stream) {
   if (!h || !q || !k || !v || !q_out || layer < 0 || layer >= h->cfg.num_layers || n < 1 || !on_device(h))
     return KVRING_ERR_INVALID_ARG;
   const void* ptrs[6] = {q, k, v, q_out, qw, kw};
@@ -338,6 +371,10 @@ kvring_status kvring_pages_write(kvring_pages_t* h, int32_t layer, const void* q
   if (overlap(q_out, out_bytes, q, bytes(qs, qrow)) || overlap(q_out, out_bytes, k, bytes(ks, krow)) ||
       overlap(q_out, out_bytes, v, bytes(vs, krow)) || overlap(q_out, out_bytes, h->buf, h->bytes))
     return KVRING_ERR_INVALID_ARG;
+  const size_t coord_bytes = (size_t)n * 12;
+  if (coords && (!aligned(coords, 4) || overlap(q_out, out_bytes, coords, coord_bytes) ||
+                 overlap(coords, coord_bytes, h->buf, h->bytes)))
+    return KVRING_ERR_INVALID_ARG;
   for (const void* p : {qw, kw})
     if (p && overlap(q_out, out_bytes, p, (size_t)D * 2)) return KVRING_ERR_INVALID_ARG;
   kvr::PagesWrite w{};
@@ -350,11 +387,26 @@ kvring_status kvring_pages_write(kvring_pages_t* h, int32_t layer, const void* q
   w.qw = static_cast<const uint16_t*>(qw);
   w.kw = static_cast<const uint16_t*>(kw);
   w.q_out = static_cast<uint16_t*>(q_out);
+  w.coords = coords;
   w.eps = eps;
   w.T = n;
   w.layer = layer;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return recorded(h, s, [&] { return kvr::launch_pages_write(h->dev, w, h->sm_count, s); }, q_out, out_bytes);
+}
+
+kvring_status kvring_pages_write(kvring_pages_t* h, int32_t layer, const void* q, const void* k, const void* v,
+                                 int64_t qs, int64_t ks, int64_t vs, const void* qw, const void* kw, float eps,
+                                 void* q_out, int32_t n, void* stream) {
+  if (h && h->dev.pt) return KVRING_ERR_INVALID_ARG;   // its tokens have coordinates
+  return write_tokens(h, layer, q, k, v, qs, ks, vs, qw, kw, eps, nullptr, q_out, n, stream);
+}
+
+kvring_status kvring_pages_write_3d(kvring_pages_t* h, int32_t layer, const void* q, const void* k, const void* v,
+                                    int64_t qs, int64_t ks, int64_t vs, const void* qw, const void* kw, float eps,
+                                    const int32_t* coords, void* q_out, int32_t n, void* stream) {
+  if (!h || !h->dev.pt || !coords) return KVRING_ERR_INVALID_ARG;
+  return write_tokens(h, layer, q, k, v, qs, ks, vs, qw, kw, eps, coords, q_out, n, stream);
 }
 
 kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const void* q, int64_t q_stride, void* out,
@@ -366,6 +418,7 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   if (q_stride % 8 || q_stride < row || q_stride > (int64_t)1 << 40) return KVRING_ERR_INVALID_ARG;
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return KVRING_ERR_INVALID_ARG;
   if (!(scale >= 0.f) || !std::isfinite(scale)) return KVRING_ERR_INVALID_ARG;
+  if (h->dev.ks) return KVRING_ERR_UNSUPPORTED;
   if (n > h->cfg.max_tokens) return KVRING_ERR_CAPACITY;
   const size_t out_bytes = (size_t)n * row * 2;
   if (overlap(out, out_bytes, q, ((size_t)(n - 1) * q_stride + row) * 2) || overlap(out, out_bytes, h->buf, h->bytes))
