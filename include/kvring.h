@@ -568,7 +568,9 @@ kvring_status kvring_pages_write_3d(kvring_pages_t* pages, int32_t layer, const 
  * out: bf16 [num_tokens][Hq][d], q with a token stride (elements, a multiple
  * of 8), out contiguous, overlapping neither q nor the cache's buffer; rows
  * past the plan's tokens stay as they were.  Scores, softmax statistics and sums are fp32; probabilities
- * are rounded once, to bf16 (f16 over an E4M3 cache).  Finite cached values
+ * are rounded once, to bf16 (f16 over an E4M3 cache; over block scales what is
+ * rounded is the probability with its value's scale).  Block scales' bytes outside 87 .. 167
+ * (2^-40 .. 2^40) are read as the nearest of these.  Finite cached values
  * of any size give finite results at any length.  Cached tokens that
  * a query's mask hides do not affect it, whatever they hold. */
 kvring_status kvring_pages_attention(kvring_pages_t* pages, int32_t layer, const void* q, int64_t q_stride, void* out,

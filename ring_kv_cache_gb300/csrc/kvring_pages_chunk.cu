@@ -79,8 +79,13 @@ constexpr int kUnitQueue = 4;
 constexpr int kUnitCost = 3;      // (8,192 causal queries: 404, 372, 372, 380 us with 2, 3, 4, 6)
 constexpr int kTileBits = 40;     // of the sums over requests: places in the low bits, units above
 constexpr int kChunkSmem = 232448;
+// Tiles whose blocks' exponents are kept.  When a tile's are written its slot for
+// keys is free, so the helpers are through the entry kRaws before, whose slot the
+// MMAs of the entry kSlots before that have left: the values of the tile seven
+// before (four at d = 128) have been multiplied, so its exponents have been read.
+constexpr int kExpTiles = 8;
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool BLK>
 struct ChunkLayout {
   // Streams: a row group's 128 rows, and at d = 64 half of each tile's tokens.
   static constexpr int kHalves = D == 128 ? 1 : 2;               // token halves of a tile
@@ -114,9 +119,11 @@ struct ChunkLayout {
   static constexpr int kKV = kQBufs * 2 * kQGroup;
   static constexpr int kRawAt = kKV + kSlots * kSlot;
   static constexpr int kMisc = kRawAt + kRaws * kRaw;
-  static constexpr int kMiscBytes = 1536;
+  static constexpr int kMiscBytes = BLK ? 1280 : 1536;
   static constexpr int kMl = kMisc + kMiscBytes;                 // float2 [2][2][halves][128]: their maxima and sums, by unit parity
-  static constexpr int kBytes = 1024 + kMl + (kHalves > 1 ? 4 * kHalves * kTile * 8 : 0);
+  // float [tiles][3][8], a tile in turn: 2^e_k, e_v and 2^-e_v of its blocks (BLK)
+  static constexpr int kExp = kMl + (kHalves > 1 ? 4 * kHalves * kTile * 8 : 0);
+  static constexpr int kBytes = 1024 + kExp + (BLK ? kExpTiles * 96 : 0);
   static_assert(kBytes <= kChunkSmem, "fits one CTA per SM");
 };
 
@@ -135,6 +142,7 @@ struct Unit {
   int end;         // no unit follows
   int table;       // the request's row of the block tables
   int wild;        // a masked tile holds values that are not finite
+  int n0;          // this CTA's tiles before it
 };
 
 // The words of the step that describe a request, and what follows from them.
@@ -169,6 +177,7 @@ struct ChunkMisc {
   // its MMAs have read it; and the E4M3 tiles before they are widened
   uint64_t full[11], ready[11], empty[11], raw_full[6], raw_empty[6];
   uint64_t p_half[4];   // the first half of the probabilities there
+  uint64_t exps[kExpTiles];   // a tile's exponents there
   uint64_t done[2], grp[2];
   unsigned long long ws[24];
   long long total, base;
@@ -177,7 +186,7 @@ struct ChunkMisc {
   uint32_t tmem;
   int b0, rt0, parts, abort, last[2];
 };
-static_assert(sizeof(ChunkMisc) <= ChunkLayout<128, false>::kMiscBytes, "misc block");
+static_assert(sizeof(ChunkMisc) <= ChunkLayout<128, true, true>::kMiscBytes, "misc block");
 
 // The key tiles [t0, t0 + nt) of row tile rt.
 __device__ __forceinline__ int chunk_tiles(const PagedAttn& a, const ChunkReq& r, int rt, int tpu, int* t0) {
@@ -249,11 +258,17 @@ __device__ __forceinline__ uint32_t clean_values(uint4* at, uint4 w, bool inside
   return b;
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
+// BLK: an E4M3 cache with a scale 2^e per 16 tokens.  As in the kernel for few rows the
+// values' exponent joins the score before the maximum is taken, and the
+// normaliser's sums of 16 take it back; a block's 16 columns have a factor and an offset
+// of their own in the multiply-add that makes the exponentials' arguments, so a tile
+// costs eight factors, offsets and sums more per row.
+template <int D, bool E4M3, bool BLK>
+__global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PagesDev p, const PagedAttn a) {
-  using L = ChunkLayout<D, E4M3>;
+  static_assert(E4M3 || !BLK, "block scales are of E4M3 codes");
+  using L = ChunkLayout<D, E4M3, BLK>;
   // Probabilities handed over in two parts, so that the first half's product
   // runs beside the second half's exponentials: over an E4M3 cache a gain (757
   // queries over 5,788 tokens, 40 heads: 86.4 -> 83.8 us), over a bf16 one, whose
@@ -300,6 +315,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
       mbar_init(bar(misc->raw_full[i]), 1);
       mbar_init(bar(misc->raw_empty[i]), kHelpThreads);
     }
+    for (int i = 0; i < kExpTiles; ++i) mbar_init(bar(misc->exps[i]), 1);
     for (int g = 0; g < 2; ++g) mbar_init(bar(misc->done[g]), 1);
     for (int g = 0; g < 2; ++g) mbar_init(bar(misc->grp[g]), kTile * L::kHalves);
     misc->abort = 0;
@@ -441,6 +457,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         u.h = h;
         u.table = rq.row;
         u.wild = 0;
+        u.n0 = n >> 1;
         u.whole = ntile == nt;
         // the CTAs whose ranges hold a tile of this unit (the owner of place x
         // is the last CTA whose range starts at or before x)
@@ -461,9 +478,30 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         return __ldcg(tab + (tok >> p.logP));
       };
       int page = page_of(tile0);
+      // The exponents of K and V of 16 tokens, block `lane` of the tile (K in the low
+      // byte): their page is that of the piece they lie in.
+      auto exps_of = [&](int t, int pg) -> int {
+        const int id = __shfl_sync(0xFFFFFFFFu, pg, (lane & 7) * KVRING_SCALE_BLOCK / box_rows);
+        if (lane >= 8 || id < 0 || id >= p.num_pages) return 127 | 127 << 8;
+        const int tok = (t * kTile + lane * KVRING_SCALE_BLOCK) & (p.P - 1);
+        const size_t at = ((size_t)(layer0 + id) * p.Hkv + h << p.logP >> 4) + (tok >> 4);
+        return __ldcg(p.ks + at) | (int)__ldcg(p.vs + at) << 8;
+      };
+      int page2 = -2, exps = 0, exps2 = 0;
+      if constexpr (BLK) {
+        page2 = ntile > 1 ? page_of(tile0 + 1) : -2;
+        exps = exps_of(tile0, page);
+      }
       for (int j = 0; j < ntile && !stopped; ++j) {
         const int tile = tile0 + j;
-        const int ahead = j + 1 < ntile ? page_of(tile + 1) : -2;
+        int ahead;
+        if constexpr (BLK) {
+          ahead = page2;
+          page2 = j + 2 < ntile ? page_of(tile + 2) : -2;
+          if (j + 1 < ntile) exps2 = exps_of(tile + 1, ahead);
+        } else {
+          ahead = j + 1 < ntile ? page_of(tile + 1) : -2;
+        }
         const unsigned there = __ballot_sync(0xFFFFFFFFu, page != -2);
         const int row0 = (tile * kTile + lane * box_rows) & (p.P - 1);
         const bool ok = page >= 0 && page < p.num_pages;
@@ -480,6 +518,22 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kBoxes; ++c)
               tma_load_3d(dst + c * L::kAtom, kv ? &tmV : &tmK, c * 64, row0, c2, bar(full[s]));
+          }
+          if constexpr (BLK) {
+            if (kv == 0) {
+              const int at = (n >> 1) % kExpTiles;
+              if (lane < 8) {
+                auto within = [](int e) { return e < kMinExp ? kMinExp : (e > kMaxExp ? kMaxExp : e); };
+                const int ek = within(exps & 0xFF), ev = within(exps >> 8);
+                float* e = reinterpret_cast<float*>(sm + L::kExp) + 24 * at + lane;
+                e[0] = __uint_as_float((uint32_t)ek << 23);
+                e[8] = (float)(ev - 127);
+                e[16] = __uint_as_float((uint32_t)(254 - ev) << 23);
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(misc->exps[at]));
+              exps = exps2;
+            }
           }
           // the queries behind the unit's first keys: their place is free
           // once the previous unit's last scores have been computed
@@ -775,7 +829,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
           query_factor(em, up, down);
           // (at least 1e-30: a factor that underflows would make NaN of what is
           // masked, and such scores are all alike anyway)
-          f_row = fmaxf(f_row * __ldcg(sc + u.h) * up, 1e-30f);
+          f_row = fmaxf(f_row * (BLK ? 1.0f : __ldcg(sc + u.h)) * up, 1e-30f);
 #pragma unroll
           for (int i = 0; i < D / 8 / L::kHalves; ++i) {
             uint4* at = chunk_at(half * (D / 8 / L::kHalves) + i);
@@ -807,7 +861,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         float moff = kShift<E4M3>;
         // (over an E4M3 cache a score is at most 4 x 448 x 128 < 2^18, so the
         // factor tells)
-        bool huge = E4M3 && __any_sync(0xFFFFFFFFu, f_row > 8.0f);
+        bool huge = E4M3 && !BLK && __any_sync(0xFFFFFFFFu, f_row > 8.0f);
         // 32 scores to probabilities, as pairs of the 16-bit type; their sum
         // is added to lsum
         auto probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, float moff, float2& lsum) {
@@ -834,6 +888,30 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             for (int i = 0; i < w; ++i) e[i] = __fadd2_rn(e[i], e[i + w]);
           lsum = __fadd2_rn(lsum, e[0]);
         };
+        // The same for 32 columns of two blocks: factors, offsets and weights of
+        // their sums are theirs (e: their place among the tile's exponents).
+        auto block_probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, const float* e, float moff, bool direct,
+                                       float2& lsum) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float fr = direct ? 1.0f : f_row * e[b], mo = direct ? moff : moff + e[8 + b], over = e[16 + b];
+            const float2 fr2 = make_float2(fr, fr), mo2 = make_float2(mo, mo);
+            float2 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 x = __ffma2_rn(
+                  make_float2(__uint_as_float(s32[16 * b + 2 * i]), __uint_as_float(s32[16 * b + 2 * i + 1])), fr2, mo2);
+              y[i] = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pw[8 * b + i] = f32x2_to_f16x2(y[i].x, y[i].y);
+#pragma unroll
+            for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+              for (int i = 0; i < w; ++i) y[i] = __fadd2_rn(y[i], y[i + w]);
+            lsum = __ffma2_rn(y[0], make_float2(over, over), lsum);
+          }
+        };
         // Scores so large that factor x score, not rounded in the fused
         // multiply-add, may lie well above its rounding, the maximum: the
         // differences of the rounded ones (for the largest exactly 0) go in
@@ -844,6 +922,14 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < L::kCols; ++c)
             sr[c] = __float_as_uint((__fmul_rn(__uint_as_float(sr[c]), f_row) - mu) * over);
+          moff = kShift<E4M3>;
+        };
+        // (over blocks: the whole difference, to be taken as it is)
+        auto block_differences = [&](uint32_t (&sr)[L::kCols], const float* e) {
+          const float mu = m_run == -INFINITY ? 0.f : m_run;
+#pragma unroll
+          for (int c = 0; c < L::kCols; ++c)
+            sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), f_row * e[c >> 4]), e[8 + (c >> 4)]) - mu);
           moff = kShift<E4M3>;
         };
         int j = 0;
@@ -870,6 +956,27 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
                 if (!(seen >> c & 1u)) sr[32 * w + c] = __float_as_uint(-INFINITY);
             }
           }
+          const int n = u.n0 + j;
+          const float* exps = reinterpret_cast<const float*>(sm + L::kExp) + 24 * (n % kExpTiles) + half * (L::kCols / 16);
+          float tmax;
+          if constexpr (BLK) {
+            wait(misc->exps[n % kExpTiles], (n / kExpTiles) & 1);
+            __syncwarp();
+            float w[L::kCols / 16];
+#pragma unroll
+            for (int b = 0; b < L::kCols / 16; ++b) {
+              auto v = [&](int i) { return __uint_as_float(sr[16 * b + i]); };
+              const float a0 = fmax3(v(0), v(1), v(2)), a1 = fmax3(v(3), v(4), v(5)), a2 = fmax3(v(6), v(7), v(8));
+              const float a3 = fmax3(v(9), v(10), v(11)), a4 = fmax3(v(12), v(13), v(14));
+              // (rounded as block_differences does, so that the largest gives exactly 0)
+              w[b] = __fadd_rn(__fmul_rn(fmax3(fmax3(a0, a1, a2), fmax3(a3, a4, v(15)), a4), f_row * exps[b]), exps[8 + b]);
+            }
+#pragma unroll
+            for (int k = L::kCols / 32; k > 0; k >>= 1)
+#pragma unroll
+              for (int i = 0; i < k; ++i) w[i] = fmaxf(w[i], w[i + k]);
+            tmax = w[0];
+          } else {
           float mx[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
@@ -878,7 +985,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               mx[k] = fmax3(mx[k], __uint_as_float(sr[16 * i + 2 * k]), __uint_as_float(sr[16 * i + 2 * k + 1]));
-          const float tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
+          tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
+          }
           const bool need = tmax > m_run + kRaise || (m_run == -INFINITY && tmax > m_run);
           const float m_new = need ? tmax : m_run;
           if (__any_sync(0xFFFFFFFFu, need)) {
@@ -903,17 +1011,26 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
             }
             m_run = m_new;
             moff = kShift<E4M3> - (m_run == -INFINITY ? 0.f : m_run);
-            if constexpr (!slow && !E4M3) {
+            if constexpr (!slow && (!E4M3 || BLK)) {
               huge = __any_sync(0xFFFFFFFFu, fabsf(moff) > 0x1p20f);
-              if (huge) differences(sr);
+              if (huge) {
+                if constexpr (BLK) block_differences(sr, exps);
+                else differences(sr);
+              }
             }
           }
-          if constexpr (slow) differences(sr);
+          if constexpr (slow) {
+            if constexpr (BLK) block_differences(sr, exps);
+            else differences(sr);
+          }
           float2 lsum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < L::kCols / 32; ++c) {
             uint32_t pw[16];
-            probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
+            if constexpr (BLK)
+              block_probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, exps + 2 * c, moff, slow || huge, lsum);
+            else
+              probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
             tmem_st16(tS + 16 * c, pw);
             if constexpr (kTwo) {
               if (c + 1 == L::kCols / 64) {
@@ -957,7 +1074,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
         tc_fence_after();
         constexpr int kC = D / 32 / L::kHalves;        // 32-column groups of this thread
         const int c_first = half * kC;
-        const float scale_v = E4M3 ? __ldcg(sc + p.Hkv + u.h) : 1.0f;
+        const float scale_v = E4M3 && !BLK ? __ldcg(sc + p.Hkv + u.h) : 1.0f;
         const float inv = ell > 0.f || ell != ell ? scale_v / ell : 0.f;   // (of the row, both halves)
         const bool whole = u.whole;
         const int first = u.first, last = u.last;
@@ -1114,41 +1231,47 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3>::kThreads, 1)
     atomicOr(reinterpret_cast<unsigned*>(p.state + PST_ERROR), KVRING_PAGES_ERR_TIMEOUT);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool BLK>
 cudaError_t prepare_one() {
-  using L = ChunkLayout<D, E4M3>;
+  using L = ChunkLayout<D, E4M3, BLK>;
   // the register split must fit what a block is launched with, or the warps
   // that ask for more would wait for ever
   cudaFuncAttributes at;
-  const cudaError_t e = cudaFuncGetAttributes(&at, k_paged_chunk<D, E4M3>);
+  const cudaError_t e = cudaFuncGetAttributes(&at, k_paged_chunk<D, E4M3, BLK>);
   if (e != cudaSuccess) return e;
   if (L::kRegsSoft && at.numRegs * L::kThreads <
                           L::kRegsSoft * L::kSoftThreads + L::kRegsRest * (L::kThreads - L::kSoftThreads))
     return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(k_paged_chunk<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ChunkLayout<D, E4M3>::kBytes);
+  return cudaFuncSetAttribute(k_paged_chunk<D, E4M3, BLK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ChunkLayout<D, E4M3, BLK>::kBytes);
 }
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool BLK>
 cudaError_t go(const PagesDev& p, const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV,
                const PagedAttn& a, cudaStream_t s) {
-  return launch_pdl(k_paged_chunk<D, E4M3>, dim3((unsigned)a.ctas), dim3(ChunkLayout<D, E4M3>::kThreads),
-                    ChunkLayout<D, E4M3>::kBytes, s, *tmQ, *tmK, *tmV, p, a);
+  return launch_pdl(k_paged_chunk<D, E4M3, BLK>, dim3((unsigned)a.ctas), dim3(ChunkLayout<D, E4M3, BLK>::kThreads),
+                    ChunkLayout<D, E4M3, BLK>::kBytes, s, *tmQ, *tmK, *tmV, p, a);
 }
 
 }  // namespace
 
 cudaError_t paged_chunk_prepare() {
-  cudaError_t e = prepare_one<128, true>();
-  if (e == cudaSuccess) e = prepare_one<128, false>();
-  if (e == cudaSuccess) e = prepare_one<64, true>();
-  if (e == cudaSuccess) e = prepare_one<64, false>();
+  cudaError_t e = prepare_one<128, true, false>();
+  if (e == cudaSuccess) e = prepare_one<128, true, true>();
+  if (e == cudaSuccess) e = prepare_one<128, false, false>();
+  if (e == cudaSuccess) e = prepare_one<64, true, false>();
+  if (e == cudaSuccess) e = prepare_one<64, true, true>();
+  if (e == cudaSuccess) e = prepare_one<64, false, false>();
   return e;
 }
 
 cudaError_t launch_paged_chunk(const PagesDev& p, const CUtensorMap* tmQ, const CUtensorMap* tmK,
                                const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s) {
-  if (p.D == 128) return p.e4m3 ? go<128, true>(p, tmQ, tmK, tmV, a, s) : go<128, false>(p, tmQ, tmK, tmV, a, s);
-  return p.e4m3 ? go<64, true>(p, tmQ, tmK, tmV, a, s) : go<64, false>(p, tmQ, tmK, tmV, a, s);
+  if (p.D == 128) {
+    if (p.ks) return go<128, true, true>(p, tmQ, tmK, tmV, a, s);
+    return p.e4m3 ? go<128, true, false>(p, tmQ, tmK, tmV, a, s) : go<128, false, false>(p, tmQ, tmK, tmV, a, s);
+  }
+  if (p.ks) return go<64, true, true>(p, tmQ, tmK, tmV, a, s);
+  return p.e4m3 ? go<64, true, false>(p, tmQ, tmK, tmV, a, s) : go<64, false, false>(p, tmQ, tmK, tmV, a, s);
 }
 
 }  // namespace kvr

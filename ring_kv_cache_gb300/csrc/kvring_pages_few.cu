@@ -57,7 +57,7 @@ constexpr int kGroups = 8;       // groups of 16 tokens of a tile
 constexpr int kRows = kFewRows;  // query rows of a unit
 constexpr int kSmemMost = 232448;
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool BLK>
 struct FewLayout {
   // Consumer warps.  They take the 16-token groups in turn.  Eight keep up
   // with HBM over a bf16 cache; an E4M3 tile is there in half the time and
@@ -72,7 +72,8 @@ struct FewLayout {
   static constexpr int kMl = kO + kWarps * 4 * D * 4;      // float2 [warps][kRows]: their offsets and sums
   static constexpr int kRow = kMl + kWarps * kRows * 8;       // int lo, hi; float factor; pad: [kRows][4]
   static constexpr int kMisc = kRow + kRows * 16;
-  static constexpr int kFixed = kMisc + 512;
+  static constexpr int kExp = kMisc + 512;                     // uint8 [slots][16]: a tile's exponents of K and of V
+  static constexpr int kFixed = kExp + (BLK ? 16 * 16 : 0);
   static constexpr int kRoom = (kSmemMost - 1024 - kFixed) / kSlot;
   static constexpr int kSlots = kRoom > 16 ? 16 : kRoom;
   static constexpr int kBytes = 1024 + kSlots * kSlot + kFixed;
@@ -101,6 +102,8 @@ struct FewMisc {
   int abort;
   int last;
 };
+
+static_assert(sizeof(FewMisc) <= 512, "misc block");
 
 // Keeps the accumulator type of the two element types in one place.
 template <bool F16>
@@ -167,11 +170,19 @@ __device__ __forceinline__ Req make_req(const PagedAttn& a, const ReqWords& w, i
   return r;
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
+// BLK: an E4M3 cache with a scale 2^e per 16 tokens, the tokens of a warp's group.
+// The keys' goes into the group's factor.  The values' joins the score: with
+// w = s + e_v, the running maximum is that of w, p = 2^(w - m') weighs the codes, and
+// the normaliser takes p 2^-e_v = 2^(s - m').  So what the f16 probabilities
+// resolve is what a token adds to the result, whatever its block's scale, and one
+// multiplication per row and group is all it costs.  The producer reads the exponents a
+// tile ahead and puts them beside the tile's slot.
+template <int D, bool E4M3, bool BLK>
+__global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
     k_paged_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagesDev p,
                 const PagedAttn a) {
-  using L = FewLayout<D, E4M3>;
+  static_assert(E4M3 || !BLK, "block scales are of E4M3 codes");
+  using L = FewLayout<D, E4M3, BLK>;
   constexpr int kWarps = L::kWarps, kConsumers = L::kConsumers, kFewThreads = L::kThreads;
   auto sync_consumers = [] { sync_consumers_n<kConsumers>(); };
   extern __shared__ uint8_t smem_raw[];
@@ -189,7 +200,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), BLK ? 2 : 1);   // (the copies, the exponents)
       mbar_init(empty(s), kWarps);   // every consumer warp, those without a group of the tile too
     }
     misc->abort = 0;
@@ -316,8 +327,30 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         return __ldcg(tab + (tok >> p.logP));
       };
       int page = page_of(tile);
+      // The exponent of 16 tokens (lane & 7 of the tile; K, V by lane >> 3): its page is
+      // that of the piece they lie in.
+      auto exp_of = [&](int t, int pg) -> int {
+        const int piece = (lane & 7) * KVRING_SCALE_BLOCK / box_rows;
+        const int id = __shfl_sync(0xFFFFFFFFu, pg, piece);
+        if (lane >= 16 || id < 0 || id >= p.num_pages) return 127;
+        const int tok = (t * kTile + (lane & 7) * KVRING_SCALE_BLOCK) & (p.P - 1);
+        const size_t at = ((size_t)(layer0 + id) * p.Hkv + h << p.logP >> 4) + (tok >> 4);
+        return __ldcg((kv ? p.vs : p.ks) + at);
+      };
+      int page2 = -2, exp = 127, exp2 = 127;
+      if constexpr (BLK) {
+        page2 = x + 1 < ue ? page_of(tile + 1) : -2;
+        exp = exp_of(tile, page);
+      }
       for (; x < ue; ++x, ++tile, n += 2) {
-        const int ahead = x + 1 < ue ? page_of(tile + 1) : -2;
+        int ahead;
+        if constexpr (BLK) {
+          ahead = page2;
+          page2 = x + 2 < ue ? page_of(tile + 2) : -2;
+          if (x + 1 < ue) exp2 = exp_of(tile + 1, ahead);
+        } else {
+          ahead = x + 1 < ue ? page_of(tile + 1) : -2;
+        }
         const unsigned there = __ballot_sync(0xFFFFFFFFu, page != -2) & 0xFFu;
         const int row0 = (tile * kTile + box * box_rows) & (p.P - 1);
         const bool ok = page >= 0 && page < p.num_pages;
@@ -344,6 +377,14 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
             }
           }
           __syncwarp();
+          if constexpr (BLK) {
+            // (both kinds' beside the keys' slot, read with the scores)
+            const int e = exp < kMinExp ? kMinExp : (exp > kMaxExp ? kMaxExp : exp);
+            if (lane < 16) fix[L::kExp + 16 * (n % L::kSlots) + lane] = (uint8_t)e;
+            __syncwarp();
+            if (lane < 2) mbar_arrive(full((n + lane) % L::kSlots));
+            exp = exp2;
+          }
         } else {
           if (box == 0 && hf == 0) mbar_arrive_expect_tx(full(s), (uint32_t)__popc(there) * kHalves * box_bytes);
           __syncwarp();
@@ -416,7 +457,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
     const int rows = rq.nrows - r0 < kRows ? rq.nrows - r0 : kRows;
     // ---- queries and row data into shared memory
     sync_consumers();                                    // the previous unit is done with it
-    const float scale_k = E4M3 ? __ldcg(sc + h) : 1.0f;
+    const float scale_k = E4M3 && !BLK ? __ldcg(sc + h) : 1.0f;
     for (int i = threadIdx.x; i < kRows * kChunksQ; i += kConsumers) {
       const int r = i / kChunksQ, ch = i % kChunksQ;
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
@@ -505,6 +546,14 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc_[0][e] = sc_[1][e] = 0.f;
       const uint32_t sK = sbase + s * L::kSlot;
+      float exp_k = 1.0f, exp_v = 0.f, over_v = 1.0f;    // 2^e_k, e_v, 2^-e_v of the group
+      if constexpr (BLK) {
+        const uint8_t* e = fix + L::kExp + 16 * s + group;
+        const int ev = e[8];
+        exp_k = __uint_as_float((uint32_t)e[0] << 23);
+        exp_v = (float)(ev - 127);
+        over_v = __uint_as_float((uint32_t)(254 - ev) << 23);
+      }
       auto score_step = [&](int ks, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
         mma16816<E4M3>(sc_[0], qreg[ks], b0, b1);
         mma16816<E4M3>(sc_[1], qreg[ks], b2, b3);
@@ -544,7 +593,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
           pa[hr] = pa[2 + hr] = 0u;
           continue;
         }
-        const float f = fac[hr];
+        const float f = BLK ? fac[hr] * exp_k : fac[hr];
         if (masked) {
           const int4 ri = s_row[8 * hr + g];
 #pragma unroll
@@ -561,6 +610,10 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
         for (int nt = 0; nt < 2; ++nt) {
           sc_[nt][2 * hr] *= f;
           sc_[nt][2 * hr + 1] *= f;
+          if constexpr (BLK) {
+            sc_[nt][2 * hr] += exp_v;
+            sc_[nt][2 * hr + 1] += exp_v;
+          }
         }
         float mx = fmaxf(fmax3(sc_[0][2 * hr], sc_[0][2 * hr + 1], sc_[1][2 * hr]), sc_[1][2 * hr + 1]);
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
@@ -589,7 +642,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
           sum += p0 + p1;
           pa[2 * nt + hr] = pack(p0, p1);
         }
-        l_run[hr] += sum;
+        l_run[hr] += BLK ? sum * over_v : sum;
       }
       // ---- values
       wait_full();
@@ -682,7 +735,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
     }
     sync_consumers();
     const bool whole = ubase >= start && uend <= stop;
-    const float scale_v = E4M3 ? __ldcg(sc + p.Hkv + h) : 1.0f;
+    const float scale_v = E4M3 && !BLK ? __ldcg(sc + p.Hkv + h) : 1.0f;
     auto out_row = [&](int r) -> uint16_t* {
       const int row = r0 + r;
       return a.out + ((size_t)(rq.q0 + row / G) * p.Hq + h * G + row % G) * D;
@@ -795,31 +848,37 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3>::kThreads, 1)
   if (a.beside) griddep_wait();
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool BLK>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(k_paged_few<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              FewLayout<D, E4M3>::kBytes);
+  return cudaFuncSetAttribute(k_paged_few<D, E4M3, BLK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              FewLayout<D, E4M3, BLK>::kBytes);
 }
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool BLK>
 cudaError_t go(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a, cudaStream_t s) {
-  return launch_pdl(k_paged_few<D, E4M3>, dim3((unsigned)a.ctas), dim3(FewLayout<D, E4M3>::kThreads),
-                    FewLayout<D, E4M3>::kBytes, s, *tmK, *tmV, p, a);
+  return launch_pdl(k_paged_few<D, E4M3, BLK>, dim3((unsigned)a.ctas), dim3(FewLayout<D, E4M3, BLK>::kThreads),
+                    FewLayout<D, E4M3, BLK>::kBytes, s, *tmK, *tmV, p, a);
 }
 
 }  // namespace
 
 cudaError_t paged_few_prepare() {
-  cudaError_t e = prepare_one<128, true>();
-  if (e == cudaSuccess) e = prepare_one<128, false>();
-  if (e == cudaSuccess) e = prepare_one<64, true>();
-  if (e == cudaSuccess) e = prepare_one<64, false>();
+  cudaError_t e = prepare_one<128, true, false>();
+  if (e == cudaSuccess) e = prepare_one<128, true, true>();
+  if (e == cudaSuccess) e = prepare_one<128, false, false>();
+  if (e == cudaSuccess) e = prepare_one<64, true, false>();
+  if (e == cudaSuccess) e = prepare_one<64, true, true>();
+  if (e == cudaSuccess) e = prepare_one<64, false, false>();
   return e;
 }
 
 cudaError_t launch_paged_few(const PagesDev& p, const CUtensorMap* tmK, const CUtensorMap* tmV, const PagedAttn& a,
                              cudaStream_t s) {
-  if (p.D == 128) return p.e4m3 ? go<128, true>(p, tmK, tmV, a, s) : go<128, false>(p, tmK, tmV, a, s);
-  return p.e4m3 ? go<64, true>(p, tmK, tmV, a, s) : go<64, false>(p, tmK, tmV, a, s);
+  if (p.D == 128) {
+    if (p.ks) return go<128, true, true>(p, tmK, tmV, a, s);
+    return p.e4m3 ? go<128, true, false>(p, tmK, tmV, a, s) : go<128, false, false>(p, tmK, tmV, a, s);
+  }
+  if (p.ks) return go<64, true, true>(p, tmK, tmV, a, s);
+  return p.e4m3 ? go<64, true, false>(p, tmK, tmV, a, s) : go<64, false, false>(p, tmK, tmV, a, s);
 }
 
 }  // namespace kvr

@@ -418,7 +418,6 @@ kvring_status kvring_pages_attention(kvring_pages_t* h, int32_t layer, const voi
   if (q_stride % 8 || q_stride < row || q_stride > (int64_t)1 << 40) return KVRING_ERR_INVALID_ARG;
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return KVRING_ERR_INVALID_ARG;
   if (!(scale >= 0.f) || !std::isfinite(scale)) return KVRING_ERR_INVALID_ARG;
-  if (h->dev.ks) return KVRING_ERR_UNSUPPORTED;
   if (n > h->cfg.max_tokens) return KVRING_ERR_CAPACITY;
   const size_t out_bytes = (size_t)n * row * 2;
   if (overlap(out, out_bytes, q, ((size_t)(n - 1) * q_stride + row) * 2) || overlap(out, out_bytes, h->buf, h->bytes))

@@ -151,3 +151,52 @@ def check_blocks(p, s, name, want, m, slots, planned, before, scales_before, fp=
         rest = [k for k in range(first, B) if k not in off]   # places of nobody
         assert torch.equal(got[blk][:, rest], old[blk][:, rest])
     assert torch.equal(got[~touched], old[~touched]) and torch.equal(e_got[~touched], e_old[~touched])
+
+
+def cached_blocks(p, s, b, h, which):
+    """float64 (codes [total, d], scales [total]) of request b's head h."""
+    layer, n = s["layer"], s["total"][b]
+    c, sc = [getattr(p, which + x)(layer).view(torch.uint8) for x in ("_cache", "_scales")]
+    ids = p.tables[b, :-(-n // p.P)].long()
+    codes = c[ids, h].view(torch.float8_e4m3fn).double().reshape(-1, p.d)[:n]
+    e = sc[ids, h].long().clamp(LOW, HIGH).repeat_interleave(B, dim=1).reshape(-1)[:n]
+    return codes, torch.exp2(e.double() - 127)
+
+
+def attention_blocks_64(p, s, q=None, causal=True, window=0, scale=None):
+    """(out, bound) in 64 bits, NaN in rows past the plan's tokens."""
+    q = s["q"] if q is None else q
+    sm = scale or 1 / math.sqrt(p.d)
+    G = p.Hq // p.Hkv
+    out = torch.full(q.shape, math.nan, dtype=F64, device="cuda")
+    tol = torch.zeros_like(out)
+    at = 0
+    for b, (t, n) in enumerate(zip(s["total"], s["new"])):
+        if n == 0:
+            continue
+        i, j = torch.arange(t - n, t, device="cuda")[:, None], torch.arange(t, device="cuda")[None]
+        see = torch.ones((n, t), dtype=torch.bool, device="cuda")
+        if causal:
+            see = (j <= i) & ((j > i - window) if window else True)
+        for h in range(p.Hq):
+            (kc, ks), (vc, vs) = cached_blocks(p, s, b, h // G, "k"), cached_blocks(p, s, b, h // G, "v")
+            k, v = kc * ks[:, None], vc * vs[:, None]
+            x = q[at:at + n, h].double()
+            w = torch.softmax((x @ k.T * sm).masked_fill(~see, -math.inf), -1)
+            vv = torch.where(see.any(0)[:, None], v, 0.0)
+            o, a = w @ vv, w @ vv.abs()
+            # a score's fp32 sum over d products (2^-22 each with the tensor
+            # cores' truncation), the query's f16 form (2^-25 of its row's
+            # largest), and the three roundings of score + exponent - maximum,
+            # an exponent being 40 at most
+            size = (x.abs() @ k.abs().T).masked_fill(~see, 0).amax(-1, keepdim=True) * sm
+            delta = size * p.d * 2.0 ** -22 + 2.0 ** -17
+            delta = delta + 2.0 ** -24 * x.abs().amax(-1, keepdim=True) * k.abs().sum(-1).amax() * sm
+            # probabilities to f16: 2^-11, or 2^-25 of a number whose largest, the
+            # weight with the value's scale, is 2^7; the result to bf16; fp32 sums
+            lost = 2.0 ** -11 + 2 * delta + 2.0 ** -22 * math.sqrt(t)
+            most = (w * vs).amax(-1, keepdim=True) * 448
+            tol[at:at + n, h] = 2.0 ** -8 * o.abs() + lost * a * 1.01 + t * 2.0 ** -32 * most + 1e-30
+            out[at:at + n, h] = o
+        at += n
+    return out, tol
