@@ -101,9 +101,11 @@ struct ChunkLayout {
   static constexpr int kHelpers = E4M3 ? 4 : kSoftWarps + 4 - kWarpHelp;   // warps
   static constexpr int kThreads = 32 * (kWarpHelp + kHelpers);
   // Registers per thread after the split (0: none): the sum over all threads
-  // stays that of the launch (128 x 512, 96 x 640, 80 x 768).
-  static constexpr int kRegsSoft = D == 128 ? (E4M3 ? 176 : 0) : (E4M3 ? 96 : 104);
-  static constexpr int kRegsRest = D == 128 ? (E4M3 ? 80 : 0) : (E4M3 ? 48 : 64);
+  // stays that of the launch (128 x 512, 96 x 640, 80 x 768).  Over blocks each of
+  // a tile's eight has a factor and an exponent in registers beside the scores (4,096
+  // queries behind 12,288: 730 us with 176, 699 with 192, 719 with 200).
+  static constexpr int kRegsSoft = D == 128 ? (E4M3 ? (BLK ? 192 : 176) : 0) : (E4M3 ? 96 : 104);
+  static constexpr int kRegsRest = D == 128 ? (E4M3 ? (BLK ? 64 : 80) : 0) : (E4M3 ? 48 : 64);
   static constexpr int kAtom = kTile * 128;                      // 128 rows x 64 16-bit columns
   static constexpr int kAtoms = D / 64;
   static constexpr int kQGroup = kAtoms * kAtom;
@@ -262,7 +264,11 @@ __device__ __forceinline__ uint32_t clean_values(uint4* at, uint4 w, bool inside
 // values' exponent joins the score before the maximum is taken, and the
 // normaliser's sums of 16 take it back; a block's 16 columns have a factor and an offset
 // of their own in the multiply-add that makes the exponentials' arguments, so a tile
-// costs eight factors, offsets and sums more per row.
+// costs eight factors, offsets and sums more per row: a frame of 757 over 5,788 tokens 94 us, 4,096
+// queries behind 12,288 699 us (with scales per head and the same scores 93 and 688).
+// Measured and slower: the codes brought to one exponent per tile by the helpers
+// (779 us: the groups wait for them), factors read again from shared memory where they
+// are used (812 us), pairs of them kept (832 us).
 template <int D, bool E4M3, bool BLK>
 __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -478,16 +484,21 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
         return __ldcg(tab + (tok >> p.logP));
       };
       int page = page_of(tile0);
-      // The exponents of K and V of 16 tokens, block `lane` of the tile (K in the low
-      // byte): their page is that of the piece they lie in.
-      auto exps_of = [&](int t, int pg) -> int {
+      // The exponents of K and V of 16 tokens, block `lane` of the tile: their page is that
+      // of the piece they lie in.  Asked for a tile ahead, and not looked at before (any
+      // use would wait here).
+      struct Exps {
+        int k, v;
+      };
+      auto exps_of = [&](int t, int pg) -> Exps {
         const int id = __shfl_sync(0xFFFFFFFFu, pg, (lane & 7) * KVRING_SCALE_BLOCK / box_rows);
-        if (lane >= 8 || id < 0 || id >= p.num_pages) return 127 | 127 << 8;
+        if (lane >= 8 || id < 0 || id >= p.num_pages) return Exps{127, 127};
         const int tok = (t * kTile + lane * KVRING_SCALE_BLOCK) & (p.P - 1);
         const size_t at = ((size_t)(layer0 + id) * p.Hkv + h << p.logP >> 4) + (tok >> 4);
-        return __ldcg(p.ks + at) | (int)__ldcg(p.vs + at) << 8;
+        return Exps{__ldcg(p.ks + at), __ldcg(p.vs + at)};
       };
-      int page2 = -2, exps = 0, exps2 = 0;
+      int page2 = -2;
+      Exps exps{}, exps2{};
       if constexpr (BLK) {
         page2 = ntile > 1 ? page_of(tile0 + 1) : -2;
         exps = exps_of(tile0, page);
@@ -524,7 +535,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
               const int at = (n >> 1) % kExpTiles;
               if (lane < 8) {
                 auto within = [](int e) { return e < kMinExp ? kMinExp : (e > kMaxExp ? kMaxExp : e); };
-                const int ek = within(exps & 0xFF), ev = within(exps >> 8);
+                const int ek = within(exps.k), ev = within(exps.v);
                 float* e = reinterpret_cast<float*>(sm + L::kExp) + 24 * at + lane;
                 e[0] = __uint_as_float((uint32_t)ek << 23);
                 e[8] = (float)(ev - 127);
@@ -890,11 +901,11 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
         };
         // The same for 32 columns of two blocks: factors, offsets and weights of
         // their sums are theirs (e: their place among the tile's exponents).
-        auto block_probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, const float* e, float moff, bool direct,
-                                       float2& lsum) {
+        auto block_probabilities = [&](const uint32_t (&s32)[32], uint32_t* pw, const float* fr_b, const float* ev_b,
+                                       const float* over_b, float moff, float2& lsum) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float fr = direct ? 1.0f : f_row * e[b], mo = direct ? moff : moff + e[8 + b], over = e[16 + b];
+            const float fr = fr_b[b], mo = moff + ev_b[b], over = over_b[b];
             const float2 fr2 = make_float2(fr, fr), mo2 = make_float2(mo, mo);
             float2 y[8];
 #pragma unroll
@@ -924,17 +935,35 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
             sr[c] = __float_as_uint((__fmul_rn(__uint_as_float(sr[c]), f_row) - mu) * over);
           moff = kShift<E4M3>;
         };
-        // (over blocks: the whole difference, to be taken as it is)
-        auto block_differences = [&](uint32_t (&sr)[L::kCols], const float* e) {
+        constexpr int kBlk = L::kCols / 16;   // blocks of a stream's tile
+        // (over blocks: the whole difference, for a factor of 1 and no offset)
+        auto block_differences = [&](uint32_t (&sr)[L::kCols], float (&fr)[kBlk], float (&ev)[kBlk]) {
           const float mu = m_run == -INFINITY ? 0.f : m_run;
 #pragma unroll
           for (int c = 0; c < L::kCols; ++c)
-            sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), f_row * e[c >> 4]), e[8 + (c >> 4)]) - mu);
+            sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), fr[c >> 4]), ev[c >> 4]) - mu);
+#pragma unroll
+          for (int b = 0; b < kBlk; ++b) {
+            fr[b] = 1.0f;
+            ev[b] = 0.f;
+          }
           moff = kShift<E4M3>;
         };
         int j = 0;
         auto tile = [&](auto slow_tag) {
           constexpr bool slow = decltype(slow_tag)::value;
+          float fr[kBlk], ev[kBlk];   // factors and exponents of the tile's blocks (BLK)
+          const int n = u.n0 + j;
+          const float* exps = reinterpret_cast<const float*>(sm + L::kExp) + 24 * (n % kExpTiles) + half * kBlk;
+          if constexpr (BLK) {        // (there long before the scores are)
+            wait(misc->exps[n % kExpTiles], (n / kExpTiles) & 1);
+#pragma unroll
+            for (int b = 0; b < kBlk; b += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(exps + b), v4 = *reinterpret_cast<const float4*>(exps + 8 + b);
+              fr[b] = f_row * k4.x, fr[b + 1] = f_row * k4.y, fr[b + 2] = f_row * k4.z, fr[b + 3] = f_row * k4.w;
+              ev[b] = v4.x, ev[b + 1] = v4.y, ev[b + 2] = v4.z, ev[b + 3] = v4.w;
+            }
+          }
           wait(misc->s_full[st], nt_done & 1);
           __syncwarp();
           tc_fence_after();
@@ -956,23 +985,19 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
                 if (!(seen >> c & 1u)) sr[32 * w + c] = __float_as_uint(-INFINITY);
             }
           }
-          const int n = u.n0 + j;
-          const float* exps = reinterpret_cast<const float*>(sm + L::kExp) + 24 * (n % kExpTiles) + half * (L::kCols / 16);
           float tmax;
           if constexpr (BLK) {
-            wait(misc->exps[n % kExpTiles], (n / kExpTiles) & 1);
-            __syncwarp();
-            float w[L::kCols / 16];
+            float w[kBlk];
 #pragma unroll
-            for (int b = 0; b < L::kCols / 16; ++b) {
+            for (int b = 0; b < kBlk; ++b) {
               auto v = [&](int i) { return __uint_as_float(sr[16 * b + i]); };
               const float a0 = fmax3(v(0), v(1), v(2)), a1 = fmax3(v(3), v(4), v(5)), a2 = fmax3(v(6), v(7), v(8));
               const float a3 = fmax3(v(9), v(10), v(11)), a4 = fmax3(v(12), v(13), v(14));
               // (rounded as block_differences does, so that the largest gives exactly 0)
-              w[b] = __fadd_rn(__fmul_rn(fmax3(fmax3(a0, a1, a2), fmax3(a3, a4, v(15)), a4), f_row * exps[b]), exps[8 + b]);
+              w[b] = __fadd_rn(__fmul_rn(fmax3(fmax3(a0, a1, a2), fmax3(a3, a4, v(15)), a4), fr[b]), ev[b]);
             }
 #pragma unroll
-            for (int k = L::kCols / 32; k > 0; k >>= 1)
+            for (int k = kBlk / 2; k > 0; k >>= 1)
 #pragma unroll
               for (int i = 0; i < k; ++i) w[i] = fmaxf(w[i], w[i + k]);
             tmax = w[0];
@@ -1014,13 +1039,13 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
             if constexpr (!slow && (!E4M3 || BLK)) {
               huge = __any_sync(0xFFFFFFFFu, fabsf(moff) > 0x1p20f);
               if (huge) {
-                if constexpr (BLK) block_differences(sr, exps);
+                if constexpr (BLK) block_differences(sr, fr, ev);
                 else differences(sr);
               }
             }
           }
           if constexpr (slow) {
-            if constexpr (BLK) block_differences(sr, exps);
+            if constexpr (BLK) block_differences(sr, fr, ev);
             else differences(sr);
           }
           float2 lsum = make_float2(0.f, 0.f);
@@ -1028,7 +1053,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
           for (int c = 0; c < L::kCols / 32; ++c) {
             uint32_t pw[16];
             if constexpr (BLK)
-              block_probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, exps + 2 * c, moff, slow || huge, lsum);
+              block_probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, fr + 2 * c, ev + 2 * c, exps + 16 + 2 * c,
+                                  moff, lsum);
             else
               probabilities(*reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c), pw, moff, lsum);
             tmem_st16(tS + 16 * c, pw);

@@ -57,6 +57,11 @@ constexpr int kGroups = 8;       // groups of 16 tokens of a tile
 constexpr int kRows = kFewRows;  // query rows of a unit
 constexpr int kSmemMost = 232448;
 
+// Block scales: the producer fetches the exponents of kExpBatch tiles at once, a lane
+// per block.  When it writes those of tile T and the next three, slots of tile T are
+// free, so every warp is through with the tiles up to T - 8 (16 slots are 8 tiles),
+// and of the tiles T - 16 .. T - 13, whose places these take, nothing is read any more.
+constexpr int kExpTiles = 16, kExpBatch = 4;
 template <int D, bool E4M3, bool BLK>
 struct FewLayout {
   // Consumer warps.  They take the 16-token groups in turn.  Eight keep up
@@ -72,8 +77,8 @@ struct FewLayout {
   static constexpr int kMl = kO + kWarps * 4 * D * 4;      // float2 [warps][kRows]: their offsets and sums
   static constexpr int kRow = kMl + kWarps * kRows * 8;       // int lo, hi; float factor; pad: [kRows][4]
   static constexpr int kMisc = kRow + kRows * 16;
-  static constexpr int kExp = kMisc + 512;                     // uint8 [slots][16]: a tile's exponents of K and of V
-  static constexpr int kFixed = kExp + (BLK ? 16 * 16 : 0);
+  static constexpr int kExp = kMisc + 512;                     // uint8 [kExpTiles][16]: a tile's exponents of K and of V
+  static constexpr int kFixed = kExp + (BLK ? kExpTiles * 16 : 0);
   static constexpr int kRoom = (kSmemMost - 1024 - kFixed) / kSlot;
   static constexpr int kSlots = kRoom > 16 ? 16 : kRoom;
   static constexpr int kBytes = 1024 + kSlots * kSlot + kFixed;
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(full(s), BLK ? 2 : 1);   // (the copies, the exponents)
+      mbar_init(full(s), 1);
       mbar_init(empty(s), kWarps);   // every consumer warp, those without a group of the tile too
     }
     misc->abort = 0;
@@ -327,29 +332,37 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
         return __ldcg(tab + (tok >> p.logP));
       };
       int page = page_of(tile);
-      // The exponent of 16 tokens (lane & 7 of the tile; K, V by lane >> 3): its page is
-      // that of the piece they lie in.
-      auto exp_of = [&](int t, int pg) -> int {
-        const int piece = (lane & 7) * KVRING_SCALE_BLOCK / box_rows;
-        const int id = __shfl_sync(0xFFFFFFFFu, pg, piece);
-        if (lane >= 16 || id < 0 || id >= p.num_pages) return 127;
-        const int tok = (t * kTile + (lane & 7) * KVRING_SCALE_BLOCK) & (p.P - 1);
-        const size_t at = ((size_t)(layer0 + id) * p.Hkv + h << p.logP >> 4) + (tok >> 4);
-        return __ldcg((kv ? p.vs : p.ks) + at);
+      // A lane's block of the four tiles from t on: its page, and with that its exponents,
+      // each asked for a batch ahead of its use (one at a time per tile, they held
+      // the producer: 128 decoding requests of 64 columns 298 us).
+      struct Exps {
+        int k, v;
       };
-      int page2 = -2, exp = 127, exp2 = 127;
+      const int tile_end = rq.t0 + (int)(ue - ubase);
+      auto block_tok = [&](int t) { return (t + (lane >> 3)) * kTile + (lane & 7) * KVRING_SCALE_BLOCK; };
+      auto block_page = [&](int t) -> int {
+        const int tok = block_tok(t);
+        if (t + (lane >> 3) >= tile_end || tok >= rq.hi || tok + KVRING_SCALE_BLOCK <= rq.lo) return -2;
+        return __ldcg(tab + (tok >> p.logP));
+      };
+      auto block_exps = [&](int t, int id) -> Exps {
+        if (id < 0 || id >= p.num_pages) return Exps{127, 127};
+        const size_t at = ((size_t)(layer0 + id) * p.Hkv + h << p.logP >> 4) + ((block_tok(t) & (p.P - 1)) >> 4);
+        return Exps{__ldcg(p.ks + at), __ldcg(p.vs + at)};
+      };
+      int next_page = -2, batch = 0;
+      Exps exps{}, next_exps{};
       if constexpr (BLK) {
-        page2 = x + 1 < ue ? page_of(tile + 1) : -2;
-        exp = exp_of(tile, page);
+        next_exps = block_exps(tile, block_page(tile));
+        next_page = block_page(tile + kExpBatch);
       }
-      for (; x < ue; ++x, ++tile, n += 2) {
-        int ahead;
-        if constexpr (BLK) {
-          ahead = page2;
-          page2 = x + 2 < ue ? page_of(tile + 2) : -2;
-          if (x + 1 < ue) exp2 = exp_of(tile + 1, ahead);
-        } else {
-          ahead = x + 1 < ue ? page_of(tile + 1) : -2;
+      for (; x < ue; ++x, ++tile, n += 2, ++batch) {
+        const int ahead = x + 1 < ue ? page_of(tile + 1) : -2;
+        const bool fresh = BLK && batch % kExpBatch == 0;
+        if (fresh) {
+          exps = next_exps;
+          next_exps = block_exps(tile + kExpBatch, next_page);
+          next_page = block_page(tile + 2 * kExpBatch);
         }
         const unsigned there = __ballot_sync(0xFFFFFFFFu, page != -2) & 0xFFu;
         const int row0 = (tile * kTile + box * box_rows) & (p.P - 1);
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int sk = (n + k) % L::kSlots;
-              mbar_arrive_expect_tx(full(sk), (uint32_t)__popc(there) * box_bytes);
+              if (!fresh) mbar_arrive_expect_tx(full(sk), (uint32_t)__popc(there) * box_bytes);
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 if (there >> i & 1)
@@ -377,13 +390,19 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
             }
           }
           __syncwarp();
-          if constexpr (BLK) {
-            // (both kinds' beside the keys' slot, read with the scores)
-            const int e = exp < kMinExp ? kMinExp : (exp > kMaxExp ? kMaxExp : exp);
-            if (lane < 16) fix[L::kExp + 16 * (n % L::kSlots) + lane] = (uint8_t)e;
+          if (fresh) {
+            // (behind the copies: they may still be on their way)
+            auto within = [](int e) { return (uint8_t)(e < kMinExp ? kMinExp : (e > kMaxExp ? kMaxExp : e)); };
+            uint8_t* e = fix + L::kExp + 16 * (((n >> 1) + (lane >> 3)) % kExpTiles) + (lane & 7);
+            e[0] = within(exps.k);
+            e[8] = within(exps.v);
             __syncwarp();
-            if (lane < 2) mbar_arrive(full((n + lane) % L::kSlots));
-            exp = exp2;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mbar_arrive_expect_tx(full((n + k) % L::kSlots), (uint32_t)__popc(there) * box_bytes);
+            }
+            __syncwarp();
           }
         } else {
           if (box == 0 && hf == 0) mbar_arrive_expect_tx(full(s), (uint32_t)__popc(there) * kHalves * box_bytes);
@@ -409,6 +428,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
   // and the rest of the range runs through on whatever the slots hold, so
   // every barrier is still met and every ticket still drawn.
   int s = 0;                                            // the next slot, and its barrier's phase
+  int ntiles = 0;                                       // tiles so far
   uint32_t phase = 0;
   auto wait_full = [&]() {
     if (!mbar_try_wait(full(s), phase) && !*abort) mbar_wait_bounded(full(s), phase, abort, a.wait_ns);
@@ -529,7 +549,8 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
     const int all_hi = s_row[0].y, all_lo = s_row[rows - 1].x;
 
     int group = warp;                                    // this warp's group of the tile, if below kGroups
-    for (int tile = rq.t0 + (int)(x - ubase); x < ue; ++x, ++tile, group += group < kGroups ? kWarps - kGroups : -kGroups) {
+    for (int tile = rq.t0 + (int)(x - ubase); x < ue;
+         ++x, ++tile, ++ntiles, group += group < kGroups ? kWarps - kGroups : -kGroups) {
       const int tok0 = tile * kTile + group * 16;        // this warp's tokens
       // ---- scores
       wait_full();
@@ -548,7 +569,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
       const uint32_t sK = sbase + s * L::kSlot;
       float exp_k = 1.0f, exp_v = 0.f, over_v = 1.0f;    // 2^e_k, e_v, 2^-e_v of the group
       if constexpr (BLK) {
-        const uint8_t* e = fix + L::kExp + 16 * s + group;
+        const uint8_t* e = fix + L::kExp + 16 * (ntiles % kExpTiles) + group;
         const int ev = e[8];
         exp_k = __uint_as_float((uint32_t)e[0] << 23);
         exp_v = (float)(ev - 127);
