@@ -385,16 +385,14 @@ constexpr int kWriteWarps = 4;
 constexpr int kWriteBatch = 4;
 
 // AXES: 3-D positions: each pair's cos and sin from the row of its own coordinate,
-// once per token.  KV false: the queries alone, beside the kernel that writes blocks
-// with scales: it starts when that one has seen its predecessors done, and waits
-// for it at the end.
+// once per token.  KV false: the queries alone, of the kernel that writes blocks with
+// scales.  bx: the block of tokens.
 template <int D, bool E4M3, bool HALVES, bool AXES, bool KV>
-__global__ void __launch_bounds__(kWriteWarps * 32, 8)
-    k_pages_write(const PagesDev p, const PagesWrite w) {
+__device__ __forceinline__ void write_tokens(const PagesDev& p, const PagesWrite& w, const int bx) {
   constexpr int LPR = D / 8, TPW = 32 / LPR;
   const int lane = threadIdx.x & 31, c = lane % LPR;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);   // (uniform, and known to be)
-  const int t = blockIdx.x * TPW + lane / LPR;
+  const int t = bx * TPW + lane / LPR;
   const int e0 = HALVES ? 4 * c : 8 * c;            // the lane's first 4 values
   const int e1 = HALVES ? D / 2 + 4 * c : 8 * c + 4;
   const bool mine = t < w.T;
@@ -437,7 +435,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
       inv_v = __ldcg(inv + p.Hkv + h);
     }
   };
-  if constexpr (KV) griddep_wait();
+  griddep_wait();
   griddep_launch_dependents();
   // Everything that depends on nothing else is asked for at once; only the
   // cos/sin row waits, for the position.  Key/value heads are dealt out from
@@ -460,10 +458,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
   const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // bf16 ones
   const uint4 gq = w.qw ? load(w.qw) : one, gk = w.kw ? load(w.kw) : one;
   tokens = tokens < w.T ? tokens : w.T;
-  if (blockIdx.x * TPW >= tokens) {
-    if constexpr (!KV) griddep_wait();
-    return;
-  }
+  if (bx * TPW >= tokens) return;
   bool valid = t < tokens;
   if (!valid) {
     slot = -1;
@@ -562,10 +557,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
       if (valid) store_bf16(q_out + h * D, x);
     }
   }
-  if constexpr (!KV) {
-    griddep_wait();
-    return;
-  }
+  if constexpr (!KV) return;
   if (hk0 >= p.Hkv) return;
   matrix(gk);
   // row of (page, head 0, offset) in the layer's caches; heads are P rows apart
@@ -582,6 +574,11 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
   }
 }
 
+template <int D, bool E4M3, bool HALVES, bool AXES>
+__global__ void __launch_bounds__(kWriteWarps * 32, 8) k_pages_write(const PagesDev p, const PagesWrite w) {
+  write_tokens<D, E4M3, HALVES, AXES, true>(p, w, blockIdx.x);
+}
+
 // ------------------------------------------- write into blocks with scales ---
 // Keys and values into an E4M3 cache whose blocks of 16 tokens have a scale
 // 2^e each:  e = least with amax <= 448 2^e over the step's tokens of the block,
@@ -592,17 +589,24 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8)
 // subnormals): a scale of amax / 448 itself would use the top binade better by less than
 // one step in 16 and round every code again with each growth.
 //
-// Bound by HBM as the write above.  A warp takes the tokens of a block that are
-// new (a run: the step's tokens with consecutive slots of one block) and a
-// head: all its values are in registers when their size is known, so each is
-// read once, and a block's codes leave as whole lines.  Runs begin anywhere, so a
+// Bound by HBM as the write above, and by issue.  A run is the step's tokens with
+// consecutive slots of one block; four warps hold a run's rows, four each, and a
+// head's keys and values, until their sizes are known, so each value is read
+// once, and a block's codes leave as whole lines.  Runs begin anywhere, so a
 // group of 16 consecutive tokens of the step owns those that begin in it: up to
 // 16 runs (single tokens) and up to 31 tokens, of which the first 16 and a last
 // run of up to 16 make two turns at most (mostly one).  Sizes of rows are
-// exchanged through shared memory, a lane per row: segmented maximum over the
-// runs, the exponent, and back by shuffles.  cos/sin rows of the group's tokens lie in
-// shared memory for all heads of the block's four warps.
-constexpr int kBlockWarps = 4;
+// exchanged through shared memory, one barrier per turn and head; every warp takes the
+// maximum over the runs by shuffles, a lane per row of keys and of values.
+// cos/sin rows of the group's tokens lie in shared memory for the block's heads.  Blocks that
+// take the queries (the write's code above) lie between those of keys and values.
+// Measured (GB300): 16,384 tokens, 32/8 heads x 128, 377 MB: 70.7 us, 5.3 TB/s; 757 tokens of
+// 40 heads 12.8 us, 48 single tokens of 10 heads, half of whose blocks move to larger
+// scales, 3.3 us.  (A warp for a whole run, 64 values a thread and 168 registers:
+// 80, 16.2 and 7.2 us; queries by warps of that shape as well 111, 19.0 and 7.6 us.)
+constexpr int kBlockWarps = kWriteWarps;
+constexpr int kBlocksPerSm = 7;   // (16,384 tokens: 82, 75.7, 70.7, 69.9 us with 5, 6, 7, 8; nine tokens best with fewer)
+constexpr int kBlockHeads = 2;    // of a block of keys and values (77 us, 78 with four, 82 with one, all at six blocks)
 
 __device__ __forceinline__ int block_exponent(float amax) {
   const uint32_t b = __float_as_uint(amax);
@@ -612,20 +616,31 @@ __device__ __forceinline__ int block_exponent(float amax) {
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // 2^e
 
 template <int D, bool HALVES, bool AXES>
-__global__ void __launch_bounds__(kBlockWarps * 32, 3) k_pages_write_blocks(const PagesDev p, const PagesWrite w) {
-  constexpr int LPR = D / 8, TPW = 32 / LPR, IT = 16 / TPW;
+__global__ void __launch_bounds__(kBlockWarps * 32, kBlocksPerSm) k_pages_write_blocks(const PagesDev p, const PagesWrite w) {
   constexpr int B = KVRING_SCALE_BLOCK;
+  // Blocks of queries and of keys and values in turn, as many of the former as 16
+  // tokens take, so that the one's arithmetic runs beside the other's copies.
+  constexpr int kQueries = B / (32 / (D / 8));
+  const int per = w.kv_blocks + kQueries, group = blockIdx.x / per, unit = blockIdx.x % per;
+  if (unit >= w.kv_blocks) {
+    write_tokens<D, false, HALVES, AXES, false>(p, w, group * kQueries + unit - w.kv_blocks);
+    return;
+  }
   static_assert(B == 16, "a turn is one block");
+  constexpr int LPR = D / 8, TPW = 32 / LPR;         // lanes of a row, rows of a warp's access
+  constexpr int RPW = B / kBlockWarps, IT = RPW / TPW;   // rows of a warp, accesses for them
+  constexpr int kOld = 15 * 16 / kBlockWarps;        // a warp's share of what blocks may have held before
   __shared__ __align__(16) float s_cs[32][D];        // cos, sin of the window's tokens
-  __shared__ float s_max[kBlockWarps][16];
+  __shared__ float s_max[2][2][B];                   // sizes of rows, of keys and values, two turns in turn
+  __shared__ uint32_t s_old[kBlockWarps][kOld];      // rows of the layer's cache to be rounded again
+  __shared__ uint8_t s_run[kBlockWarps][kOld];       // and the first row of the run that they are of
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
   const int e0 = HALVES ? 4 * c : 8 * c, e1 = HALVES ? D / 2 + 4 * c : 8 * c + 4;
-  const int step = kBlockWarps * gridDim.y, h0 = blockIdx.y * kBlockWarps + warp;
   griddep_wait();
   griddep_launch_dependents();
   // The window: lane i looks at token 16 g - 1 + i.
-  const int t_lane = blockIdx.x * B - 1 + lane;
+  const int t_lane = group * B - 1 + lane;
   int tokens = __ldcg(p.state + PST_TOKENS);
   int slot = t_lane >= 0 && t_lane < w.T ? __ldcg(p.slots + t_lane) : -1;
   tokens = tokens < w.T ? tokens : w.T;
@@ -678,26 +693,29 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 3) k_pages_write_blocks(cons
   };
   // The rows of a turn, `base` its first lane: whole runs, at most 16.
   auto rows_of = [&](int base) { return end - base > 16 ? last - base : end - base; };
+  const int row0 = warp * RPW + sub;                 // this lane's rows of a turn: row0 + i * TPW
   uint4 kr[IT], vr[IT];
   auto fetch = [&](int h, int base) {
     const unsigned live = (store_mask >> base) & ((1u << rows_of(base)) - 1);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-      const int r = i * TPW + sub;
+      const int r = row0 + i * TPW;
       kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
       if (live >> r & 1u) {
-        const long long t = (long long)blockIdx.x * B - 1 + base + r;
+        const long long t = (long long)group * B - 1 + base + r;
         kr[i] = load(w.k + t * w.k_stride + h * D);
         vr[i] = load(w.v + t * w.v_stride + h * D);
       }
     }
   };
-  if (h0 < p.Hkv) fetch(h0, f);
+  int h = unit * gridDim.y + blockIdx.y, base = f;
+  const int step = w.kv_blocks * gridDim.y;
+  if (h < p.Hkv) fetch(h, base);
   {
-    constexpr int kPer = 32 / kBlockWarps, kPart = D / 64;   // rows of a warp, pairs of a lane
-    float2 v[kPer][kPart];
+    constexpr int kRows = 32 / kBlockWarps, kPart = D / 64;   // rows of a warp, pairs of a lane
+    float2 v[kRows][kPart];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < kRows; ++j) {
       const int i = f + j * kBlockWarps + warp;
       const int xyz[3] = {__shfl_sync(0xFFFFFFFFu, at[0], i & 31), __shfl_sync(0xFFFFFFFFu, at[1], i & 31),
                           __shfl_sync(0xFFFFFFFFu, at[2], i & 31)};
@@ -709,7 +727,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 3) k_pages_write_blocks(cons
       }
     }
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < kRows; ++j) {
       const int i = f + j * kBlockWarps + warp;
       if (i < end) {
 #pragma unroll
@@ -717,7 +735,6 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 3) k_pages_write_blocks(cons
       }
     }
   }
-  __syncthreads();
   float gk[8];
   if (w.kw) {
     widen(load(w.kw), gk);
@@ -725,133 +742,187 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 3) k_pages_write_blocks(cons
 #pragma unroll
     for (int e = 0; e < 8; ++e) gk[e] = 1.0f;
   }
-  const long long page_lane = member ? slot >> p.logP : 0;
-  // rows of the cache [layer][page][head][offset], of this lane's token at head 0
-  const size_t row_lane = (((size_t)w.layer * p.num_pages + page_lane) * p.Hkv << p.logP) + (slot & (p.P - 1));
-  for (int h = h0; h < p.Hkv; h += step) {
-    int base = f;
-    while (base < end) {
-      const int n = rows_of(base);
-      const unsigned here = (members >> base) & ((1u << n) - 1);
-      const unsigned firsts = (lead >> base) & here, live = (store_mask >> base) & here;
-      // Lane r < 16: row r of the turn, its run's first row and the row behind its last.
-      const int r = lane & 15;
-      const size_t row_r = __shfl_sync(0xFFFFFFFFu, row_lane, (base + r) & 31) + ((size_t)h << p.logP);
-      const int slot_r = __shfl_sync(0xFFFFFFFFu, slot, (base + r) & 31);
-      const unsigned upto = firsts & ((2u << r) - 1), behind = (firsts | ~here) & ~((2u << r) - 1);
-      const int from = upto ? 31 - __clz(upto) : 0;
-      const int to = __ffs(behind) - 1;              // (here has at most 16 bits: there is one)
-      const bool row_here = (here >> r & 1u) && lane < 16;
-      const int held = (slot_r & (B - 1)) - (r - from);   // tokens the block held before
-      const size_t block = row_r >> 4;
-      int old_k = 0, old_v = 0;
-      if (row_here && held > 0) {
-        old_k = min(max((int)__ldcg(p.ks + block), kMinExp), kMaxExp);
-        old_v = min(max((int)__ldcg(p.vs + block), kMinExp), kMaxExp);
-      }
-      auto put = [&](const float (&x)[IT][8], uint8_t* cache, uint8_t* scales, int old) {
+  const size_t layer0 = (size_t)w.layer * p.num_pages * p.Hkv << p.logP;   // the layer's first row of the cache
+  // row [page][head 0][offset] of this lane's token
+  const uint32_t row_lane =
+      member ? ((uint32_t)(slot >> p.logP) * (uint32_t)p.Hkv << p.logP) + (uint32_t)(slot & (p.P - 1)) : 0u;
+  __syncthreads();
+  auto size_of = [&](const float (&x)[8]) {          // of a row, in all its lanes
+    float m = 0.f;                                   // (a maximum passes over NaN)
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          float m = 0.f;
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+    if (m == INFINITY) {                             // of the others
+      m = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float y = fabsf(x[i][e]);
-            m = fmaxf(m, y < INFINITY ? y : 0.f);    // (not the infinite ones, nor NaN)
-          }
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-          if (c == 0) s_max[warp][i * TPW + sub] = m;
-        }
-        __syncwarp();
-        float m = s_max[warp][r];
-        __syncwarp();
-        // maximum over the run: up to its last row, then back from there
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-          const float y = __shfl_up_sync(0xFFFFFFFFu, m, o, 16);
-          if (r - o >= from) m = fmaxf(m, y);
-        }
-        m = __shfl_sync(0xFFFFFFFFu, m, to - 1, 16);
-        const int need = block_exponent(m), exp = held > 0 ? max(need, old) : need;
-        const float inv = power(127 - exp);           // 2^-(exp - 127)
-        if (row_here && r == from) scales[block] = (uint8_t)exp;
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-          const int k = i * TPW + sub;
-          const float s = __shfl_sync(0xFFFFFFFFu, inv, k);
-          const size_t row = __shfl_sync(0xFFFFFFFFu, row_r, k);
-          if (!(live >> k & 1u)) continue;
-          const uint32_t a =
-              f32x2_to_e4m3x2(x[i][0] * s, x[i][1] * s) | ((uint32_t)f32x2_to_e4m3x2(x[i][2] * s, x[i][3] * s) << 16);
-          const uint32_t b =
-              f32x2_to_e4m3x2(x[i][4] * s, x[i][5] * s) | ((uint32_t)f32x2_to_e4m3x2(x[i][6] * s, x[i][7] * s) << 16);
-          uint8_t* dst = cache + row * D;
-          if constexpr (HALVES) {
-            *reinterpret_cast<uint32_t*>(dst + e0) = a;
-            *reinterpret_cast<uint32_t*>(dst + e1) = b;
-          } else {
-            *reinterpret_cast<uint2*>(dst + e0) = make_uint2(a, b);
-          }
-        }
-        // blocks whose tokens from before move to a larger scale
-        unsigned grown = __ballot_sync(0xFFFFFFFFu, row_here && r == from && held > 0 && exp > old);
-        while (grown) {
-          const int k = __ffs(grown) - 1;
-          grown &= grown - 1;
-          const int n_old = __shfl_sync(0xFFFFFFFFu, held, k);
-          const float ratio = power(__shfl_sync(0xFFFFFFFFu, old - exp, k));
-          uint8_t* rows = cache + (__shfl_sync(0xFFFFFFFFu, row_r, k) - n_old) * D;
-          for (int i = lane; i < n_old * (D / 8); i += 32) {
-            const uint2 u = __ldcg(reinterpret_cast<const uint2*>(rows) + i);
-            uint32_t o[2];
-            const uint32_t in[2] = {u.x, u.y};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 lo = e4m3x2_to_f32x2((uint16_t)in[e]), hi = e4m3x2_to_f32x2((uint16_t)(in[e] >> 16));
-              o[e] = f32x2_to_e4m3x2(lo.x * ratio, lo.y * ratio) |
-                     ((uint32_t)f32x2_to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
-            }
-            reinterpret_cast<uint2*>(rows)[i] = make_uint2(o[0], o[1]);
-          }
-        }
-      };
-      float x[IT][8];
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        widen(kr[i], x[i]);
-        float rs = 1.0f;
-        if (w.kw) {
-          float sq = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sq = fmaf(x[i][e], x[i][e], sq);
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-          rs = rsqrtf(sq * (1.0f / D) + w.eps);
-        }
-        const float* cs = s_cs[(base + i * TPW + sub) & 31] + 8 * c;   // (anything in rows that are none)
-        const float4 a = *reinterpret_cast<const float4*>(cs), b = *reinterpret_cast<const float4*>(cs + 4);
-        const float cc[4] = {a.x, a.z, b.x, b.z}, ss[4] = {a.y, a.w, b.y, b.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int lo = HALVES ? e : 2 * e, hi = HALVES ? 4 + e : 2 * e + 1;
-          const float u = x[i][lo] * rs * gk[lo], v = x[i][hi] * rs * gk[hi];
-          x[i][lo] = u * cc[e] - v * ss[e];
-          x[i][hi] = u * ss[e] + v * cc[e];
-        }
-        if (!(live >> (i * TPW + sub) & 1u)) {        // (its cos and sin may be anything)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-        }
-      }
-      put(x, p.k, p.ks, old_k);
-#pragma unroll
-      for (int i = 0; i < IT; ++i) widen(vr[i], x[i]);
-      base += n;
-      // (the next turn's values, or the next head's, on their way)
-      if (base < end) fetch(h, base);
-      else if (h + step < p.Hkv) fetch(h + step, f);
-      put(x, p.v, p.vs, old_v);
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
     }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    return m;
+  };
+  auto size_of_bf16 = [&](uint4 v) {                 // the same of a row as it came
+    const uint32_t u[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu};
+    uint32_t m2 = __vmaxu2(__vmaxu2(u[0], u[1]), __vmaxu2(u[2], u[3]));
+    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+    if (m >= 0x7F80u) {
+      m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t y = u[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+        m = max(m, y < 0x7F80u ? y : 0u);
+      }
+    }
+    float f = __uint_as_float(m << 16);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) f = fmaxf(f, __shfl_xor_sync(0xFFFFFFFFu, f, o));
+    return f;
+  };
+  int place = 0;
+  while (h < p.Hkv) {
+    const int n = rows_of(base);
+    const unsigned here = (members >> base) & ((1u << n) - 1);
+    const unsigned firsts = (lead >> base) & here, live = (store_mask >> base) & here;
+    // Lanes r and 16 + r: row r of the turn, of keys and of values; its run's first row
+    // and the row behind its last.
+    const int r = lane & 15;
+    const uint32_t row_r = __shfl_sync(0xFFFFFFFFu, row_lane, (base + r) & 31) + ((uint32_t)h << p.logP);
+    const int slot_r = __shfl_sync(0xFFFFFFFFu, slot, (base + r) & 31);
+    const unsigned upto = firsts & ((2u << r) - 1), behind = (firsts | ~here) & ~((2u << r) - 1);
+    const int from = upto ? 31 - __clz(upto) : 0;
+    const int to = __ffs(behind) - 1;                // (here has at most 16 bits: there is one)
+    const int held = (slot_r & (B - 1)) - (r - from);   // tokens the block held before
+    uint8_t* scale = (lane < 16 ? p.ks : p.vs) + ((layer0 + row_r) >> 4);
+    int old = 0;
+    if ((here >> r & 1u) && held > 0) old = __ldcg(scale);
+    float x[IT][8];
+    uint4 values[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int k = row0 + i * TPW;
+      const float mv = size_of_bf16(vr[i]);
+      values[i] = vr[i];
+      widen(kr[i], x[i]);
+      float rs = 1.0f;
+      if (w.kw) {
+        float sq = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sq = fmaf(x[i][e], x[i][e], sq);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+        rs = rsqrtf(sq * (1.0f / D) + w.eps);
+      }
+      const float* cs = s_cs[(base + k) & 31] + 8 * c;
+      const float4 a = *reinterpret_cast<const float4*>(cs), b = *reinterpret_cast<const float4*>(cs + 4);
+      const float cc[4] = {a.x, a.z, b.x, b.z}, ss[4] = {a.y, a.w, b.y, b.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int lo = HALVES ? e : 2 * e, hi = HALVES ? 4 + e : 2 * e + 1;
+        const float u = x[i][lo] * rs * gk[lo], v = x[i][hi] * rs * gk[hi];   // (scaled first: huge rows stay finite)
+        x[i][lo] = u * cc[e] - v * ss[e];
+        x[i][hi] = u * ss[e] + v * cc[e];
+      }
+      const float mk = size_of(x[i]);                // (of anything in a row that is none)
+      if (c == 0) {
+        const bool is = live >> k & 1u;
+        s_max[place][0][k] = is ? mk : 0.f;
+        s_max[place][1][k] = is ? mv : 0.f;
+      }
+    }
+    // the next turn's values, or the next head's, on their way
+    const bool more = base + n < end;
+    const int h_next = more ? h : h + step, base_next = more ? base + n : f;
+    if (h_next < p.Hkv) fetch(h_next, base_next);
+    __syncthreads();
+    // maximum over the run: up to its last row, then back from there
+    float m = s_max[place][lane >> 4][r];
+    place ^= 1;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const float y = __shfl_up_sync(0xFFFFFFFFu, m, o, 16);
+      if (r - o >= from) m = fmaxf(m, y);
+    }
+    m = __shfl_sync(0xFFFFFFFFu, m, to - 1, 16);
+    old = min(max(old, kMinExp), kMaxExp);
+    const int need = block_exponent(m), exp = held > 0 ? max(need, old) : need;
+    const float inv = power(127 - exp);              // 2^-(exp - 127)
+    const bool first = (here >> r & 1u) && r == from;
+    if (warp == 0 && first) *scale = (uint8_t)exp;
+    uint8_t *kc = p.k + layer0 * D, *vc = p.v + layer0 * D;
+    auto store = [&](uint8_t* dst, const float (&y)[8], float s) {
+      const uint32_t a = f32x2_to_e4m3x2(y[0] * s, y[1] * s) | ((uint32_t)f32x2_to_e4m3x2(y[2] * s, y[3] * s) << 16);
+      const uint32_t b = f32x2_to_e4m3x2(y[4] * s, y[5] * s) | ((uint32_t)f32x2_to_e4m3x2(y[6] * s, y[7] * s) << 16);
+      if constexpr (HALVES) {
+        *reinterpret_cast<uint32_t*>(dst + e0) = a;
+        *reinterpret_cast<uint32_t*>(dst + e1) = b;
+      } else {
+        *reinterpret_cast<uint2*>(dst + e0) = make_uint2(a, b);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      const int k = row0 + i * TPW;
+      const float sk = __shfl_sync(0xFFFFFFFFu, inv, k), sv = __shfl_sync(0xFFFFFFFFu, inv, 16 + k);
+      const size_t row = (size_t)__shfl_sync(0xFFFFFFFFu, row_r, k) * D;
+      if (live >> k & 1u) {
+        store(kc + row, x[i], sk);
+        widen(values[i], x[i]);
+        store(vc + row, x[i], sv);
+      }
+    }
+    // Tokens from before in blocks that move to a larger scale: every warp takes
+    // every fourth row, its share in a list, so that they are on their way at once.
+    const unsigned grown = __ballot_sync(0xFFFFFFFFu, first && held > 0 && exp > old);
+    const float ratio = power(old - exp);
+    for (int kind = 0; kind < 2; ++kind) {
+      if ((grown >> (16 * kind) & 0xFFFFu) == 0) continue;
+      const int mine = grown >> (16 * kind + r) & 1u ? held : 0;   // (both halves of the warp alike)
+      int sum = mine;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, sum, o, 16);
+        if (r >= o) sum += y;
+      }
+      const int total = __shfl_sync(0xFFFFFFFFu, sum, 15);
+      __syncwarp();
+      if (lane < 16) {
+        for (int i = 0; i < mine; ++i) {
+          const int k = sum - mine + i;
+          if (k % kBlockWarps == warp) {
+            s_old[warp][k / kBlockWarps] = row_r - held + i;
+            s_run[warp][k / kBlockWarps] = (uint8_t)r;
+          }
+        }
+      }
+      __syncwarp();
+      const int count = (total - warp + kBlockWarps - 1) / kBlockWarps;
+      uint8_t* cache = kind ? vc : kc;
+      constexpr int G = 4;                           // accesses on their way
+#pragma unroll 1
+      for (int i0 = 0; i0 < count; i0 += G * TPW) {
+        uint2 v[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const int k = i0 + i * TPW + sub;
+          if (k < count) v[i] = __ldcg(reinterpret_cast<const uint2*>(cache + (size_t)s_old[warp][k] * D) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          const int k = i0 + i * TPW + sub;
+          const float s = __shfl_sync(0xFFFFFFFFu, ratio, 16 * kind + (k < count ? s_run[warp][k] : 0));
+          if (k >= count) continue;
+          uint32_t o[2];
+          const uint32_t in[2] = {v[i].x, v[i].y};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 lo = e4m3x2_to_f32x2((uint16_t)in[e]), hi = e4m3x2_to_f32x2((uint16_t)(in[e] >> 16));
+            o[e] = f32x2_to_e4m3x2(lo.x * s, lo.y * s) | ((uint32_t)f32x2_to_e4m3x2(hi.x * s, hi.y * s) << 16);
+          }
+          reinterpret_cast<uint2*>(cache + (size_t)s_old[warp][k] * D)[c] = make_uint2(o[0], o[1]);
+        }
+      }
+    }
+    h = h_next;
+    base = base_next;
   }
 }
 
@@ -898,9 +969,28 @@ cudaError_t launch_pages_release(const PagesDev& p, const int32_t* rows, int B, 
   return launch_pdl(k_pages_release, dim3(1), dim3(kPlanThreads), plan_smem(p, B), s, p, rows, B);
 }
 
+static cudaError_t launch_write_blocks(const PagesDev& p, PagesWrite w, int sm_count, cudaStream_t s) {
+  const int groups = (w.T + KVRING_SCALE_BLOCK - 1) / KVRING_SCALE_BLOCK;
+  w.kv_blocks = (p.Hkv + kBlockHeads - 1) / kBlockHeads;
+  const int blocks = groups * (w.kv_blocks + KVRING_SCALE_BLOCK / (256 / p.D));
+  // few tokens: split the heads over blocks too, until every SM has what it holds
+  const int heads = (p.Hq + kWriteWarps - 1) / kWriteWarps, most = heads > kBlockHeads ? heads : kBlockHeads;
+  int split = (kBlocksPerSm * sm_count + blocks - 1) / blocks;
+  split = split < 1 ? 1 : (split > most ? most : split);
+  const dim3 grid((unsigned)blocks, (unsigned)split), block(kBlockWarps * 32);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, s, p, w); };
+  if (p.D == 128) {
+    if (p.pt) return p.halves ? go(k_pages_write_blocks<128, true, true>) : go(k_pages_write_blocks<128, false, true>);
+    return p.halves ? go(k_pages_write_blocks<128, true, false>) : go(k_pages_write_blocks<128, false, false>);
+  }
+  if (p.pt) return p.halves ? go(k_pages_write_blocks<64, true, true>) : go(k_pages_write_blocks<64, false, true>);
+  return p.halves ? go(k_pages_write_blocks<64, true, false>) : go(k_pages_write_blocks<64, false, false>);
+}
+
 cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_count, cudaStream_t s) {
+  if (p.ks) return launch_write_blocks(p, w, sm_count, s);
   const int tpw = 32 / (p.D / 8), blocks = (w.T + tpw - 1) / tpw;
-  const int htot = p.Hq + (p.ks ? 0 : 2 * p.Hkv), most = (htot + kWriteWarps - 1) / kWriteWarps;
+  const int htot = p.Hq + 2 * p.Hkv, most = (htot + kWriteWarps - 1) / kWriteWarps;
   // few tokens: split the heads over blocks too, until every SM has the eight
   // blocks that it holds
   int split = (8 * sm_count + blocks - 1) / blocks;
@@ -908,31 +998,16 @@ cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_co
   const dim3 grid((unsigned)blocks, (unsigned)split), block(kWriteWarps * 32);
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, s, p, w); };
   // a kernel by head size, pairing and positions
-  auto pick = [&](auto e4m3, auto kv) {
-    constexpr bool E = decltype(e4m3)::value, KV = decltype(kv)::value;
+  auto pick = [&](auto e4m3) {
+    constexpr bool E = decltype(e4m3)::value;
     if (p.D == 128) {
-      if (p.pt) return p.halves ? go(k_pages_write<128, E, true, true, KV>) : go(k_pages_write<128, E, false, true, KV>);
-      return p.halves ? go(k_pages_write<128, E, true, false, KV>) : go(k_pages_write<128, E, false, false, KV>);
+      if (p.pt) return p.halves ? go(k_pages_write<128, E, true, true>) : go(k_pages_write<128, E, false, true>);
+      return p.halves ? go(k_pages_write<128, E, true, false>) : go(k_pages_write<128, E, false, false>);
     }
-    if (p.pt) return p.halves ? go(k_pages_write<64, E, true, true, KV>) : go(k_pages_write<64, E, false, true, KV>);
-    return p.halves ? go(k_pages_write<64, E, true, false, KV>) : go(k_pages_write<64, E, false, false, KV>);
+    if (p.pt) return p.halves ? go(k_pages_write<64, E, true, true>) : go(k_pages_write<64, E, false, true>);
+    return p.halves ? go(k_pages_write<64, E, true, false>) : go(k_pages_write<64, E, false, false>);
   };
-  if (!p.ks) return p.e4m3 ? pick(std::true_type{}, std::true_type{}) : pick(std::false_type{}, std::true_type{});
-  // keys and values first; the queries' kernel starts beside that one
-  const int groups = (w.T + KVRING_SCALE_BLOCK - 1) / KVRING_SCALE_BLOCK, each = (p.Hkv + kBlockWarps - 1) / kBlockWarps;
-  int heads = (3 * sm_count + groups - 1) / groups;   // three blocks to an SM, as long as that leaves a head per warp
-  heads = heads < 1 ? 1 : (heads > each ? each : heads);
-  const dim3 bgrid((unsigned)groups, (unsigned)heads), bblock(kBlockWarps * 32);
-  auto put = [&](auto kernel) { return launch_pdl(kernel, bgrid, bblock, 0, s, p, w); };
-  cudaError_t e;
-  if (p.D == 128) {
-    if (p.pt) e = p.halves ? put(k_pages_write_blocks<128, true, true>) : put(k_pages_write_blocks<128, false, true>);
-    else e = p.halves ? put(k_pages_write_blocks<128, true, false>) : put(k_pages_write_blocks<128, false, false>);
-  } else {
-    if (p.pt) e = p.halves ? put(k_pages_write_blocks<64, true, true>) : put(k_pages_write_blocks<64, false, true>);
-    else e = p.halves ? put(k_pages_write_blocks<64, true, false>) : put(k_pages_write_blocks<64, false, false>);
-  }
-  return e == cudaSuccess ? pick(std::false_type{}, std::false_type{}) : e;
+  return p.e4m3 ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // namespace kvr

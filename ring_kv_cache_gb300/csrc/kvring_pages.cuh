@@ -105,6 +105,7 @@ struct PagesWrite {
   const int32_t* coords;  // [T][3], 3-D RoPE
   float eps;
   int T, layer;
+  int kv_blocks;          // blocks of keys and values per 16 tokens (block scales)
 };
 cudaError_t launch_pages_write(const PagesDev& p, const PagesWrite& w, int sm_count, cudaStream_t s);
 
