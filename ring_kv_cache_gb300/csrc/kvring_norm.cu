@@ -14,9 +14,9 @@
 // in the registers of the threads that share it, eight per 16-byte load, so a norm
 // costs one exchange (two for a layer norm).  The tables' rows come from L1, where
 // the rows of an SM find them (a session's tokens lie together).  Measured (GB300):
-// 16,384 rows of 5,120, bf16, post norm, gate, 16 rows of fp32 tables, 674 MB: 148 us,
-// 4.5 TB/s; the instructions of a row's start and sums and the trips to L1 for 61 KB
-// of tables per row take what is left.  757 rows of 5,120, fp32 stream: 8.8 us; nine
+// 16,384 rows of 5,120, bf16, post norm, gate, 16 rows of fp32 tables, 674 MB: 137 us,
+// 4.9 TB/s; the instructions of a row's start and sums and the trips to L1 for 61 KB
+// of tables per row take what is left.  757 rows of 5,120, fp32 stream: 9.0 us; nine
 // rows of 1,280: 2.0 us.  Measured and slower: persistent blocks with rows ahead in
 // shared memory (cp.async), the tables from L1 (283 us: shared memory takes L1's
 // room) or held in registers (208 us: eight columns a thread, 534 instructions a warp
@@ -140,10 +140,12 @@ __global__ void __launch_bounds__(NV < 4 ? 1024 : (NV == 4 ? 512 : 416), 1)
   griddep_launch_dependents();
   if (row >= a.n) return;   // (whole warps, and no block-wide sum where a block has several rows)
   const int r = a.index ? __ldcg(a.index + row) : (a.mods > 1 ? row : 0);
+  // A warp's groups lie side by side, so that their addresses differ by constants.
+  const int v0 = (tid >> 5) * (32 * NV) + lane;
   auto each = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (FULL || i * T + tid < a.vecs) f(i, i * T + tid);
+      if (FULL || v0 + 32 * i < a.vecs) f(i, v0 + 32 * i);
   };
   Raw8<F32> hr[NV];
   uint4 yr[NV];
@@ -262,12 +264,13 @@ cudaError_t go(const NormDev& d, bool f32, int T, cudaStream_t s) {
 
 cudaError_t launch_residual_norm(const NormDev& d, bool f32, cudaStream_t s) {
   // Groups of eight columns a thread.  Few rows: one, for latency (9 rows of 1,280:
-  // 2.0 us, with five 2.4).  Else four or five, for a row's fixed instructions are
-  // then shared by more columns (16,384 rows of 5,120, one: 287 us, two: 167,
-  // four: 148), or what leaves the fewest places empty.
+  // 2.0 us, with five 2.4).  Else many, for a row's fixed instructions are then
+  // shared by more columns (16,384 bf16 rows of 5,120, one: 287 us, two: 167, four:
+  // 146, five: 137; 757 fp32 rows, whose groups take more registers, two: 10.8, four:
+  // 9.0, five: 11.3), unless fewer leave fewer places empty.
   auto threads = [&](int nv) { return (d.vecs + 32 * nv - 1) / (32 * nv) * 32; };
-  int nv = 4;
-  for (int k : {5, 2})
+  int nv = f32 ? 4 : 5;
+  for (int k : {f32 ? 5 : 4, 2})
     if (threads(k) * k < threads(nv) * nv) nv = k;
   if (d.vecs <= 1024 && (long long)d.n * d.vecs <= 152 * 1024) nv = 1;
   const int T = threads(nv);
