@@ -230,13 +230,13 @@ kvring_status kvring_project_write(kvring_t* ring, const void* x, const void* w,
  * for none (1, 0, 0); weight, post_weight: bf16 [width] or NULL (ones).
  * mod_index: int32 [num_tokens] rows, or NULL: row 0 of one, or row t of
  * num_tokens; a token whose row is outside [0, mod_rows) gets NaN.
- * Rows lie stride elements apart (multiples of 8, at least width where there is
- * more than one row), so slices of packed tensors can be passed.
+ * Rows lie stride elements apart (multiples of 8, at most 2^28, at least width where
+ * there is more than one row), so slices of packed tensors can be passed.
  * y NULL: h is normed as it is (h_out, gate, post_weight NULL, post_norm none).
  * x_out NULL and norm KVRING_NORM_NONE: the sum alone.  h_out may be NULL when x_out
- * is not.  h_out may be h (with its stride); no other result may lie over an
- * argument or the other result.  Everything between reading and the one rounding
- * of each result is fp32, squares included; x_out comes from the unrounded sum.
+ * is not.  h_out may be h (with its stride); no other result's span, first row to
+ * last, may lie over that of an argument or the other result.  Everything between
+ * reading and the one rounding of each result is fp32, squares included; x_out comes from the unrounded sum.
  * Works on the current device, and keeps no state.
  * ------------------------------------------------------------------------ */
 #define KVRING_NORM_NONE 0
@@ -553,7 +553,10 @@ kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const voi
  *           from before; these are then rounded to the new scale,
  *           code = e4m3(code * (old / new))
  *   code  = e4m3(value / scale)
- * Values that are not finite have no part in `need`: infinities saturate, NaN stays. */
+ * Values that are not finite have no part in `need`: infinities saturate, NaN stays.
+ * A scale raised by a write whose plan is then dropped stays raised, and the
+ * tokens rounded to it.  A block that two rows of the tables share must not be
+ * appended to. */
 kvring_status kvring_pages_write_3d(kvring_pages_t* pages, int32_t layer, const void* q, const void* k, const void* v,
                                     int64_t q_stride, int64_t k_stride, int64_t v_stride, const void* q_weight,
                                     const void* k_weight, float eps, const int32_t* coords, void* q_out,

@@ -325,7 +325,7 @@ extern "C" kvring_status kvring_residual_norm(const kvring_norm_config* c, const
   for (const void* p : {h, y, gate, scale, shift, post_weight, weight, (const void*)h_out, (const void*)x_out})
     if (!aligned16(p)) return KVRING_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(mod_index) & 3) return KVRING_ERR_INVALID_ARG;
-  const int64_t n = c->num_tokens, w = c->width, most = (int64_t)1 << 32;
+  const int64_t n = c->num_tokens, w = c->width, most = (int64_t)1 << 28;
   auto stride_ok = [&](const void* p, int64_t s, int64_t rows) {
     return !p || (s % 8 == 0 && s <= most && (s >= w || (rows == 1 && s >= 0)));
   };

@@ -71,6 +71,10 @@ struct PagesDev {
 // nearest of these.  With both products' range in mind: a weight 2^(score + e - m)
 // that counts is never lost beside the normaliser's 2^(score - m).
 constexpr int kMinExp = 127 - 40, kMaxExp = 127 + 40;
+// The most a query row's factor may be over blocks, so that it times a key's scale
+// stays finite (and 0 times it 0).  Rows beyond are one-hot on their largest score
+// with this one too: scores that differ at all differ by more than 2^14 then.
+constexpr float kMostFactor = 0x1p87f;
 
 struct PagedAttn {
   const uint16_t* q;

@@ -841,6 +841,7 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
           // (at least 1e-30: a factor that underflows would make NaN of what is
           // masked, and such scores are all alike anyway)
           f_row = fmaxf(f_row * (BLK ? 1.0f : __ldcg(sc + u.h)) * up, 1e-30f);
+          if constexpr (BLK) f_row = fminf(f_row, kMostFactor);
 #pragma unroll
           for (int i = 0; i < D / 8 / L::kHalves; ++i) {
             uint4* at = chunk_at(half * (D / 8 / L::kHalves) + i);

@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
         // (at least 1e-30: a factor that underflows would make NaN of what is
         // masked, and such scores are all alike anyway)
         fac = fmaxf(fac * scale_k * up, 1e-30f);
+        if constexpr (BLK) fac = fminf(fac, kMostFactor);
         uint32_t hq[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)

@@ -132,6 +132,21 @@ def test_strides_in_place_and_what_lies_beside():
     assert bool((h[:, :8] == 9.0).all()) and bool((h[0] == 9.0).all())
 
 
+@pytest.mark.parametrize("width", [64, 1288, 5120])
+def test_fp32_rows_that_begin_in_the_middle_of_a_sector(width):
+    """16-byte aligned and no more: the rows' 32-byte accesses are two of 16."""
+    t = tensors(9, width, F32, rows=3, seed=10)
+    beside = lambda x: torch.zeros((x.shape[0], width + 8), dtype=F32, device="cuda")[:, 4:4 + width]  # noqa: E731
+    h, ho = beside(t["h"]), beside(t["h"])
+    h.copy_(t["h"])
+    mod = torch.zeros((3, 3 * width + 8), dtype=F32, device="cuda")[:, 4:4 + 3 * width].view(3, 3, width)
+    mod.copy_(t["mod"])
+    assert h.data_ptr() % 32 == 16 and mod.data_ptr() % 32 == 16
+    a = check(dict(t, h=h, mod=mod), idx=t["idx"], norm="layer", h_out=ho)
+    b = check(t, idx=t["idx"], norm="layer")
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("width", [64, 1280, 5120])
 def test_a_row_that_no_table_has_gets_nan(width):
     t = tensors(10, width, BF, rows=3, seed=7)

@@ -118,6 +118,31 @@ def test_scores_of_any_size(d, new):
     close(p.attention(0, q), want, tol)
 
 
+@pytest.mark.parametrize("d,new", [(64, 1), (128, 1), (64, 90), (128, 90)])
+def test_the_largest_queries_over_the_largest_scales(d, new):
+    """Factors beyond what fp32 holds: one-hot on the largest score, and keys of zeros score 0."""
+    p, s = cache_of(2, 1, d, 16, [200], [new], seed=21)
+    p.k_scales(0).view(torch.uint8).fill_(HIGH)
+    c = p.k_cache(0)
+    x = torch.zeros(c.shape, device="cuda")
+    page, off = int(p.tables[0, 77 // 16]), 77 % 16
+    x[page, 0, off, 3] = 2.0 ** -9
+    c.copy_(x.to(c.dtype))
+    q = torch.zeros_like(s["q"])
+    q[..., 3] = 1.5 * 2.0 ** 127
+    q[::2, :, 3] *= -1
+    out = p.attention(0, q, causal=False).double()
+    at = torch.arange(200, device="cuda")
+    ids = p.tables[0, at // 16].long()
+    v = p.v_cache(0).view(torch.uint8)[ids, 0, at % 16].view(torch.float8_e4m3fn).double()
+    v = v * torch.exp2(p.v_scales(0).view(torch.uint8)[ids, 0, 0].double() - 127)[:, None]
+    others = torch.cat([v[:77], v[78:]]).mean(0)
+    for t in range(new):   # (the fp32 sum of 199 values and f16 probabilities: 2^-10 of their sizes)
+        want = others if t % 2 == 0 else v[77]
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 * v.abs().mean(0) if t % 2 == 0 else 0)
+        close(out[t], want.expand(2, -1), tol.expand(2, -1))
+
+
 @pytest.mark.parametrize("rise", [0.03, 0.4, 3.0])
 @pytest.mark.parametrize("d,new", [(128, 1), (128, 70), (64, 3), (64, 200)])
 def test_scores_that_keep_rising(d, new, rise):
