@@ -386,66 +386,65 @@ def residual_norm(h, y=None, gate=None, residual_scale: float = 1.0, post_norm: 
     ``mod_rows[t]`` (int32), else row 0 of one or row t of n.  Norms are "rms",
     "layer" or None.  Returns (h_out, x): h_out is h itself without y, x is None
     without ``norm``; ``h_out=h`` updates the stream in place."""
-    for t, name in ((h, "h"), (y, "y"), (gate, "gate"), (scale, "scale"), (shift, "shift"), (mod_rows, "mod_rows"),
-                    (weight, "weight"), (post_weight, "post_weight"), (h_out, "h_out"), (x_out, "x_out")):
-        if not isinstance(t, torch.Tensor) and (t is not None or name == "h"):
-            raise ValueError(f"{name} must be a tensor")
-    if not h.is_cuda or h.dim() != 2:
-        raise ValueError("h must be a 2-D CUDA tensor")
-    dev, stream_type = h.get_device(), h.dtype
-    n, width = h.shape
-    if width < 8 or width & 7 or width > 16384:
-        raise ValueError("width must be a multiple of 8, at most 16384")
-    if norm not in NORMS or post_norm not in NORMS:
-        raise ValueError("norms are 'rms', 'layer' or None")
-    bf, f32 = torch.bfloat16, torch.float32
-    hs = _rows(h, n, width, "h", dev, f32, bf)
-    ys = os_ = xs = m = ms = 0
-    mod = index = None
-    if y is not None:
-        ys = _rows(y, n, width, "y", dev, bf)
-        if h_out is None:
-            h_out = _empty_on(stream, (n, width), stream_type, h.device)
-        os_ = _rows(h_out, n, width, "h_out", dev, stream_type)
-    elif gate is not None or post_norm or post_weight is not None or h_out is not None:
-        raise ValueError("gate, post_norm, post_weight and h_out need y")
-    elif norm is None:
-        raise ValueError("nothing to compute")
-    if norm is not None:
-        if x_out is None:
-            x_out = _empty_on(stream, (n, width), bf, h.device)
-        xs = _rows(x_out, n, width, "x_out", dev, bf)
-    elif weight is not None or scale is not None or shift is not None or x_out is not None:
-        raise ValueError("weight, scale, shift and x_out need a norm")
-    if post_weight is not None and not post_norm:
-        raise ValueError("post_weight needs a post_norm")
-    for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
-        if t is None:
-            continue
-        if mod is None:
-            m, mod = (t.shape[0] if t.dim() == 2 else 0), t.dtype
-            ms = _rows(t, m, width, name, dev, f32, bf)
-        elif _rows(t, m, width, name, dev, mod) != ms:
-            raise ValueError("gate, scale and shift must have one row stride")
-    if mod_rows is not None:
-        if mod is None:
-            raise ValueError("mod_rows needs gate, scale or shift")
-        if mod_rows.get_device() != dev or mod_rows.dtype != torch.int32 or mod_rows.shape != (n,) \
-                or not mod_rows.is_contiguous():
-            raise ValueError(f"mod_rows must be a contiguous int32 tensor [{n}] on cuda:{dev}")
-        index = mod_rows.data_ptr()
-    elif mod is not None and m != 1 and m != n:
-        raise ValueError(f"gate, scale and shift have {m} rows: mod_rows says which is whose")
-    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
-        if t is not None and (t.dtype != bf or t.get_device() != dev or t.shape != (width,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{width}] on cuda:{dev}")
-    cfg = KvringNormConfig(n, width, OUT_F32 if stream_type == f32 else OUT_BF16, OUT_BF16 if mod == bf else OUT_F32, m,
-                           NORMS[post_norm], NORMS[norm], 0, hs, ys, ms, os_, xs, eps, residual_scale)
-    s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-    args = (ctypes.byref(cfg), h.data_ptr(), None if y is None else y.data_ptr(), None if gate is None else gate.data_ptr(),
-            None if scale is None else scale.data_ptr(), None if shift is None else shift.data_ptr(), index,
-            None if post_weight is None else post_weight.data_ptr(), None if weight is None else weight.data_ptr(),
-            None if h_out is None else h_out.data_ptr(), None if x_out is None else x_out.data_ptr(), s)
+    try:
+        if not h.is_cuda or h.dim() != 2:
+            raise ValueError("h must be a 2-D CUDA tensor")
+        dev, stream_type = h.get_device(), h.dtype
+        n, width = h.shape
+        if width < 8 or width & 7 or width > 16384:
+            raise ValueError("width must be a multiple of 8, at most 16384")
+        if norm not in NORMS or post_norm not in NORMS:
+            raise ValueError("norms are 'rms', 'layer' or None")
+        bf, f32 = torch.bfloat16, torch.float32
+        hs = _rows(h, n, width, "h", dev, f32, bf)
+        ys = os_ = xs = m = ms = 0
+        mod = index = None
+        if y is not None:
+            ys = _rows(y, n, width, "y", dev, bf)
+            if h_out is None:
+                h_out = _empty_on(stream, (n, width), stream_type, h.device)
+            os_ = _rows(h_out, n, width, "h_out", dev, stream_type)
+        elif gate is not None or post_norm or post_weight is not None or h_out is not None:
+            raise ValueError("gate, post_norm, post_weight and h_out need y")
+        elif norm is None:
+            raise ValueError("nothing to compute")
+        if norm is not None:
+            if x_out is None:
+                x_out = _empty_on(stream, (n, width), bf, h.device)
+            xs = _rows(x_out, n, width, "x_out", dev, bf)
+        elif weight is not None or scale is not None or shift is not None or x_out is not None:
+            raise ValueError("weight, scale, shift and x_out need a norm")
+        if post_weight is not None and not post_norm:
+            raise ValueError("post_weight needs a post_norm")
+        for t, name in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+            if t is None:
+                continue
+            if mod is None:
+                m, mod = (t.shape[0] if t.dim() == 2 else 0), t.dtype
+                ms = _rows(t, m, width, name, dev, f32, bf)
+            elif _rows(t, m, width, name, dev, mod) != ms:
+                raise ValueError("gate, scale and shift must have one row stride")
+        if mod_rows is not None:
+            if mod is None:
+                raise ValueError("mod_rows needs gate, scale or shift")
+            if mod_rows.get_device() != dev or mod_rows.dtype != torch.int32 or mod_rows.shape != (n,) \
+                    or not mod_rows.is_contiguous():
+                raise ValueError(f"mod_rows must be a contiguous int32 tensor [{n}] on cuda:{dev}")
+            index = mod_rows.data_ptr()
+        elif mod is not None and m != 1 and m != n:
+            raise ValueError(f"gate, scale and shift have {m} rows: mod_rows says which is whose")
+        for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+            if t is not None and (t.dtype != bf or t.get_device() != dev or t.shape != (width,) or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous bfloat16 tensor [{width}] on cuda:{dev}")
+        cfg = KvringNormConfig(n, width, OUT_F32 if stream_type == f32 else OUT_BF16, OUT_BF16 if mod == bf else OUT_F32, m,
+                               NORMS[post_norm], NORMS[norm], 0, hs, ys, ms, os_, xs, eps, residual_scale)
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+        args = (ctypes.byref(cfg), h.data_ptr(), None if y is None else y.data_ptr(), None if gate is None else gate.data_ptr(),
+                None if scale is None else scale.data_ptr(), None if shift is None else shift.data_ptr(), index,
+                None if post_weight is None else post_weight.data_ptr(), None if weight is None else weight.data_ptr(),
+                None if h_out is None else h_out.data_ptr(), None if x_out is None else x_out.data_ptr(), s)
+    except AttributeError:
+        raise ValueError("h, y, the tables, weights, rows and results must be tensors") from None
     if torch.cuda.current_device() == dev:
         _check(lib().kvring_residual_norm(*args), "kvring_residual_norm")
     else:

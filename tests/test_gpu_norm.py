@@ -208,7 +208,7 @@ def test_refusals():
            dict(ok, shift=mod[:, 2].contiguous()), dict(ok, shift=mod[:2, 2]), dict(ok, norm="batch"), dict(ok, norm=None),
            dict(ok, post_weight=t["pw"]), dict(ok, weight=t["w"][:32]), dict(ok, weight=t["w"].float()), dict(mod_rows=t["idx"]),
            dict(ok, h_out=torch.empty_like(h).float()), dict(ok, x_out=torch.empty_like(h)[:5]), dict(ok, gate=mod[:1, 0].expand(3, 64)),
-           dict(ok, gate=mod[:, 0].cpu())]
+           dict(ok, gate=mod[:, 0].cpu()), dict(ok, gate=0.5), dict(ok, mod_rows=[0] * 6), dict(ok, weight=1.0), dict(ok, x_out=3)]
     for kw in bad:
         with pytest.raises(ValueError):
             kv.residual_norm(h, y, **kw)
@@ -218,6 +218,8 @@ def test_refusals():
     for a, b in ((h[:, :60], y[:, :60]), (h.half(), y), (h.cpu(), y.cpu()), (h, y[:5]), (h, y.float()), (h[:, ::2], y[:, :32])):
         with pytest.raises(ValueError):
             kv.residual_norm(a, b)
+    with pytest.raises(ValueError):
+        kv.residual_norm([1.0] * 8, y)
     for kw in (dict(x_out=y), dict(eps=-1.0), dict(residual_scale=math.inf), dict(x_out=h)):
         with pytest.raises(kv.KvRingError):
             kv.residual_norm(h, y, **kw)
