@@ -14,9 +14,9 @@
 // in the registers of the threads that share it, eight per 16-byte load, so a norm
 // costs one exchange (two for a layer norm).  The tables' rows come from L1, where
 // the rows of an SM find them (a session's tokens lie together).  Measured (GB300):
-// 16,384 rows of 5,120, bf16, post norm, gate, 16 rows of fp32 tables, 674 MB: 137 us,
-// 4.9 TB/s; the instructions of a row's start and sums and the trips to L1 for 61 KB
-// of tables per row take what is left.  757 rows of 5,120, fp32 stream: 9.0 us; nine
+// 16,384 rows of 5,120, bf16, post norm, gate, 16 rows of fp32 tables, 672 MB: 130 us,
+// 5.2 TB/s; the instructions of a row's start and sums and the trips to L1 for 61 KB
+// of tables per row take what is left.  757 rows of 5,120, fp32 stream: 8.8 us; nine
 // rows of 1,280: 2.0 us.  Measured and slower: persistent blocks with rows ahead in
 // shared memory (cp.async), the tables from L1 (283 us: shared memory takes L1's
 // room) or held in registers (208 us: eight columns a thread, 534 instructions a warp
@@ -158,12 +158,13 @@ __global__ void __launch_bounds__(NV < 4 ? 1024 : (NV == 4 ? 512 : 416), 1)
   const bool known = r >= 0 && r < a.mods;
   const long long mrow = known ? (long long)r * a.mod_stride : 0;
   const float nan = __int_as_float(0x7FFFFFFF);
-  // z = f(z, table), in two steps, so that every load is on its way before the first
-  // value is used and no store lies between (over which none would be moved)
-  auto ask = [&](auto& t, const void* base, long long at, bool wide) {
+  // z = f(z, table), every load on its way before the first value is used (no store
+  // lies between, over which none would be moved).  Only here, behind the sums: the
+  // tables are near, and the registers hold no more (five groups: 116 registers
+  // instead of 128 and spills, 130 us instead of 137).
+  auto with_table = [&](const void* base, auto m32, long long at, bool wide, auto f) {
+    Raw8<decltype(m32)::value> t[NV];
     each([&](int i, int v) { t[i].template load<true>(base, at + 8 * v, wide); });
-  };
-  auto with = [&](const auto& t, auto f) {
     each([&](int i, int) {
       Pairs g;
       t[i].widen(g);
@@ -171,6 +172,8 @@ __global__ void __launch_bounds__(NV < 4 ? 1024 : (NV == 4 ? 512 : 416), 1)
       for (int e = 0; e < 4; ++e) z[i][e] = f(z[i][e], g[e]);
     });
   };
+  using Mods = std::integral_constant<bool, M32>;
+  using Bf16 = std::false_type;
   auto times = [](float2 x, float2 y) { return __fmul2_rn(x, y); };
   // 1 / sqrt(mean square + eps), after the mean is taken away (layer); places
   // behind the row's end hold zeros
@@ -201,16 +204,17 @@ __global__ void __launch_bounds__(NV < 4 ? 1024 : (NV == 4 ? 512 : 416), 1)
       for (int e = 0; e < 4; ++e) z[i][e] = make_float2(0.f, 0.f);
   }
   if (a.y) {
-    Raw8<false> pw[NV];
-    Raw8<M32> gr[NV];
-    if (a.post_w) ask(pw, a.post_w, 0, false);
-    if (a.gate) ask(gr, a.gate, mrow, a.m_wide);
     each([&](int i, int) { widen8(yr[i], z[i]); });
     float f = a.post != KVRING_NORM_NONE ? standard(a.post) : 1.0f;
-    if (a.post_w) with(pw, times);
-    if (a.gate) with(gr, times);
+    if (a.post_w) with_table(a.post_w, Bf16{}, 0, false, times);
+    if (a.gate) with_table(a.gate, Mods{}, mrow, a.m_wide, times);
     f = known ? f * a.alpha : nan;
-    with(hr, [f](float2 x, float2 h) { return __ffma2_rn(x, make_float2(f, f), h); });
+    each([&](int i, int) {
+      Pairs h;
+      hr[i].widen(h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[i][e] = __ffma2_rn(z[i][e], make_float2(f, f), h[e]);
+    });
     if (a.h_out) {
       each([&](int i, int v) {
         if constexpr (F32) {
@@ -232,21 +236,15 @@ __global__ void __launch_bounds__(NV < 4 ? 1024 : (NV == 4 ? 512 : 416), 1)
     each([&](int i, int) { hr[i].widen(z[i]); });
   }
   if (a.norm == KVRING_NORM_NONE) return;
-  Raw8<false> w[NV];
-  Raw8<M32> sr[NV], br[NV];
-  if (a.w) ask(w, a.w, 0, false);
-  if (a.scale) ask(sr, a.scale, mrow, a.m_wide);
-  if (NV < 4 && a.shift) ask(br, a.shift, mrow, a.m_wide);
   float f = standard(a.norm);
   if (!known) f = nan;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) z[i][e] = __fmul2_rn(z[i][e], make_float2(f, f));
-  if (a.w) with(w, times);
-  if (a.scale) with(sr, [](float2 x, float2 y) { return __ffma2_rn(x, y, x); });
-  if (NV >= 4 && a.shift) ask(br, a.shift, mrow, a.m_wide);   // (the registers do not hold more)
-  if (a.shift) with(br, [](float2 x, float2 y) { return __fadd2_rn(x, y); });
+  if (a.w) with_table(a.w, Bf16{}, 0, false, times);
+  if (a.scale) with_table(a.scale, Mods{}, mrow, a.m_wide, [](float2 x, float2 y) { return __ffma2_rn(x, y, x); });
+  if (a.shift) with_table(a.shift, Mods{}, mrow, a.m_wide, [](float2 x, float2 y) { return __fadd2_rn(x, y); });
   uint4* o = reinterpret_cast<uint4*>(a.x_out + row * a.x_stride);
   each([&](int i, int v) { o[v] = narrow8(z[i]); });
 }
@@ -265,9 +263,9 @@ cudaError_t go(const NormDev& d, bool f32, int T, cudaStream_t s) {
 cudaError_t launch_residual_norm(const NormDev& d, bool f32, cudaStream_t s) {
   // Groups of eight columns a thread.  Few rows: one, for latency (9 rows of 1,280:
   // 2.0 us, with five 2.4).  Else many, for a row's fixed instructions are then
-  // shared by more columns (16,384 bf16 rows of 5,120, one: 287 us, two: 167, four:
-  // 146, five: 137; 757 fp32 rows, whose groups take more registers, two: 10.8, four:
-  // 9.0, five: 11.3), unless fewer leave fewer places empty.
+  // shared by more columns (16,384 bf16 rows of 5,120, one: 287 us, two: 153, four:
+  // 154, five: 130; 757 fp32 rows, whose groups take more registers, two: 8.8, four:
+  // 8.8, five: 11.3), unless fewer leave fewer places empty.
   auto threads = [&](int nv) { return (d.vecs + 32 * nv - 1) / (32 * nv) * 32; };
   int nv = f32 ? 4 : 5;
   for (int k : {f32 ? 5 : 4, 2})
