@@ -439,7 +439,8 @@ def residual_norm(h, y=None, gate=None, residual_scale: float = 1.0, post_norm: 
         cfg = KvringNormConfig(n, width, OUT_F32 if stream_type == f32 else OUT_BF16, OUT_BF16 if mod == bf else OUT_F32, m,
                                NORMS[post_norm], NORMS[norm], 0, hs, ys, ms, os_, xs, eps, residual_scale)
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
-        args = (ctypes.byref(cfg), h.data_ptr(), None if y is None else y.data_ptr(), None if gate is None else gate.data_ptr(),
+        args = (ctypes.byref(cfg), h.data_ptr(), None if y is None else y.data_ptr(),
+                None if gate is None else gate.data_ptr(),
                 None if scale is None else scale.data_ptr(), None if shift is None else shift.data_ptr(), index,
                 None if post_weight is None else post_weight.data_ptr(), None if weight is None else weight.data_ptr(),
                 None if h_out is None else h_out.data_ptr(), None if x_out is None else x_out.data_ptr(), s)
@@ -682,6 +683,13 @@ class KvPages:
     """A paged cache of every layer of a model for many requests, on one CUDA
     device (the current one unless ``device`` names another).
 
+    ``block_scales``: an E4M3 cache whose keys and values have a scale for every 16
+    tokens and head (``k_scales``, ``v_scales``), which ``write`` sets, instead of
+    one per head (``set_scales``).  ``rope3d`` = (pairs that turn by t, by y; the rest
+    by x): tokens have positions (t, y, x), below ``max_position``, given to
+    ``write``; ``rope_frequencies`` "section" makes each section a RoPE of its own,
+    "head" gives pair i the frequency that it has in 1-D.
+
     A step: ``plan`` the new tokens of its requests, then for every layer
     ``write`` and ``attention``, then ``commit``; ``release`` ends requests.
     All of it runs on the device and can be captured in a CUDA graph.  Calls
@@ -712,8 +720,13 @@ class KvPages:
             raise ValueError("rope_frequencies must be 'section' or 'head'")
         if rope3d is None and (rope_frequencies != "section" or max_position is not None):
             raise ValueError("rope_frequencies and max_position need rope3d")
-        if rope3d is not None and (len(rope3d) != 2 or int(rope3d[0]) < 1 or (max_position is not None and max_position < 1)):
-            raise ValueError("rope3d must be (pairs of t, pairs of y), max_position positive")
+        if rope3d is not None:
+            try:
+                rope3d = tuple(int(x) for x in rope3d)
+            except TypeError:
+                rope3d = ()
+            if len(rope3d) != 2 or rope3d[0] < 1 or (max_position is not None and max_position < 1):
+                raise ValueError("rope3d must be (pairs of t, pairs of y), max_position positive")
         self.device = d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
         self.Hq, self.Hkv, self.d, self.P = int(q_heads), int(kv_heads), int(head_dim), int(page_size)
         self.L, self.num_pages, self.R = int(layers), int(num_pages), int(max_requests)
@@ -782,7 +795,8 @@ class KvPages:
                 raise ValueError(f"layer must be in [0, {self.L})")
             shape = (self.num_pages, self.Hkv, self.P // SCALE_BLOCK)
             n = shape[0] * shape[1] * shape[2]
-            self._caches[off, layer] = self.buf[off + layer * n:off + (layer + 1) * n].view(torch.float8_e8m0fnu).view(shape)
+            part = self.buf[off + layer * n:off + (layer + 1) * n]
+            self._caches[off, layer] = part.view(torch.float8_e8m0fnu).view(shape)
         return self._caches[off, layer]
 
     def k_scales(self, layer: int = 0) -> torch.Tensor:
@@ -894,7 +908,8 @@ class KvPages:
         q_out = self._result(q_out, n, "q_out", stream)
         args = (_i32(layer), q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(q_norm), _ptr(k_norm), float(eps))
         if self.three_d:
-            self._call(_LIB.kvring_pages_write_3d, "kvring_pages_write_3d", stream, *args, pos.data_ptr(), q_out.data_ptr(), n)
+            self._call(_LIB.kvring_pages_write_3d, "kvring_pages_write_3d", stream, *args, pos.data_ptr(), q_out.data_ptr(),
+                       n)
         else:
             self._call(_LIB.kvring_pages_write, "kvring_pages_write", stream, *args, q_out.data_ptr(), n)
         return q_out

@@ -264,8 +264,8 @@ cudaError_t launch_residual_norm(const NormDev& d, bool f32, cudaStream_t s) {
   // Groups of eight columns a thread.  Few rows: one, for latency (9 rows of 1,280:
   // 2.0 us, with five 2.4).  Else many, for a row's fixed instructions are then
   // shared by more columns (16,384 bf16 rows of 5,120, one: 287 us, two: 153, four:
-  // 154, five: 130; 757 fp32 rows, whose groups take more registers, two: 8.8, four:
-  // 8.8, five: 11.3), unless fewer leave fewer places empty.
+  // 154, five: 130; 757 fp32 rows, whose groups take more registers, two and
+  // four: 8.8, five: 9.4), unless fewer leave fewer places empty.
   auto threads = [&](int nv) { return (d.vecs + 32 * nv - 1) / (32 * nv) * 32; };
   int nv = f32 ? 4 : 5;
   for (int k : {f32 ? 5 : 4, 2})

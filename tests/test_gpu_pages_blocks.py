@@ -253,7 +253,7 @@ def test_a_captured_write_follows_the_plan():
 def test_refusals():
     mk = lambda **kw: kv.KvPages(2, 2, 64, 16, 8, 2, 64, 32, **kw)  # noqa: E731
     for kw in (dict(block_scales=True, cache_dtype=BF), dict(rope3d=(0, 4)), dict(rope3d=(33, 0)), dict(rope3d=(8, 25)), dict(rope3d=(8, -1)),
-               dict(rope3d=(8,)), dict(rope3d=(8, 8), rope_frequencies="all"), dict(rope_frequencies="head"), dict(max_position=10),
+               dict(rope3d=(8,)), dict(rope3d=8), dict(rope3d=(8, None)), dict(rope3d=(8, 8), rope_frequencies="all"), dict(rope_frequencies="head"), dict(max_position=10),
                dict(rope3d=(8, 8), max_position=0), dict(rope3d=(8, 8), max_position=(1 << 24) + 1)):
         with pytest.raises(ValueError):
             mk(**kw)
