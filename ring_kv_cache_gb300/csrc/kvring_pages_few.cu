@@ -310,6 +310,11 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
     const uint32_t box_bytes = (uint32_t)(box_rows * (E4M3 ? D : 128));
     const long long layer0 = (long long)a.layer * p.num_pages;
     const int none = p.L * p.num_pages * p.Hkv;   // past the map: reads as zeros
+    [[maybe_unused]] const uint8_t *layer_ks = p.ks, *layer_vs = p.vs;
+    if constexpr (BLK) {
+      layer_ks += layer0 * p.Hkv << p.logP >> 4;
+      layer_vs += layer0 * p.Hkv << p.logP >> 4;
+    }
     int n = 0;                               // slots filled so far
     bool stopped = a.debug_stall;            // a wait gave up (or test support: nothing is copied)
     while (x < stop && !stopped) {
@@ -338,17 +343,18 @@ __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
       struct Exps {
         int k, v;
       };
-      const int tile_end = rq.t0 + (int)(ue - ubase);
-      auto block_tok = [&](int t) { return (t + (lane >> 3)) * kTile + (lane & 7) * KVRING_SCALE_BLOCK; };
+      // (within a layer places of blocks fit 31 bits)
+      const int end_tok = min(rq.hi, (rq.t0 + (int)(ue - ubase)) * kTile);
+      const int lane_tok = (lane >> 3) * kTile + (lane & 7) * KVRING_SCALE_BLOCK;
       auto block_page = [&](int t) -> int {
-        const int tok = block_tok(t);
-        if (t + (lane >> 3) >= tile_end || tok >= rq.hi || tok + KVRING_SCALE_BLOCK <= rq.lo) return -2;
-        return __ldcg(tab + (tok >> p.logP));
+        const int tok = t * kTile + lane_tok;
+        return tok < end_tok && tok + KVRING_SCALE_BLOCK > rq.lo ? __ldcg(tab + (tok >> p.logP)) : -2;
       };
       auto block_exps = [&](int t, int id) -> Exps {
-        if (id < 0 || id >= p.num_pages) return Exps{127, 127};
-        const size_t at = ((size_t)(layer0 + id) * p.Hkv + h << p.logP >> 4) + ((block_tok(t) & (p.P - 1)) >> 4);
-        return Exps{__ldcg(p.ks + at), __ldcg(p.vs + at)};
+        if ((unsigned)id >= (unsigned)p.num_pages) return Exps{127, 127};
+        const unsigned at =
+            ((unsigned)(id * p.Hkv + h) << (p.logP - 4)) + (unsigned)((t * kTile + lane_tok) & (p.P - 1)) / KVRING_SCALE_BLOCK;
+        return Exps{__ldcg(layer_ks + at), __ldcg(layer_vs + at)};
       };
       int next_page = -2, batch = 0;
       Exps exps{}, next_exps{};
