@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8) k_pages_write(const Pages
 // scales, 3.3 us.  (A warp for a whole run, 64 values a thread and 168 registers:
 // 80, 16.2 and 7.2 us; queries by warps of that shape as well 111, 19.0 and 7.6 us.)
 constexpr int kBlockWarps = kWriteWarps;
-constexpr int kBlocksPerSm = 7;   // (16,384 tokens: 82, 75.7, 70.7, 69.9 us with 5, 6, 7, 8; nine tokens best with fewer)
+constexpr int kBlocksPerSm = 7;   // (16,384 tokens: 82, 75.7, 70.7, 69.9 us with 5, 6, 7, 8)
 constexpr int kBlockHeads = 2;    // of a block of keys and values (77 us, 78 with four, 82 with one, all at six blocks)
 
 __device__ __forceinline__ int block_exponent(float amax) {

@@ -180,8 +180,8 @@ __device__ __forceinline__ Req make_req(const PagedAttn& a, const ReqWords& w, i
 // w = s + e_v, the running maximum is that of w, p = 2^(w - m') weighs the codes, and
 // the normaliser takes p 2^-e_v = 2^(s - m').  So what the f16 probabilities
 // resolve is what a token adds to the result, whatever its block's scale, and one
-// multiplication per row and group is all it costs.  The producer reads the exponents a
-// tile ahead and puts them beside the tile's slot.
+// multiplication per row and group is all it costs.  The producer reads the exponents of
+// four tiles at a time, four tiles ahead, into a ring of their own (kExpTiles).
 template <int D, bool E4M3, bool BLK>
 __global__ void __launch_bounds__(FewLayout<D, E4M3, BLK>::kThreads, 1)
     k_paged_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagesDev p,
