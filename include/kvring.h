@@ -573,7 +573,9 @@ kvring_status kvring_pages_write_3d(kvring_pages_t* pages, int32_t layer, const 
  * past the plan's tokens stay as they were.  Scores, softmax statistics and sums are fp32; probabilities
  * are rounded once, to bf16 (f16 over an E4M3 cache; over block scales what is
  * rounded is the probability with its value's scale).  Block scales' bytes outside 87 .. 167
- * (2^-40 .. 2^40) are read as the nearest of these.  Finite cached values
+ * (2^-40 .. 2^40) are read as the nearest of these, and a row of queries whose factor, 2^e scale
+ * log2(e) with 2^e the power of two at or below its largest size, is beyond 2^69 as one of 2^69
+ * (its scores keep their order).  Finite cached values
  * of any size give finite results at any length.  Cached tokens that
  * a query's mask hides do not affect it, whatever they hold. */
 kvring_status kvring_pages_attention(kvring_pages_t* pages, int32_t layer, const void* q, int64_t q_stride, void* out,

@@ -71,10 +71,13 @@ struct PagesDev {
 // nearest of these.  With both products' range in mind: a weight 2^(score + e - m)
 // that counts is never lost beside the normaliser's 2^(score - m).
 constexpr int kMinExp = 127 - 40, kMaxExp = 127 + 40;
-// The most a query row's factor may be over blocks, so that it times a key's scale
-// stays finite (and 0 times it 0).  Rows beyond are one-hot on their largest score
-// with this one too: scores that differ at all differ by more than 2^14 then.
-constexpr float kMostFactor = 0x1p87f;
+// The most a query row's factor may be over blocks.  A raw score is below 4 x 448 x 128 <
+// 2^18 (f16 queries, codes), so with a key's scale of 2^40 it stays below 2^127: scores, and
+// the differences of two, are finite.  (With 2^87 the factor alone was: raw scores from 2 on over
+// the largest scale made inf, and inf - inf NaN.)  Rows beyond are read with this factor: their
+// scores keep their order, and two that fp32 tells apart beside a raw score of 1 differ by
+// 2^69 2^-40 2^-24 = 2^5 at least, over the smallest scale, so such a row is one-hot all the same.
+constexpr float kMostFactor = 0x1p69f;
 
 struct PagedAttn {
   const uint16_t* q;
