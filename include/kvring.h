@@ -543,7 +543,9 @@ kvring_status kvring_pages_write(kvring_pages_t* pages, int32_t layer, const voi
  * go and what attention lets them see stays with their places in the request.  A
  * token with a coordinate outside [0, max_position) sets
  * KVRING_PAGES_ERR_POSITION; its row of q_out and its place in the cache stay as
- * they were.  kvring_pages_write refuses such a cache, and this call a 1-D one.
+ * they were (with block scales its codes do, and the block's scale where the step has
+ * no other token in it; once committed, the place counts as one that holds a token).
+ * kvring_pages_write refuses such a cache, and this call a 1-D one.
  *
  * In a cache with block scales (either call) 16 tokens at places 16 b .. 16 b + 15
  * of a request share a scale per head, of keys and of values:

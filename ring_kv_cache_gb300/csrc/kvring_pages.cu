@@ -846,7 +846,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kBlocksPerSm) k_pages_write_
     const int need = block_exponent(m), exp = held > 0 ? max(need, old) : need;
     const float inv = power(127 - exp);              // 2^-(exp - 127)
     const bool first = (here >> r & 1u) && r == from;
-    if (warp == 0 && first) *scale = (uint8_t)exp;
+    // (a run of skipped tokens alone leaves its block's scale, as its codes)
+    if (warp == 0 && first && (live >> from & ((1u << (to - from)) - 1))) *scale = (uint8_t)exp;
     uint8_t *kc = p.k + layer0 * D, *vc = p.v + layer0 * D;
     auto store = [&](uint8_t* dst, const float (&y)[8], float s) {
       const uint32_t a = f32x2_to_e4m3x2(y[0] * s, y[1] * s) | ((uint32_t)f32x2_to_e4m3x2(y[2] * s, y[3] * s) << 16);

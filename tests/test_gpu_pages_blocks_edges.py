@@ -1,10 +1,12 @@
 """Block scales on the GPU at the ends of their range: the largest queries over
-the largest keys."""
+the largest keys, and steps whose tokens were all skipped."""
 import pytest
 import torch
 
+import ring_kv_cache_gb300 as kv
 from _blockscheck import B, HIGH, LOW, cache_of
 from _pagescheck import close, errors
+from test_gpu_pages_blocks import inputs, places, run
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -73,3 +75,25 @@ def test_large_queries_keep_blocks_in_order(d, new):
     out = p.attention(0, q, causal=False).double()
     want = values(p, 0, total)[48 + 7]
     close(out, want.expand_as(out), (2.0 ** -8 + 2.0 ** -10) * want.abs().expand_as(out))
+
+
+SKIPS = [([17], [1], [0]), ([32], [16], list(range(16))), ([48], [48], list(range(16, 32))),
+         ([40, 16, 5], [8, 16, 5], list(range(16)) + [24, 25]), ([33, 34, 35], [1, 2, 3], [0, 1, 2, 3, 4, 5]), ([21], [2], [0, 1])]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("total,new,bad", SKIPS, ids=[str(i) for i in range(len(SKIPS))])
+def test_blocks_whose_tokens_were_all_skipped_stay_as_they_were(total, new, bad, d):
+    """Codes and scales both, in a layer that is written again under the same plan too."""
+    n = sum(new)
+    p, s = cache_of(4, 2, d, 16, total, new, seed=34, rope3d=(8, 12), max_position=100)
+    q, k, v, wq, wk = inputs(p, n, 35)
+    xyz = places(n, 36, 100)
+    good = xyz.clone()
+    xyz[bad, 1] = 100
+    run(p, s, q, k, v, wq, wk, "adjacent", (8, 12), "section", xyz, skip=bad)
+    assert errors(p) == kv.PAGES_ERR_POSITION
+    p.state[kv.PAGES_STATE["error"]] = 0
+    run(p, s, q, k, v, wq, wk, "adjacent", (8, 12), "section", good)
+    assert errors(p) == 0
+    run(p, s, q, k, v, wq, wk, "adjacent", (8, 12), "section", xyz, skip=bad)
