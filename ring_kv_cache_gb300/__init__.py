@@ -393,6 +393,8 @@ def residual_norm(h, y=None, gate=None, residual_scale: float = 1.0, post_norm: 
         n, width = h.shape
         if width < 8 or width & 7 or width > 16384:
             raise ValueError("width must be a multiple of 8, at most 16384")
+        if n >> 31:   # (ctypes would wrap it)
+            raise ValueError("h must have fewer than 2^31 rows")
         if norm not in NORMS or post_norm not in NORMS:
             raise ValueError("norms are 'rms', 'layer' or None")
         bf, f32 = torch.bfloat16, torch.float32
@@ -422,6 +424,8 @@ def residual_norm(h, y=None, gate=None, residual_scale: float = 1.0, post_norm: 
             if mod is None:
                 m, mod = (t.shape[0] if t.dim() == 2 else 0), t.dtype
                 ms = _rows(t, m, width, name, dev, f32, bf)
+                if m >> 31:
+                    raise ValueError("gate, scale and shift must have fewer than 2^31 rows")
             elif _rows(t, m, width, name, dev, mod) != ms:
                 raise ValueError("gate, scale and shift must have one row stride")
         if mod_rows is not None:
