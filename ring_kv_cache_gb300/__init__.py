@@ -849,8 +849,8 @@ class KvPages:
         if rows is not None:
             self._int_arg(rows, "rows", (n,))
         num_tokens = _i32(num_tokens)
-        self._call(_LIB.kvring_pages_plan, "kvring_pages_plan", stream, _ptr(rows), new_tokens.data_ptr(), n, num_tokens,
-                   num_tokens if max_new is None else _i32(max_new))
+        self._call(_LIB.kvring_pages_plan, "kvring_pages_plan", stream, _ptr(rows), new_tokens.data_ptr(), _i32(n),
+                   num_tokens, num_tokens if max_new is None else _i32(max_new))
         step = self._steps.get((n, num_tokens))
         if step is None:
             if len(self._steps) >= 256:
@@ -866,7 +866,7 @@ class KvPages:
     def release(self, rows, stream=None) -> None:
         """End the requests in ``rows`` (int32): their pages become free."""
         n = self._int_arg(rows, "rows").numel()
-        self._call(_LIB.kvring_pages_release, "kvring_pages_release", stream, rows.data_ptr(), n)
+        self._call(_LIB.kvring_pages_release, "kvring_pages_release", stream, rows.data_ptr(), _i32(n))
 
     def _heads(self, x, heads: int, name: str):
         """Check bf16 [n, heads, d] with whole rows of heads (a slice of a
