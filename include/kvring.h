@@ -403,6 +403,13 @@ typedef struct {
   int32_t rope_pairing;  /* KVRING_ROPE_* */
   int32_t reserved;      /* 0 */
   double rope_base;
+} kvring_pages_config;
+
+/* What a cache may have besides; a structure of its own, so that programs
+ * that know nothing of it hold kvring_pages_config and kvring_pages_layout at
+ * the sizes that they always had.  All zeros, but for `size`: nothing. */
+typedef struct {
+  int32_t size;          /* sizeof(kvring_pages_options) */
   int32_t scale_block;   /* E4M3: 0 = a scale per layer and head (kvring_pages_set_scales), or
                             KVRING_SCALE_BLOCK = a scale for every 16 tokens of a page and head, set by
                             kvring_pages_write */
@@ -414,8 +421,8 @@ typedef struct {
   int32_t rope_frequencies; /* KVRING_FREQ_* of 3-D RoPE (0 with 1-D) */
   int32_t max_position;  /* 3-D: coordinates lie in [0, max_position), at most 2^24; 0 = W * page_size
                             (0 with 1-D) */
-  int32_t reserved2;     /* 0 */
-} kvring_pages_config;
+  int32_t reserved;      /* 0 */
+} kvring_pages_options;
 
 #define KVRING_SCALE_BLOCK 16
 #define KVRING_FREQ_SECTION 0    /* each section a RoPE of its own: its j-th of m pairs turns by
@@ -438,9 +445,6 @@ typedef struct {
   size_t step_lengths; /* int32 [max_requests]: their lengths with the new tokens */
   size_t positions;    /* int32 [max_tokens]: position of each new token in its request */
   size_t slots;        /* int32 [max_tokens]: page * page_size + offset, -1 for padding */
-  size_t k_block_scales; /* uint8 [L][num_pages][Hkv][page_size / 16]: a block's scale is 2^(byte - 127),
-                            E8M0 (127 at create); with scale_block only */
-  size_t v_block_scales; /* the same */
   size_t total;        /* bytes of the whole buffer */
 } kvring_pages_layout;
 
@@ -465,6 +469,12 @@ typedef struct {
  * then zeroed).  layout.total is what kvring_pages_create needs. */
 kvring_status kvring_pages_get_layout(const kvring_pages_config* cfg, kvring_pages_layout* out);
 
+/* The same of a cache with options (NULL: none).  k_block_scales, v_block_scales (each may be
+ * NULL): where the exponents of block scales lie, uint8 [L][num_pages][Hkv][page_size / 16], a
+ * block's scale being 2^(byte - 127), E8M0 (127 at create); of no bytes without scale_block. */
+kvring_status kvring_pages_get_layout_with(const kvring_pages_config* cfg, const kvring_pages_options* options,
+                                           kvring_pages_layout* out, size_t* k_block_scales, size_t* v_block_scales);
+
 /* Create a paged cache inside `dev_buf` (device memory of at least
  * layout.total bytes, 256-byte aligned, the caller's until after
  * kvring_pages_destroy).  Every row is empty, every page free (the stack
@@ -472,6 +482,9 @@ kvring_status kvring_pages_get_layout(const kvring_pages_config* cfg, kvring_pag
  * keys and values are not cleared.  Waits for its own set-up on `stream`. */
 kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf, size_t bytes, void* stream,
                                   kvring_pages_t** out);
+/* The same with options (NULL: none). */
+kvring_status kvring_pages_create_with(const kvring_pages_config* cfg, const kvring_pages_options* options,
+                                       void* dev_buf, size_t bytes, void* stream, kvring_pages_t** out);
 kvring_status kvring_pages_destroy(kvring_pages_t* pages);
 
 /* Take over a state: lengths int32 [max_requests], tables int32

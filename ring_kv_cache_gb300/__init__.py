@@ -80,6 +80,7 @@ class KvringNormConfig(ctypes.Structure):
 
 
 class KvringPagesConfig(ctypes.Structure):
+    """The C config, and behind it the options that C takes in a structure of their own."""
     _fields_ = [(f, ctypes.c_int32) for f in (
         "num_q_heads", "num_kv_heads", "head_dim", "num_layers", "page_size", "num_pages", "max_requests",
         "max_pages_per_request", "max_tokens", "cache_dtype", "rope_pairing", "reserved")] + [
@@ -87,10 +88,20 @@ class KvringPagesConfig(ctypes.Structure):
             "scale_block", "rope_pairs_t", "rope_pairs_y", "rope_frequencies", "max_position", "reserved2")]
 
 
+class KvringPagesOptions(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in (
+        "size", "scale_block", "rope_pairs_t", "rope_pairs_y", "rope_frequencies", "max_position", "reserved")]
+
+
 class KvringPagesLayout(ctypes.Structure):
+    """The C layout, and within it where block scales lie, which C tells beside it."""
     _fields_ = [(f, ctypes.c_size_t) for f in (
         "k_cache", "v_cache", "scales", "lengths", "tables", "free_pages", "state", "step_rows", "step_cu",
         "step_lengths", "positions", "slots", "k_block_scales", "v_block_scales", "total")]
+
+
+class _PagesLayout(ctypes.Structure):   # as in C
+    _fields_ = [f for f in KvringPagesLayout._fields_ if "block" not in f[0]]
 
 
 class KvRingError(RuntimeError):
@@ -132,8 +143,12 @@ def lib():
         "kvring_project_write": (i32, [vp, vp, vp, i32, vp, i32, vp, vp, i32, vp]),
         "kvring_residual_norm": (i32, [ctypes.POINTER(KvringNormConfig)] + [vp] * 11),
         "kvring_export": (i32, [vp, vp, vp, vp, vp, vp, vp]),
-        "kvring_pages_get_layout": (i32, [ctypes.POINTER(KvringPagesConfig), ctypes.POINTER(KvringPagesLayout)]),
+        "kvring_pages_get_layout": (i32, [ctypes.POINTER(KvringPagesConfig), ctypes.POINTER(_PagesLayout)]),
+        "kvring_pages_get_layout_with": (i32, [ctypes.POINTER(KvringPagesConfig), ctypes.POINTER(KvringPagesOptions),
+                                               ctypes.POINTER(_PagesLayout), ctypes.POINTER(sz), ctypes.POINTER(sz)]),
         "kvring_pages_create": (i32, [ctypes.POINTER(KvringPagesConfig), vp, sz, vp, ctypes.POINTER(vp)]),
+        "kvring_pages_create_with": (i32, [ctypes.POINTER(KvringPagesConfig), ctypes.POINTER(KvringPagesOptions), vp, sz, vp,
+                                           ctypes.POINTER(vp)]),
         "kvring_pages_destroy": (i32, [vp]),
         "kvring_pages_restore": (i32, [vp, vp, vp, vp, i32, vp]),
         "kvring_pages_set_scales": (i32, [vp, i32, vp, vp, vp]),
@@ -660,16 +675,24 @@ def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _pages_options(cfg: KvringPagesConfig) -> KvringPagesOptions:
+    return KvringPagesOptions(ctypes.sizeof(KvringPagesOptions), cfg.scale_block, cfg.rope_pairs_t, cfg.rope_pairs_y,
+                              cfg.rope_frequencies, cfg.max_position, cfg.reserved2)
+
+
 def kvring_pages_get_layout(cfg: KvringPagesConfig) -> KvringPagesLayout:
-    lay = KvringPagesLayout()
-    _check(lib().kvring_pages_get_layout(ctypes.byref(cfg), ctypes.byref(lay)), "kvring_pages_get_layout")
-    return lay
+    lay, k, v = _PagesLayout(), ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().kvring_pages_get_layout_with(ctypes.byref(cfg), ctypes.byref(_pages_options(cfg)), ctypes.byref(lay),
+                                              ctypes.byref(k), ctypes.byref(v)), "kvring_pages_get_layout")
+    return KvringPagesLayout(k_block_scales=k.value, v_block_scales=v.value,
+                             **{f: getattr(lay, f) for f, _ in lay._fields_})
 
 
 def kvring_pages_create(cfg: KvringPagesConfig, buf: torch.Tensor, stream=None) -> int:
     h = ctypes.c_void_p()
-    _check(lib().kvring_pages_create(ctypes.byref(cfg), buf.data_ptr(), buf.numel() * buf.element_size(),
-                                     _stream_ptr(stream, buf.device), ctypes.byref(h)), "kvring_pages_create")
+    _check(lib().kvring_pages_create_with(ctypes.byref(cfg), ctypes.byref(_pages_options(cfg)), buf.data_ptr(),
+                                          buf.numel() * buf.element_size(), _stream_ptr(stream, buf.device),
+                                          ctypes.byref(h)), "kvring_pages_create")
     return h.value
 
 

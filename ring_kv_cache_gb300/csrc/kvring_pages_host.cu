@@ -3,7 +3,6 @@
 // (kvring_pages_create alone waits, for its own set-up) and none allocates
 // device memory.
 #include <cmath>
-#include <cstring>
 #include <new>
 
 #include "kvring_pages.cuh"
@@ -28,8 +27,10 @@ constexpr unsigned long long kDefaultWaitNs = 1000000000ull;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-bool config_ok(const kvring_pages_config* c) {
-  if (!c) return false;
+constexpr kvring_pages_options kNoOptions = {(int32_t)sizeof(kvring_pages_options), 0, 0, 0, 0, 0, 0};
+
+bool config_ok(const kvring_pages_config* c, const kvring_pages_options* o) {
+  if (!c || o->size != (int32_t)sizeof *o) return false;   // (another size: another header's options)
   if (c->num_kv_heads < 1 || c->num_q_heads < 1 || c->num_q_heads > 4096) return false;
   if (c->num_q_heads % c->num_kv_heads != 0 || c->num_q_heads / c->num_kv_heads > 64) return false;
   if (c->head_dim != 64 && c->head_dim != 128) return false;
@@ -43,17 +44,17 @@ bool config_ok(const kvring_pages_config* c) {
   if (c->max_tokens < 1 || c->max_tokens > (1 << 20)) return false;
   if (c->cache_dtype != KVRING_CACHE_E4M3 && c->cache_dtype != KVRING_CACHE_BF16) return false;
   if (c->rope_pairing != KVRING_ROPE_ADJACENT && c->rope_pairing != KVRING_ROPE_HALVES) return false;
-  if (c->reserved != 0 || c->reserved2 != 0) return false;
-  if (c->scale_block != 0 && (c->scale_block != KVRING_SCALE_BLOCK || c->cache_dtype != KVRING_CACHE_E4M3)) return false;
-  if (c->rope_pairs_t == 0) {
-    if (c->rope_pairs_y != 0 || c->rope_frequencies != 0 || c->max_position != 0) return false;
+  if (c->reserved != 0 || o->reserved != 0) return false;
+  if (o->scale_block != 0 && (o->scale_block != KVRING_SCALE_BLOCK || c->cache_dtype != KVRING_CACHE_E4M3)) return false;
+  if (o->rope_pairs_t == 0) {
+    if (o->rope_pairs_y != 0 || o->rope_frequencies != 0 || o->max_position != 0) return false;
   } else {
     const int pairs = c->head_dim / 2;
-    if (c->rope_pairs_t < 1 || c->rope_pairs_t > pairs || c->rope_pairs_y < 0 ||
-        c->rope_pairs_y > pairs - c->rope_pairs_t)
+    if (o->rope_pairs_t < 1 || o->rope_pairs_t > pairs || o->rope_pairs_y < 0 ||
+        o->rope_pairs_y > pairs - o->rope_pairs_t)
       return false;
-    if (c->rope_frequencies != KVRING_FREQ_SECTION && c->rope_frequencies != KVRING_FREQ_HEAD) return false;
-    if (c->max_position < 0 || c->max_position > 1 << 24) return false;
+    if (o->rope_frequencies != KVRING_FREQ_SECTION && o->rope_frequencies != KVRING_FREQ_HEAD) return false;
+    if (o->max_position < 0 || o->max_position > 1 << 24) return false;
   }
   return c->rope_base > 0.0 && std::isfinite(c->rope_base);
 }
@@ -62,15 +63,15 @@ struct Plan {
   kvring_pages_layout pub;
   size_t table, part_o, part_ml, tickets, few_o, few_ml;
   size_t cache_bytes;   // of K, and of V
-  size_t scale_bytes;   // block scales of K, and of V
+  size_t k_scales, v_scales, scale_bytes;   // block scales of K, and of V
 };
 
 // Rows of the cos/sin table.
-int table_rows(const kvring_pages_config* c) {
-  return c->rope_pairs_t && c->max_position ? c->max_position : c->max_pages_per_request * c->page_size;
+int table_rows(const kvring_pages_config* c, const kvring_pages_options* o) {
+  return o->rope_pairs_t && o->max_position ? o->max_position : c->max_pages_per_request * c->page_size;
 }
 
-Plan plan_for(const kvring_pages_config* c) {
+Plan plan_for(const kvring_pages_config* c, const kvring_pages_options* o) {
   Plan p{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -93,10 +94,10 @@ Plan plan_for(const kvring_pages_config* c) {
   p.pub.step_lengths = take(R * 4);
   p.pub.positions = take(T * 4);
   p.pub.slots = take(T * 4);
-  p.scale_bytes = c->scale_block ? p.cache_bytes / D / KVRING_SCALE_BLOCK : 0;
-  p.pub.k_block_scales = take(p.scale_bytes);
-  p.pub.v_block_scales = take(p.scale_bytes);
-  p.table = take((size_t)table_rows(c) * D * 4);
+  p.scale_bytes = o->scale_block ? p.cache_bytes / D / KVRING_SCALE_BLOCK : 0;
+  p.k_scales = take(p.scale_bytes);
+  p.v_scales = take(p.scale_bytes);
+  p.table = take((size_t)table_rows(c, o) * D * 4);
   p.part_o = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * D * 4);
   p.part_ml = take((size_t)2 * kvr::kPagedMaxCtas * kvr::kPartRows * 8);
   p.tickets = take((size_t)3 * kvr::kPagedMaxCtas * 4);   // two per CTA, and one of the other kernel
@@ -166,19 +167,33 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
 extern "C" {
 
 kvring_status kvring_pages_get_layout(const kvring_pages_config* cfg, kvring_pages_layout* out) {
+  return kvring_pages_get_layout_with(cfg, nullptr, out, nullptr, nullptr);
+}
+
+kvring_status kvring_pages_get_layout_with(const kvring_pages_config* cfg, const kvring_pages_options* options,
+                                           kvring_pages_layout* out, size_t* k_block_scales, size_t* v_block_scales) {
   if (!out) return KVRING_ERR_INVALID_ARG;
-  std::memset(out, 0, sizeof *out);
-  if (!config_ok(cfg)) return KVRING_ERR_INVALID_ARG;
-  *out = plan_for(cfg).pub;
-  return KVRING_OK;
+  const kvring_pages_options* o = options ? options : &kNoOptions;
+  const bool ok = config_ok(cfg, o);
+  const Plan p = ok ? plan_for(cfg, o) : Plan{};
+  *out = p.pub;
+  if (k_block_scales) *k_block_scales = p.k_scales;
+  if (v_block_scales) *v_block_scales = p.v_scales;
+  return ok ? KVRING_OK : KVRING_ERR_INVALID_ARG;
 }
 
 kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf, size_t bytes, void* stream,
                                   kvring_pages_t** out) {
+  return kvring_pages_create_with(cfg, nullptr, dev_buf, bytes, stream, out);
+}
+
+kvring_status kvring_pages_create_with(const kvring_pages_config* cfg, const kvring_pages_options* options,
+                                       void* dev_buf, size_t bytes, void* stream, kvring_pages_t** out) {
   if (!out) return KVRING_ERR_INVALID_ARG;
   *out = nullptr;
-  if (!config_ok(cfg) || !dev_buf || !aligned(dev_buf, kAlign)) return KVRING_ERR_INVALID_ARG;
-  const Plan p = plan_for(cfg);
+  const kvring_pages_options* o = options ? options : &kNoOptions;
+  if (!config_ok(cfg, o) || !dev_buf || !aligned(dev_buf, kAlign)) return KVRING_ERR_INVALID_ARG;
+  const Plan p = plan_for(cfg, o);
   if (bytes < p.pub.total) return KVRING_ERR_CAPACITY;
   int dev = 0, major = 0, minor = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KVRING_ERR_CUDA;
@@ -235,13 +250,13 @@ kvring_status kvring_pages_create(const kvring_pages_config* cfg, void* dev_buf,
   d.max_tokens = cfg->max_tokens;
   d.e4m3 = cfg->cache_dtype == KVRING_CACHE_E4M3;
   d.halves = cfg->rope_pairing == KVRING_ROPE_HALVES;
-  d.ks = cfg->scale_block ? b + p.pub.k_block_scales : nullptr;
-  d.vs = cfg->scale_block ? b + p.pub.v_block_scales : nullptr;
-  d.pt = cfg->rope_pairs_t;
-  d.py = cfg->rope_pairs_y;
-  d.max_pos = table_rows(cfg);
+  d.ks = o->scale_block ? b + p.k_scales : nullptr;
+  d.vs = o->scale_block ? b + p.v_scales : nullptr;
+  d.pt = o->rope_pairs_t;
+  d.py = o->rope_pairs_y;
+  d.max_pos = table_rows(cfg, o);
   double theta[64] = {};
-  const bool sections = d.pt && cfg->rope_frequencies == KVRING_FREQ_SECTION;
+  const bool sections = d.pt && o->rope_frequencies == KVRING_FREQ_SECTION;
   const int ends[4] = {0, d.pt, d.pt + d.py, d.D / 2};
   for (int i = 0; i < d.D / 2; ++i) {
     const int ax = i < ends[1] ? 0 : (i < ends[2] ? 1 : 2);
