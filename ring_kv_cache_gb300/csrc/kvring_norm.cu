@@ -63,8 +63,10 @@ __device__ __forceinline__ uint4 narrow8(const Pairs& x) {
 }
 // Eight columns of a row of either type, as they lie in memory.  fp32: one
 // 32-byte access, so that a warp's lies in whole lines; two of 16 where the
-// row is not aligned for it.  CACHED: tables, which other rows of the SM read too;
-// else past L1.
+// row is not aligned for it.  CACHED: tables, which other rows of the SM read too,
+// through L1; else past it.  (Tables may be what the kernel before wrote, and L1 may hold
+// lines of them from before that: all reads lie behind griddepcontrol.wait, which makes the
+// memory operations of the kernels before visible, L1's lines included.)
 template <bool F32>
 struct Raw8;
 template <>
@@ -83,7 +85,8 @@ struct Raw8<true> {
                      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
                      : "l"(p));
     } else {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+      const float4* p4 = reinterpret_cast<const float4*>(p);
+      const float4 a = CACHED ? p4[0] : __ldcg(p4), b = CACHED ? p4[1] : __ldcg(p4 + 1);
       x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
       x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
