@@ -15,8 +15,8 @@
 // costs one exchange (two for a layer norm).  The tables' rows come from L1, where
 // the rows of an SM find them (a session's tokens lie together).  Measured (GB300):
 // 16,384 rows of 5,120, bf16, post norm, gate, 16 rows of fp32 tables, 672 MB: 130 us,
-// 5.2 TB/s; the instructions of a row's start and sums and the trips to L1 for 61 KB
-// of tables per row take what is left.  757 rows of 5,120, fp32 stream: 8.8 us; nine
+// 5.2 TB/s; the instructions of a row's start and sums and the trips to L1 for 71 KB
+// of tables and weight per row take what is left.  757 rows of 5,120, fp32 stream: 8.8 us; nine
 // rows of 1,280: 2.0 us.  Measured and slower: persistent blocks with rows ahead in
 // shared memory (cp.async), the tables from L1 (283 us: shared memory takes L1's
 // room) or held in registers (208 us: eight columns a thread, 534 instructions a warp
@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(NV < 4 ? 1024 : (NV == 4 ? 512 : 416), 1)
   const float nan = __int_as_float(0x7FFFFFFF);
   // z = f(z, table), every load on its way before the first value is used (no store
   // lies between, over which none would be moved).  Only here, behind the sums: the
-  // tables are near, and the registers hold no more (five groups: 116 registers
-  // instead of 128 and spills, 130 us instead of 137).
+  // tables are near, and the registers hold no more (five groups of a bf16 stream: 116
+  // registers instead of 128 and spills, 130 us instead of 137; of an fp32 one, with
+  // fp32 tables and places left empty, 128 and 8 bytes of spills).
   auto with_table = [&](const void* base, auto m32, long long at, bool wide, auto f) {
     Raw8<decltype(m32)::value> t[NV];
     each([&](int i, int v) { t[i].template load<true>(base, at + 8 * v, wide); });
@@ -263,6 +264,11 @@ cudaError_t go(const NormDev& d, bool f32, int T, cudaStream_t s) {
                     : launch_pdl(k_residual_norm<NV, FULL, false, false>, grid, block, 0, s, d, T);
 }
 
+// Few rows: as many groups of eight columns as 1,024 threads on each of this card's 152 SMs take at
+// one a thread.  (bf16 rows of 5,120: 150 rows 3.3 us, 243, the last below the border, 5.3 us, 244,
+// with five, 3.7 us: above one wave of the former the border could lie lower.)
+constexpr long long kFewGroups = 152 * 1024;
+
 cudaError_t launch_residual_norm(const NormDev& d, bool f32, cudaStream_t s) {
   // Groups of eight columns a thread.  Few rows: one, for latency (9 rows of 1,280:
   // 2.0 us, with five 2.4).  Else many, for a row's fixed instructions are then
@@ -273,7 +279,7 @@ cudaError_t launch_residual_norm(const NormDev& d, bool f32, cudaStream_t s) {
   int nv = f32 ? 4 : 5;
   for (int k : {f32 ? 5 : 4, 2})
     if (threads(k) * k < threads(nv) * nv) nv = k;
-  if (d.vecs <= 1024 && (long long)d.n * d.vecs <= 152 * 1024) nv = 1;
+  if (d.vecs <= 1024 && (long long)d.n * d.vecs <= kFewGroups) nv = 1;
   const int T = threads(nv);
   const bool full = d.vecs == T * nv;
   switch (nv) {

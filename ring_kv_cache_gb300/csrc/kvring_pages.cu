@@ -601,9 +601,10 @@ __global__ void __launch_bounds__(kWriteWarps * 32, 8) k_pages_write(const Pages
 // cos/sin rows of the group's tokens lie in shared memory for the block's heads.  Blocks that
 // take the queries (the write's code above) lie between those of keys and values.
 // Measured (GB300): 16,384 tokens, 32/8 heads x 128, 377 MB: 70.7 us, 5.3 TB/s; 757 tokens of
-// 40 heads 12.8 us, 48 single tokens of 10 heads, half of whose blocks move to larger
-// scales, 3.3 us.  (A warp for a whole run, 64 values a thread and 168 registers:
-// 80, 16.2 and 7.2 us; queries by warps of that shape as well 111, 19.0 and 7.6 us.)
+// 40 heads 12.8 us (1.26 waves), 48 single tokens of 10 heads 3.3 us, with half of their blocks
+// moved to larger scales by each call 7 us.  (A warp for a whole run, 64 values a thread and 168
+// registers: 80, 16.2 and, no block moved, 7.2 us; queries by warps of that shape as well 111, 19.0
+// and 7.6 us.)
 constexpr int kBlockWarps = kWriteWarps;
 constexpr int kBlocksPerSm = 7;   // (16,384 tokens: 82, 75.7, 70.7, 69.9 us with 5, 6, 7, 8)
 constexpr int kBlockHeads = 2;    // of a block of keys and values (77 us, 78 with four, 82 with one, all at six blocks)

@@ -866,7 +866,8 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
         const int all_hi = a.causal ? u.pos0 + g * TG + 1 : u.klen;
         const int all_lo = a.window > 0 ? u.pos0 + ntok_g - a.window : 0;
         const int ntile = u.ntile;
-        // (a row that is none keeps a factor of 0 and never asks for anything)
+        // (a row that is none keeps a factor of 0 and asks for nothing; over blocks its maximum
+        // is that of the values' exponents, which asks once where one is beyond kRaise)
         float m_run = live ? -INFINITY : 0.f, ell = 0.f;
         if (!live) f_row = 0.f;
         // (nothing seen yet: 2^-inf = 0)
@@ -953,9 +954,9 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
         int j = 0;
         auto tile = [&](auto slow_tag) {
           constexpr bool slow = decltype(slow_tag)::value;
-          float fr[kBlk], ev[kBlk];   // factors and exponents of the tile's blocks (BLK)
+          [[maybe_unused]] float fr[kBlk], ev[kBlk];   // factors and exponents of the tile's blocks (BLK)
           const int n = u.n0 + j;
-          const float* exps = reinterpret_cast<const float*>(sm + L::kExp) + 24 * (n % kExpTiles) + half * kBlk;
+          [[maybe_unused]] const float* exps = reinterpret_cast<const float*>(sm + L::kExp) + 24 * (n % kExpTiles) + half * kBlk;
           if constexpr (BLK) {        // (there long before the scores are)
             wait(misc->exps[n % kExpTiles], (n / kExpTiles) & 1);
 #pragma unroll
@@ -1003,15 +1004,15 @@ __global__ void __launch_bounds__(ChunkLayout<D, E4M3, BLK>::kThreads, 1)
               for (int i = 0; i < k; ++i) w[i] = fmaxf(w[i], w[i + k]);
             tmax = w[0];
           } else {
-          float mx[8];
+            float mx[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
+            for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1]));
 #pragma unroll
-          for (int i = 1; i < L::kCols / 16; ++i)
+            for (int i = 1; i < L::kCols / 16; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mx[k] = fmax3(mx[k], __uint_as_float(sr[16 * i + 2 * k]), __uint_as_float(sr[16 * i + 2 * k + 1]));
-          tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
+              for (int k = 0; k < 8; ++k)
+                mx[k] = fmax3(mx[k], __uint_as_float(sr[16 * i + 2 * k]), __uint_as_float(sr[16 * i + 2 * k + 1]));
+            tmax = f_row * fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
           }
           const bool need = tmax > m_run + kRaise || (m_run == -INFINITY && tmax > m_run);
           const float m_new = need ? tmax : m_run;
